@@ -21,6 +21,9 @@ __all__ = [
     "sample_generators", "compress", "forward_compress", "wgrad", "wgrad_noalloc", "decompress",
     "NOALLOC_SCRATCH_BYTES", "forward_compress_workspace_size",
     "compress_workspace_size", "wgrad_workspace_size", "compressed_nbytes",
+    # the operators around the projection (block_ops.py)
+    "attention", "attention_backward", "attention_workspace_size", "attention_backward_workspace_size",
+    "add_rms_norm", "add_rms_norm_fp8", "add_rms_norm_backward", "clip_grad_norm", "MAX_HEAD_DIM",
 ]
 
 F32 = 0
@@ -380,3 +383,14 @@ def decompress(C, f, alpha, *, out=None, stream=None):
                                         _stream_ptr(stream))
     _check(st, "pamm_decompress")
     return out
+
+
+def __getattr__(name):
+    # block_ops is built on the helpers above and on torch, which the package
+    # itself does not load; it is imported on first use
+    if name in __all__:
+        from . import block_ops
+        value = getattr(block_ops, name)
+        globals()[name] = value
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

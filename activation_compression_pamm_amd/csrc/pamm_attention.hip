@@ -1,0 +1,387 @@
+// pamm_attention.hip -- attention forward on gfx950.
+//
+//   s_ij = scale <q_i, k_j>,  lse_i = log sum_j exp(s_ij),
+//   o_i = sum_j exp(s_ij - lse_i) v_j
+//
+// in one pass over the keys with a running maximum m and sum l: a block of
+// keys whose scores exceed m rescales what was summed by exp(m_old - m_new).
+// All exponentials are powers of two (scores carry log2 e).
+//
+// Scores are formed transposed, S^T = K Q^T: a lane then owns one query, its
+// statistics are two registers, the maximum needs one exchange between the
+// wave's halves, and the probabilities leave the softmax in the register
+// order that O^T = V^T P^T takes them in (pamm_attention_device.hpp).
+//
+// Queries of the heads that share a key/value head are rows of one problem:
+// row r is position r / G of head r % G.
+#include "pamm_attention_device.hpp"
+
+namespace pamm {
+
+// Running statistics of one row, and its update by 32 keys.
+//
+// The reference m follows the maximum only when it is exceeded by more than
+// 2^kSlack: until then probabilities up to 2^kSlack are summed against the old
+// reference, which fp32 sums and bf16 products hold with the same relative
+// precision, and the ND x 16 multiplications of a rescale are skipped.
+constexpr float kSlack = 8.0f;
+
+struct Running {
+    float m, l;  // m in log2 units; l: this lane's keys only
+};
+
+// s (raw products; masked ones already -inf) becomes the probabilities.
+template <int ND>
+__device__ __forceinline__ void softmax_update(f32x16& s, float c, Running& st, f32x16* acc) {
+    float top = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+    top = half_max(top) * c;
+    if (__any(top > st.m + kSlack)) {
+        const float m = fmaxf(st.m, top);
+        const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
+        st.l *= f;
+#pragma unroll
+        for (int db = 0; db < ND; ++db)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[db][i] *= f;
+        st.m = m;
+    }
+    const float ref = st.m == -INFINITY ? 0.0f : st.m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -ref));
+        sum += s[i];
+    }
+    st.l += sum;
+}
+
+__device__ __forceinline__ void mask_block(f32x16& s, int64_t key0, int64_t lo, int64_t hi) {
+    const int first = 4 * (lane_id() >> 5);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t key = key0 + first + 8 * (i >> 2) + (i & 3);
+        if (key < lo || key >= hi) s[i] = -INFINITY;
+    }
+}
+
+// Scores' factor in log2 units; its sign is folded into the query operand.
+__device__ __forceinline__ float score_factor(float scale) { return fmaxf(fabsf(scale) * kLog2e, 1e-36f); }
+
+// ---------------------------------------------------------------- many rows
+
+// Four waves of 32 rows share tiles of 64 keys (32 in fp32), which two LDS
+// buffers hold: while one is used, the next tile travels through registers
+// into the other.
+template <int DT, int ND>
+__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_kernel(AttnArgs a, int64_t row_tiles) {
+    using T = Tile<DT, ND>;
+    constexpr int BK = DT == DT_BF16 ? 64 : 32;
+    __shared__ __attribute__((aligned(16))) char lds[2][2][BK * T::PITCH];
+    const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
+
+    int64_t id = xcd_order(blockIdx.x, gridDim.x);
+    const int split = (int)(id % a.nsplit);
+    id /= a.nsplit;
+    // the last rows see the most keys: they start first
+    const int64_t tile = row_tiles - 1 - id % row_tiles;
+    const int bh = (int)(id / row_tiles), b = bh / a.Hkv, hk = bh % a.Hkv;
+    const int64_t Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
+    const int64_t rows = (int64_t)a.Sq * a.G;
+
+    // what this lane's row, this wave's rows and this workgroup's rows see
+    const int64_t r0 = tile * 128, w0 = r0 + wave * 32, row = w0 + (l & 31);
+    const int64_t pos = row / a.G;
+    const int head = hk * a.G + (int)(row % a.G);
+    const bool live = row < rows;
+    const KeyRange mine = key_range(a, live ? pos : Lq, Lq, Lk);
+    const int64_t wlast = (w0 + 31 < rows ? w0 + 31 : rows - 1) / a.G, wfirst = w0 / a.G;
+    const int64_t blast = (r0 + 127 < rows ? r0 + 127 : rows - 1) / a.G, bfirst = r0 / a.G;
+    const int64_t wend = wfirst < Lq ? key_range(a, wlast < Lq ? wlast : Lq - 1, Lq, Lk).hi : 0;
+    const int64_t wbegin = key_range(a, wfirst, Lq, Lk).lo;
+    // keys in [wall_lo, wall_hi) are seen by every row of the wave
+    const KeyRange last_range = key_range(a, wlast, Lq, Lk);
+    const int64_t wall_lo = last_range.lo;
+    const int64_t wall_hi = (w0 + 31 < rows && wlast < Lq) ? key_range(a, wfirst, Lq, Lk).hi : 0;
+    const int64_t bend = bfirst < Lq ? key_range(a, blast < Lq ? blast : Lq - 1, Lq, Lk).hi : 0;
+    const int64_t bbegin = key_range(a, bfirst, Lq, Lk).lo;
+
+    int64_t t0 = bbegin / BK, t1 = (bend + BK - 1) / BK;
+    if (t1 < t0) t1 = t0;
+    if (a.nsplit > 1) {
+        const int64_t per = (t1 - t0 + a.nsplit - 1) / a.nsplit;
+        const int64_t s0 = t0 + split * per;
+        t1 = s0 + per < t1 ? s0 + per : t1;
+        t0 = s0 < t1 ? s0 : t1;
+    }
+
+    const char* kbase = a.k.p + b * a.k.sb + hk * a.k.sh;
+    const char* vbase = a.v.p + b * a.v.sb + hk * a.v.sh;
+    uint4 qf[T::NS];
+    load_row_operand<DT, ND>(qf, a.q.p + b * a.q.sb + pos * a.q.ss + head * a.q.sh, live && pos < Lq, a.D);
+    if (a.scale < 0.0f)
+#pragma unroll
+        for (int s = 0; s < T::NS; ++s) qf[s] = negate16<DT>(qf[s]);
+    const float c = score_factor(a.scale);
+
+    f32x16 acc[ND];
+#pragma unroll
+    for (int db = 0; db < ND; ++db) acc[db] = f32x16{};
+    Running st{-INFINITY, 0.0f};
+
+    TileCopy<DT, ND, BK, 256> kc, vc;
+    if (t0 < t1) {
+        kc.fetch(kbase + t0 * BK * a.k.ss, a.k.ss, Lk - t0 * BK, a.D, tid);
+        vc.fetch(vbase + t0 * BK * a.v.ss, a.v.ss, Lk - t0 * BK, a.D, tid);
+        kc.put(lds[0][0], tid);
+        vc.put(lds[0][1], tid);
+    }
+    __syncthreads();
+    int cur = 0;
+    for (int64_t t = t0; t < t1; ++t, cur ^= 1) {
+        const bool more = t + 1 < t1;
+        if (more) {
+            kc.fetch(kbase + (t + 1) * BK * a.k.ss, a.k.ss, Lk - (t + 1) * BK, a.D, tid);
+            vc.fetch(vbase + (t + 1) * BK * a.v.ss, a.v.ss, Lk - (t + 1) * BK, a.D, tid);
+        }
+#pragma unroll
+        for (int kb = 0; kb < BK / 32; ++kb) {
+            const int64_t key0 = t * BK + kb * 32;
+            if (key0 >= wend || key0 + 32 <= wbegin) continue;
+            f32x16 s{};
+#pragma unroll
+            for (int i = 0; i < T::NS; ++i)
+                s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], kb * 32, i), qf[i], s);
+            if (key0 < wall_lo || key0 + 32 > wall_hi) mask_block(s, key0, mine.lo, mine.hi);
+            softmax_update<ND>(s, c, st, acc);
+            Packed<DT> p;
+            p.set(s);
+            trans_product<DT, ND>(lds[cur][1], kb * 32, p, acc);
+        }
+        if (more) {
+            kc.put(lds[cur ^ 1][0], tid);
+            vc.put(lds[cur ^ 1][1], tid);
+        }
+        __syncthreads();
+    }
+
+    if (!live) return;
+    const float sum = half_sum(st.l);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float lse2 = sum == 0.0f ? -INFINITY : st.m + __builtin_amdgcn_logf(sum);
+    const int64_t at = ((int64_t)b * a.H + head) * a.Sq + pos;
+    if (a.nsplit > 1) {
+        store_rows<DT_F32, ND>(reinterpret_cast<char*>(a.part_o + (at * a.nsplit + split) * a.D), acc, inv, a.D);
+        if (l < 32) a.part_lse[at * a.nsplit + split] = lse2;
+    } else {
+        store_rows<DT, ND>(a.o.p + b * a.o.sb + pos * a.o.ss + head * a.o.sh, acc, inv, a.D);
+        if (l < 32) a.lse[at] = lse2 * kLn2;
+    }
+}
+
+// ----------------------------------------------------------------- few rows
+
+// At most 32 rows (single tokens): every wave takes the same rows and 32-key
+// blocks of its own, wave w the blocks w, w + 4, ... of this part, so nothing
+// waits for another wave until the end.  A lane reads its K operand straight
+// from memory (16 bytes of one key a step, the wave 32 keys), V goes through
+// the wave's own LDS tile; the next block's loads are issued as soon as the
+// registers of the current one are used.
+template <int DT, int ND>
+__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_few_kernel(AttnArgs a) {
+    using T = Tile<DT, ND>;
+    constexpr int OP = ND * 32 + 4;  // floats between rows of the merged result
+    constexpr int VT = 32 * T::PITCH;
+    constexpr int SH = 4 * VT > 32 * OP * 4 ? 4 * VT : 32 * OP * 4;
+    __shared__ __attribute__((aligned(16))) char lds[SH];
+    __shared__ float stat[4][2][32];
+    const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
+
+    int64_t id = xcd_order(blockIdx.x, gridDim.x);
+    const int split = (int)(id % a.nsplit);
+    id /= a.nsplit;
+    const int b = (int)(id / a.Hkv), hk = (int)(id % a.Hkv);
+    const int64_t Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
+    const int rows = a.Sq * a.G;
+    const int row = l & 31, pos = row / a.G, head = hk * a.G + row % a.G;
+    const bool live = row < rows;
+    const KeyRange mine = key_range(a, live ? pos : Lq, Lq, Lk);
+    const int64_t end = Lq > 0 ? key_range(a, Lq - 1, Lq, Lk).hi : 0;
+    const int64_t begin = key_range(a, 0, Lq, Lk).lo;
+    const int64_t n0 = begin / 32;
+    int64_t n1 = (end + 31) / 32;
+    if (n1 < n0) n1 = n0;
+    const int64_t per = (n1 - n0 + a.nsplit - 1) / a.nsplit;
+    const int64_t p0 = n0 + split * per, p1 = p0 + per < n1 ? p0 + per : n1;
+
+    const char* kbase = a.k.p + b * a.k.sb + hk * a.k.sh;
+    const char* vbase = a.v.p + b * a.v.sb + hk * a.v.sh;
+    uint4 qf[T::NS], kf[T::NS];
+    load_row_operand<DT, ND>(qf, a.q.p + b * a.q.sb + pos * a.q.ss + head * a.q.sh, live && pos < Lq, a.D);
+    if (a.scale < 0.0f)
+#pragma unroll
+        for (int s = 0; s < T::NS; ++s) qf[s] = negate16<DT>(qf[s]);
+    const float c = score_factor(a.scale);
+    f32x16 acc[ND];
+#pragma unroll
+    for (int db = 0; db < ND; ++db) acc[db] = f32x16{};
+    Running st{-INFINITY, 0.0f};
+    char* vt = lds + wave * VT;
+    TileCopy<DT, ND, 32, 64> vc;
+
+    int64_t t = p0 + wave;
+    if (t < p1) {
+        load_row_operand<DT, ND>(kf, kbase + (t * 32 + row) * a.k.ss, t * 32 + row < Lk, a.D);
+        vc.fetch(vbase + t * 32 * a.v.ss, a.v.ss, Lk - t * 32, a.D, l);
+    }
+    for (; t < p1; t += 4) {
+        const int64_t key0 = t * 32, next = key0 + 128;
+        f32x16 s{};
+#pragma unroll
+        for (int i = 0; i < T::NS; ++i) s = mma_step<DT>(kf[i], qf[i], s);
+        __builtin_amdgcn_wave_barrier();
+        vc.put(vt, l);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (t + 4 < p1) {
+            load_row_operand<DT, ND>(kf, kbase + (next + row) * a.k.ss, next + row < Lk, a.D);
+            vc.fetch(vbase + next * a.v.ss, a.v.ss, Lk - next, a.D, l);
+        }
+        mask_block(s, key0, mine.lo, mine.hi);
+        softmax_update<ND>(s, c, st, acc);
+        Packed<DT> p;
+        p.set(s);
+        trans_product<DT, ND>(vt, 0, p, acc);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+
+    // join the four waves: the common reference first, then the sums in order
+    const float sum = half_sum(st.l);
+    if (l < 32) {
+        stat[wave][0][l] = sum == 0.0f ? -INFINITY : st.m;
+        stat[wave][1][l] = sum;
+    }
+    __syncthreads();
+    float m = -INFINITY, total = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, stat[w][0][row]);
+    const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) total += stat[w][1][row] * __builtin_amdgcn_exp2f(stat[w][0][row] - ref);
+    const float f = sum == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(st.m - ref) / total;
+    float* merged = reinterpret_cast<float*>(lds);
+    for (int w = 0; w < 4; ++w) {
+        if (w == wave && live) {
+#pragma unroll
+            for (int db = 0; db < ND; ++db)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float* to = merged + row * OP + 32 * db + 8 * (i >> 2) + 4 * (l >> 5) + (i & 3);
+                    const float x = acc[db][i] * f;
+                    *to = w == 0 ? x : *to + x;
+                }
+        }
+        __syncthreads();
+    }
+    const float lse2 = total == 0.0f ? -INFINITY : m + __builtin_amdgcn_logf(total);
+    const int64_t at = ((int64_t)b * a.H + head) * a.Sq + pos;
+    if (tid < 32 && live) {
+        if (a.nsplit > 1)
+            a.part_lse[at * a.nsplit + split] = lse2;
+        else
+            a.lse[at] = lse2 * kLn2;
+    }
+    for (int e = tid; e < rows * a.D; e += 256) {
+        const int r = e / a.D, x = e % a.D, p = r / a.G, h = hk * a.G + r % a.G;
+        const float v = merged[r * OP + x];
+        if (a.nsplit > 1) {
+            a.part_o[((((int64_t)b * a.H + h) * a.Sq + p) * a.nsplit + split) * a.D + x] = v;
+        } else {
+            char* o = a.o.p + b * a.o.sb + p * a.o.ss + h * a.o.sh;
+            if constexpr (DT == DT_BF16)
+                reinterpret_cast<__bf16*>(o)[x] = (__bf16)v;
+            else
+                reinterpret_cast<float*>(o)[x] = v;
+        }
+    }
+}
+
+// Joins the parts of one row: weights 2^(lse_part - lse).  One wave a row.
+template <int DT>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (at >= (int64_t)a.B * a.H * a.Sq) return;
+    const int l = threadIdx.x & 63;
+    const float* lse = a.part_lse + at * a.nsplit;
+    const float* po = a.part_o + at * a.nsplit * a.D;
+    float m = -INFINITY, total = 0.0f, v0 = 0.0f, v1 = 0.0f;
+    for (int s = 0; s < a.nsplit; ++s) m = fmaxf(m, lse[s]);
+    const float ref = m == -INFINITY ? 0.0f : m;
+    for (int s = 0; s < a.nsplit; ++s) {
+        const float w = __builtin_amdgcn_exp2f(lse[s] - ref);
+        total += w;
+        if (w == 0.0f) continue;
+        if (l < a.D) v0 += w * po[s * a.D + l];
+        if (l + 64 < a.D) v1 += w * po[s * a.D + l + 64];
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    const int64_t pos = at % a.Sq, bh = at / a.Sq;
+    char* o = a.o.p + (bh / a.H) * a.o.sb + pos * a.o.ss + (bh % a.H) * a.o.sh;
+    if constexpr (DT == DT_BF16) {
+        if (l < a.D) reinterpret_cast<__bf16*>(o)[l] = (__bf16)(v0 * inv);
+        if (l + 64 < a.D) reinterpret_cast<__bf16*>(o)[l + 64] = (__bf16)(v1 * inv);
+    } else {
+        if (l < a.D) reinterpret_cast<float*>(o)[l] = v0 * inv;
+        if (l + 64 < a.D) reinterpret_cast<float*>(o)[l + 64] = v1 * inv;
+    }
+    if (l == 0) a.lse[at] = total == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(total)) * kLn2;
+}
+
+int attention_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int num_cus) {
+    const int64_t rows = Sq * G;
+    const bool few = rows <= kFewRows;
+    const int64_t tiles = few ? 1 : (rows + 127) / 128;
+    const int64_t blocks = B * Hkv * tiles, want = few ? 4 * num_cus : 2 * num_cus, least = few ? 256 : 512;
+    if (blocks == 0 || blocks >= want) return 1;
+    const int64_t by_keys = (Sk + least - 1) / least;
+    int64_t n = (want + blocks - 1) / blocks;
+    if (n > by_keys) n = by_keys;
+    if (n > 64) n = 64;
+    return n < 1 ? 1 : (int)n;
+}
+
+template <int DT, int ND>
+static void launch_attention(const AttnArgs& a, hipStream_t st) {
+    const int64_t rows = (int64_t)a.Sq * a.G;
+    if (rows <= kFewRows) {
+        const dim3 grid((unsigned)((int64_t)a.B * a.Hkv * a.nsplit));
+        hipLaunchKernelGGL((attention_few_kernel<DT, ND>), grid, dim3(256), 0, st, a);
+    } else {
+        const int64_t tiles = (rows + 127) / 128;
+        const dim3 grid((unsigned)((int64_t)a.B * a.Hkv * tiles * a.nsplit));
+        hipLaunchKernelGGL((attention_kernel<DT, ND>), grid, dim3(256), 0, st, a, tiles);
+    }
+    if (a.nsplit > 1) {
+        const dim3 grid((unsigned)(((int64_t)a.B * a.H * a.Sq + 3) / 4));
+        hipLaunchKernelGGL((attention_join_kernel<DT>), grid, dim3(256), 0, st, a);
+    }
+}
+
+hipError_t run_attention(const AttnArgs& a, int dtype, hipStream_t st) {
+    const int nd = (a.D + 31) / 32;
+#define PAMM_CASE(DT, ND) \
+    if (dtype == DT && nd == ND) launch_attention<DT, ND>(a, st)
+    PAMM_CASE(DT_BF16, 1);
+    PAMM_CASE(DT_BF16, 2);
+    PAMM_CASE(DT_BF16, 3);
+    PAMM_CASE(DT_BF16, 4);
+    PAMM_CASE(DT_F32, 1);
+    PAMM_CASE(DT_F32, 2);
+    PAMM_CASE(DT_F32, 3);
+    PAMM_CASE(DT_F32, 4);
+#undef PAMM_CASE
+    return hipGetLastError();
+}
+
+}  // namespace pamm

@@ -1,0 +1,239 @@
+// pamm_attention_device.hpp -- tiles and matrix products shared by the
+// attention kernels (gfx950).
+//
+// Everything is built from one 32 x 32 product whose operands are 16 bytes a
+// lane: bf16 takes one v_mfma_f32_32x32x16_bf16 (a contraction of 16), fp32
+// four v_mfma_f32_32x32x2f32 (a contraction of 8).  A lane holds row (A) or
+// column (B) l % 32, elements of the 16-byte group 2 s + l / 32 of step s.
+//
+// Result element i of lane l is D[8 (i / 4) + 4 (l / 32) + i % 4][l % 32].
+// That is also a valid B operand of the next product when its contraction
+// runs over D's rows in that same order: a contraction's order is free as long
+// as both operands agree, so probabilities go from one product to the next in
+// the registers they were born in, and only the A operand is fetched in
+// matching order (trans_product below).
+#pragma once
+#include "pamm_block_kernels.hpp"
+#include "pamm_device.hpp"
+
+namespace pamm {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// A tile of rows in LDS, ND x 32 elements a row, rows PITCH bytes apart.  The
+// 16-byte group c of row r lies at slot c ^ key(r): sixteen rows read at one
+// group (row operand) fall into sixteen different slots of the 256-byte bank
+// line, and the eight 64-byte pieces that half a wave reads for a transposed
+// operand (four rows and four more) do not share banks either.
+template <int DT, int ND>
+struct Tile {
+    static constexpr int ES = Elem<DT>::size;
+    static constexpr int PE = Elem<DT>::per16;
+    static constexpr int PITCH = (ND <= 2 ? 64 : 128) * ES;
+    static constexpr int NS = ND * ES;        // 32-byte contraction steps of a row
+    static constexpr int CPR = 2 * NS;        // 16-byte groups of a row that are used
+    __device__ static __forceinline__ int key(int r) {
+        if constexpr (PITCH == 128) {
+            const int r2 = r >> 1;
+            return ((r2 & 1) << 2) | ((r2 >> 1) & 3);
+        } else {
+            return ((r & 3) << 2) | ((r >> 2) & 3);
+        }
+    }
+    __device__ static __forceinline__ int offset(int r, int c) { return r * PITCH + ((c ^ key(r)) << 4); }
+};
+
+// One 32 x 32 product step; a and b are 16 bytes of A and B.
+template <int DT>
+__device__ __forceinline__ f32x16 mma_step(const uint4& a, const uint4& b, f32x16 c) {
+    if constexpr (DT == DT_BF16) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+    } else {
+        const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[j], y[j], c, 0, 0, 0);
+        return c;
+    }
+}
+
+// 32 x 32 results as the B operand of a product that contracts over D's rows:
+// bf16 rounds each value once (nearest even) and packs, fp32 keeps them.
+template <int DT> struct Packed;
+template <> struct Packed<DT_BF16> {
+    bf16x8 v[2];
+    __device__ __forceinline__ void set(const f32x16& d) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = (__bf16)d[i];
+    }
+};
+template <> struct Packed<DT_F32> {
+    f32x16 v;
+    __device__ __forceinline__ void set(const f32x16& d) { v = d; }
+};
+
+// acc[db] += (the 32 rows of `tile` from row r0, transposed) x b, for the ND
+// 32-element column blocks db: acc[db][e][col] += sum_r tile[r][32 db + e] b[r][col].
+// bf16 reads its operand with the transposing LDS load: the 16 lanes of a
+// group point at four rows of 32 bytes and each gets one column of the four.
+template <int DT, int ND>
+__device__ __forceinline__ void trans_product(const char* tile, int r0, const Packed<DT>& b, f32x16* acc) {
+    using T = Tile<DT, ND>;
+    const int l = lane_id(), h = l >> 5;
+    if constexpr (DT == DT_BF16) {
+        const int row = 4 * h + ((l & 15) >> 2);
+        const int c = ((l >> 4) & 1) * 2 + ((l & 3) >> 1), sub = (l & 1) * 8;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int db = 0; db < ND; ++db) {
+                typedef __attribute__((address_space(3))) s16x4* lds_s4;
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_s4)(tile + (r0 + 16 * t) * T::PITCH + T::offset(row, 4 * db + c) + sub));
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_s4)(tile + (r0 + 16 * t) * T::PITCH + T::offset(row + 8, 4 * db + c) + sub));
+                typedef short s16x8 __attribute__((ext_vector_type(8)));
+                const s16x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), b.v[t], acc[db], 0, 0, 0);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int row = r0 + 8 * (i >> 2) + 4 * h + (i & 3);
+#pragma unroll
+            for (int db = 0; db < ND; ++db) {
+                const int e = 32 * db + (l & 31);
+                const float a = *reinterpret_cast<const float*>(tile + T::offset(row, e >> 2) + (e & 3) * 4);
+                acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, b.v[i], acc[db], 0, 0, 0);
+            }
+        }
+    }
+}
+
+// Row operand of step s: 16 bytes of row r0 + l % 32.
+template <int DT, int ND>
+__device__ __forceinline__ uint4 row_operand(const char* tile, int r0, int s) {
+    const int l = lane_id();
+    return *reinterpret_cast<const uint4*>(tile + Tile<DT, ND>::offset(r0 + (l & 31), 2 * s + (l >> 5)));
+}
+
+// This lane's 16-byte groups of one global row (zero where !ok or past D).
+template <int DT, int ND>
+__device__ __forceinline__ void load_row_operand(uint4* f, const char* row, bool ok, int D) {
+    const int h = lane_id() >> 5;
+#pragma unroll
+    for (int s = 0; s < Tile<DT, ND>::NS; ++s) {
+        const int c = 2 * s + h;
+        f[s] = make_uint4(0, 0, 0, 0);
+        if (ok && c * Elem<DT>::per16 < D) f[s] = *reinterpret_cast<const uint4*>(row + c * 16);
+    }
+}
+
+// Flip the sign of every element (exact).
+template <int DT>
+__device__ __forceinline__ uint4 negate16(uint4 v) {
+    const uint32_t m = DT == DT_BF16 ? 0x80008000u : 0x80000000u;
+    return make_uint4(v.x ^ m, v.y ^ m, v.z ^ m, v.w ^ m);
+}
+
+// The two halves of a wave hold the other half of a column: v of lane l % 32
+// and of lane l % 32 + 32, in every lane.
+__device__ __forceinline__ float half_max(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Copies rows [0, ROWS) of a tile through registers: fetch() issues the
+// global loads, put() writes them to LDS.  NT threads take part.  Rows at or
+// past `rows` and elements past D become zero.
+template <int DT, int ND, int ROWS, int NT>
+struct TileCopy {
+    using T = Tile<DT, ND>;
+    static constexpr int N = ROWS * T::CPR;
+    static constexpr int PER = (N + NT - 1) / NT;
+    uint4 r[PER];
+    __device__ __forceinline__ void fetch(const char* base, int64_t stride, int64_t rows, int D, int tid) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int id = tid + i * NT, row = id / T::CPR, c = id % T::CPR;
+            r[i] = make_uint4(0, 0, 0, 0);
+            if ((N % NT == 0 || id < N) && row < rows && c * T::PE < D)
+                r[i] = *reinterpret_cast<const uint4*>(base + row * stride + c * 16);
+        }
+    }
+    __device__ __forceinline__ void put(char* tile, int tid) const {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int id = tid + i * NT, row = id / T::CPR, c = id % T::CPR;
+            if (N % NT == 0 || id < N) *reinterpret_cast<uint4*>(tile + T::offset(row, c)) = r[i];
+        }
+    }
+};
+
+// Keys [lo, hi) that query position p sees, given the sequence's lengths.
+struct KeyRange {
+    int64_t lo, hi;
+};
+__device__ __forceinline__ KeyRange key_range(const AttnArgs& a, int64_t p, int64_t Lq, int64_t Lk) {
+    KeyRange r{0, Lk};
+    if (p >= Lq) {
+        r.hi = 0;
+    } else if (a.causal) {
+        const int64_t last = p + Lk - Lq;  // < Lk
+        r.hi = last + 1;
+        if (a.window) r.lo = last + 1 - a.window;
+        if (r.hi < 0) r.hi = 0;
+        if (r.lo < 0) r.lo = 0;
+    }
+    return r;
+}
+
+__device__ __forceinline__ int64_t valid_length(const int32_t* len, int b, int64_t most) {
+    if (!len) return most;
+    const int64_t v = len[b];
+    return v < 0 ? 0 : v > most ? most : v;
+}
+
+// Workgroups are dealt to the 8 XCDs in turn; give each XCD one contiguous
+// piece of the work list, so that the workgroups that share keys share an L2.
+__device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
+    const int64_t x = id % 8, s = id / 8, q = total / 8, r = total % 8;
+    return x * q + (x < r ? x : r) + s;
+}
+
+// Writes ND blocks of 32 x 32 results that are transposed rows: this lane's
+// row `row` gets elements 32 db + 8 (i / 4) + 4 h + i % 4, scaled by f.
+template <int DT, int ND>
+__device__ __forceinline__ void store_rows(char* row, const f32x16* acc, float f, int D) {
+    const int h = lane_id() >> 5;
+#pragma unroll
+    for (int db = 0; db < ND; ++db) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int e = 32 * db + 8 * g + 4 * h;
+            if (e >= D) continue;
+            const float x0 = acc[db][4 * g] * f, x1 = acc[db][4 * g + 1] * f, x2 = acc[db][4 * g + 2] * f,
+                        x3 = acc[db][4 * g + 3] * f;
+            if constexpr (DT == DT_BF16) {
+                bf16x2 u, v;
+                u[0] = (__bf16)x0, u[1] = (__bf16)x1, v[0] = (__bf16)x2, v[1] = (__bf16)x3;
+                uint2 w;
+                w.x = __builtin_bit_cast(uint32_t, u), w.y = __builtin_bit_cast(uint32_t, v);
+                *reinterpret_cast<uint2*>(row + 2 * e) = w;
+            } else {
+                *reinterpret_cast<float4*>(row + 4 * e) = make_float4(x0, x1, x2, x3);
+            }
+        }
+    }
+}
+
+}  // namespace pamm
