@@ -57,13 +57,10 @@ __device__ __forceinline__ void softmax_update(f32x16& s, float c, Running& st, 
     st.l += sum;
 }
 
-__device__ __forceinline__ void mask_block(f32x16& s, int64_t key0, int64_t lo, int64_t hi) {
-    const int first = 4 * (lane_id() >> 5);
+__device__ __forceinline__ void mask_block(f32x16& s, int key0, const KeyRange& r) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t key = key0 + first + 8 * (i >> 2) + (i & 3);
-        if (key < lo || key >= hi) s[i] = -INFINITY;
-    }
+    for (int i = 0; i < 16; ++i)
+        if (!sees(key0, i, r)) s[i] = -INFINITY;
 }
 
 // Scores' factor in log2 units; its sign is folded into the query operand.
@@ -87,31 +84,22 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_kernel(A
     // the last rows see the most keys: they start first
     const int64_t tile = row_tiles - 1 - id % row_tiles;
     const int bh = (int)(id / row_tiles), b = bh / a.Hkv, hk = bh % a.Hkv;
-    const int64_t Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
-    const int64_t rows = (int64_t)a.Sq * a.G;
+    const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
+    const int rows = a.Sq * a.G;
 
     // what this lane's row, this wave's rows and this workgroup's rows see
-    const int64_t r0 = tile * 128, w0 = r0 + wave * 32, row = w0 + (l & 31);
-    const int64_t pos = row / a.G;
-    const int head = hk * a.G + (int)(row % a.G);
+    const int r0 = (int)tile * 128, w0 = r0 + wave * 32, row = w0 + (l & 31);
+    const int pos = row / a.G, head = hk * a.G + row % a.G;
     const bool live = row < rows;
-    const KeyRange mine = key_range(a, live ? pos : Lq, Lq, Lk);
-    const int64_t wlast = (w0 + 31 < rows ? w0 + 31 : rows - 1) / a.G, wfirst = w0 / a.G;
-    const int64_t blast = (r0 + 127 < rows ? r0 + 127 : rows - 1) / a.G, bfirst = r0 / a.G;
-    const int64_t wend = wfirst < Lq ? key_range(a, wlast < Lq ? wlast : Lq - 1, Lq, Lk).hi : 0;
-    const int64_t wbegin = key_range(a, wfirst, Lq, Lk).lo;
-    // keys in [wall_lo, wall_hi) are seen by every row of the wave
-    const KeyRange last_range = key_range(a, wlast, Lq, Lk);
-    const int64_t wall_lo = last_range.lo;
-    const int64_t wall_hi = (w0 + 31 < rows && wlast < Lq) ? key_range(a, wfirst, Lq, Lk).hi : 0;
-    const int64_t bend = bfirst < Lq ? key_range(a, blast < Lq ? blast : Lq - 1, Lq, Lk).hi : 0;
-    const int64_t bbegin = key_range(a, bfirst, Lq, Lk).lo;
+    KeyRange mine = key_range(a, live ? pos : Lq, Lq, Lk);
+    if (mine.hi < mine.lo) mine.hi = mine.lo;
+    const RowsRange wr = rows_range(a, w0, 32, rows, Lq, Lk), br = rows_range(a, r0, 128, rows, Lq, Lk);
 
-    int64_t t0 = bbegin / BK, t1 = (bend + BK - 1) / BK;
+    int t0 = br.begin / BK, t1 = (br.end + BK - 1) / BK;
     if (t1 < t0) t1 = t0;
     if (a.nsplit > 1) {
-        const int64_t per = (t1 - t0 + a.nsplit - 1) / a.nsplit;
-        const int64_t s0 = t0 + split * per;
+        const int per = (t1 - t0 + a.nsplit - 1) / a.nsplit;
+        const int s0 = t0 + split * per;
         t1 = s0 + per < t1 ? s0 + per : t1;
         t0 = s0 < t1 ? s0 : t1;
     }
@@ -132,28 +120,29 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_kernel(A
 
     TileCopy<DT, ND, BK, 256> kc, vc;
     if (t0 < t1) {
-        kc.fetch(kbase + t0 * BK * a.k.ss, a.k.ss, Lk - t0 * BK, a.D, tid);
-        vc.fetch(vbase + t0 * BK * a.v.ss, a.v.ss, Lk - t0 * BK, a.D, tid);
+        kc.fetch(kbase + t0 * BK * a.k.ss, (int)a.k.ss, Lk - t0 * BK, a.D, tid);
+        vc.fetch(vbase + t0 * BK * a.v.ss, (int)a.v.ss, Lk - t0 * BK, a.D, tid);
         kc.put(lds[0][0], tid);
         vc.put(lds[0][1], tid);
     }
     __syncthreads();
     int cur = 0;
-    for (int64_t t = t0; t < t1; ++t, cur ^= 1) {
+    for (int t = t0; t < t1; ++t, cur ^= 1) {
         const bool more = t + 1 < t1;
         if (more) {
-            kc.fetch(kbase + (t + 1) * BK * a.k.ss, a.k.ss, Lk - (t + 1) * BK, a.D, tid);
-            vc.fetch(vbase + (t + 1) * BK * a.v.ss, a.v.ss, Lk - (t + 1) * BK, a.D, tid);
+            kc.fetch(kbase + (t + 1) * BK * a.k.ss, (int)a.k.ss, Lk - (t + 1) * BK, a.D, tid);
+            vc.fetch(vbase + (t + 1) * BK * a.v.ss, (int)a.v.ss, Lk - (t + 1) * BK, a.D, tid);
         }
 #pragma unroll
         for (int kb = 0; kb < BK / 32; ++kb) {
-            const int64_t key0 = t * BK + kb * 32;
-            if (key0 >= wend || key0 + 32 <= wbegin) continue;
+            const int key0 = t * BK + kb * 32;
+            if (key0 >= wr.end || key0 + 32 <= wr.begin) continue;
             f32x16 s{};
 #pragma unroll
             for (int i = 0; i < T::NS; ++i)
                 s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], kb * 32, i), qf[i], s);
-            if (key0 < wall_lo || key0 + 32 > wall_hi) mask_block(s, key0, mine.lo, mine.hi);
+            settle<DT>(s);
+            if (key0 < wr.all_lo || key0 + 32 > wr.all_hi) mask_block(s, key0, mine);
             softmax_update<ND>(s, c, st, acc);
             Packed<DT> p;
             p.set(s);
@@ -166,6 +155,8 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_kernel(A
         __syncthreads();
     }
 
+#pragma unroll
+    for (int db = 0; db < ND; ++db) settle<DT>(acc[db]);
     if (!live) return;
     const float sum = half_sum(st.l);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -202,18 +193,18 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_few_kern
     const int split = (int)(id % a.nsplit);
     id /= a.nsplit;
     const int b = (int)(id / a.Hkv), hk = (int)(id % a.Hkv);
-    const int64_t Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
+    const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
     const int rows = a.Sq * a.G;
     const int row = l & 31, pos = row / a.G, head = hk * a.G + row % a.G;
     const bool live = row < rows;
-    const KeyRange mine = key_range(a, live ? pos : Lq, Lq, Lk);
-    const int64_t end = Lq > 0 ? key_range(a, Lq - 1, Lq, Lk).hi : 0;
-    const int64_t begin = key_range(a, 0, Lq, Lk).lo;
-    const int64_t n0 = begin / 32;
-    int64_t n1 = (end + 31) / 32;
+    KeyRange mine = key_range(a, live ? pos : Lq, Lq, Lk);
+    if (mine.hi < mine.lo) mine.hi = mine.lo;
+    const RowsRange br = rows_range(a, 0, rows, rows, Lq, Lk);
+    const int n0 = br.begin / 32;
+    int n1 = (br.end + 31) / 32;
     if (n1 < n0) n1 = n0;
-    const int64_t per = (n1 - n0 + a.nsplit - 1) / a.nsplit;
-    const int64_t p0 = n0 + split * per, p1 = p0 + per < n1 ? p0 + per : n1;
+    const int per = (n1 - n0 + a.nsplit - 1) / a.nsplit;
+    const int p0 = n0 + split * per, p1 = p0 + per < n1 ? p0 + per : n1;
 
     const char* kbase = a.k.p + b * a.k.sb + hk * a.k.sh;
     const char* vbase = a.v.p + b * a.v.sb + hk * a.v.sh;
@@ -230,31 +221,38 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_few_kern
     char* vt = lds + wave * VT;
     TileCopy<DT, ND, 32, 64> vc;
 
-    int64_t t = p0 + wave;
-    if (t < p1) {
-        load_row_operand<DT, ND>(kf, kbase + (t * 32 + row) * a.k.ss, t * 32 + row < Lk, a.D);
-        vc.fetch(vbase + t * 32 * a.v.ss, a.v.ss, Lk - t * 32, a.D, l);
-    }
+    auto fetch = [&](int key0) {
+        const RowView view(kbase + key0 * a.k.ss, (int)a.k.ss, Lk - key0, 32, a.D * T::ES);
+#pragma unroll
+        for (int i = 0; i < T::NS; ++i) {
+            const int g = 2 * i + (l >> 5);
+            kf[i] = view.load(g * T::PE < a.D ? row * (int)a.k.ss + g * 16 : kOutside);
+        }
+        vc.fetch(vbase + key0 * a.v.ss, (int)a.v.ss, Lk - key0, a.D, l);
+    };
+    int t = p0 + wave;
+    if (t < p1) fetch(t * 32);
     for (; t < p1; t += 4) {
-        const int64_t key0 = t * 32, next = key0 + 128;
+        const int key0 = t * 32;
         f32x16 s{};
 #pragma unroll
         for (int i = 0; i < T::NS; ++i) s = mma_step<DT>(kf[i], qf[i], s);
+        settle<DT>(s);
         __builtin_amdgcn_wave_barrier();
         vc.put(vt, l);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        if (t + 4 < p1) {
-            load_row_operand<DT, ND>(kf, kbase + (next + row) * a.k.ss, next + row < Lk, a.D);
-            vc.fetch(vbase + next * a.v.ss, a.v.ss, Lk - next, a.D, l);
-        }
-        mask_block(s, key0, mine.lo, mine.hi);
+        if (t + 4 < p1) fetch(key0 + 128);
+        if (key0 < br.all_lo || key0 + 32 > br.all_hi) mask_block(s, key0, mine);
         softmax_update<ND>(s, c, st, acc);
         Packed<DT> p;
         p.set(s);
         trans_product<DT, ND>(vt, 0, p, acc);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
+
+#pragma unroll
+    for (int db = 0; db < ND; ++db) settle<DT>(acc[db]);
 
     // join the four waves: the common reference first, then the sums in order
     const float sum = half_sum(st.l);

@@ -37,21 +37,15 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
     const int64_t id = xcd_order(blockIdx.x, gridDim.x);
     const int64_t tile = row_tiles - 1 - id % row_tiles;
     const int bh = (int)(id / row_tiles), b = bh / a.Hkv, hk = bh % a.Hkv;
-    const int64_t Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
-    const int64_t rows = (int64_t)a.Sq * a.G;
-    const int64_t r0 = tile * 128, w0 = r0 + wave * 32, row = w0 + (l & 31);
-    const int64_t pos = row / a.G;
-    const int head = hk * a.G + (int)(row % a.G);
+    const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
+    const int rows = a.Sq * a.G;
+    const int r0 = (int)tile * 128, w0 = r0 + wave * 32, row = w0 + (l & 31);
+    const int pos = row / a.G, head = hk * a.G + row % a.G;
     const bool live = row < rows;
-    const KeyRange mine = key_range(a, live ? pos : Lq, Lq, Lk);
-    const int64_t wlast = (w0 + 31 < rows ? w0 + 31 : rows - 1) / a.G, wfirst = w0 / a.G;
-    const int64_t blast = (r0 + 127 < rows ? r0 + 127 : rows - 1) / a.G, bfirst = r0 / a.G;
-    const int64_t wend = wfirst < Lq ? key_range(a, wlast < Lq ? wlast : Lq - 1, Lq, Lk).hi : 0;
-    const int64_t wbegin = key_range(a, wfirst, Lq, Lk).lo;
-    const int64_t wall_lo = key_range(a, wlast, Lq, Lk).lo;
-    const int64_t wall_hi = (w0 + 31 < rows && wlast < Lq) ? key_range(a, wfirst, Lq, Lk).hi : 0;
-    const int64_t bend = bfirst < Lq ? key_range(a, blast < Lq ? blast : Lq - 1, Lq, Lk).hi : 0;
-    const int64_t t0 = key_range(a, bfirst, Lq, Lk).lo / BK, t1 = (bend + BK - 1) / BK;
+    KeyRange mine = key_range(a, live ? pos : Lq, Lq, Lk);
+    if (mine.hi < mine.lo) mine.hi = mine.lo;
+    const RowsRange wr = rows_range(a, w0, 32, rows, Lq, Lk), br = rows_range(a, r0, 128, rows, Lq, Lk);
+    const int t0 = br.begin / BK, t1 = (br.end + BK - 1) / BK;
 
     const char* kbase = a.k.p + b * a.k.sb + hk * a.k.sh;
     const char* vbase = a.v.p + b * a.v.sb + hk * a.v.sh;
@@ -79,37 +73,37 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
     for (int db = 0; db < ND; ++db) acc[db] = f32x16{};
     TileCopy<DT, ND, BK, 256> kc, vc;
     if (t0 < t1) {
-        kc.fetch(kbase + t0 * BK * a.k.ss, a.k.ss, Lk - t0 * BK, a.D, tid);
-        vc.fetch(vbase + t0 * BK * a.v.ss, a.v.ss, Lk - t0 * BK, a.D, tid);
+        kc.fetch(kbase + t0 * BK * a.k.ss, (int)a.k.ss, Lk - t0 * BK, a.D, tid);
+        vc.fetch(vbase + t0 * BK * a.v.ss, (int)a.v.ss, Lk - t0 * BK, a.D, tid);
         kc.put(lds[0][0], tid);
         vc.put(lds[0][1], tid);
     }
     __syncthreads();
     int cur = 0;
-    for (int64_t t = t0; t < t1; ++t, cur ^= 1) {
+    for (int t = t0; t < t1; ++t, cur ^= 1) {
         const bool more = t + 1 < t1;
         if (more) {
-            kc.fetch(kbase + (t + 1) * BK * a.k.ss, a.k.ss, Lk - (t + 1) * BK, a.D, tid);
-            vc.fetch(vbase + (t + 1) * BK * a.v.ss, a.v.ss, Lk - (t + 1) * BK, a.D, tid);
+            kc.fetch(kbase + (t + 1) * BK * a.k.ss, (int)a.k.ss, Lk - (t + 1) * BK, a.D, tid);
+            vc.fetch(vbase + (t + 1) * BK * a.v.ss, (int)a.v.ss, Lk - (t + 1) * BK, a.D, tid);
         }
 #pragma unroll
         for (int kb = 0; kb < BK / 32; ++kb) {
-            const int64_t key0 = t * BK + kb * 32;
-            if (key0 >= wend || key0 + 32 <= wbegin) continue;
+            const int key0 = t * BK + kb * 32;
+            if (key0 >= wr.end || key0 + 32 <= wr.begin) continue;
             f32x16 s{}, dp{};
 #pragma unroll
             for (int i = 0; i < T::NS; ++i) {
                 s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], kb * 32, i), qf[i], s);
                 dp = mma_step<DT>(row_operand<DT, ND>(lds[cur][1], kb * 32, i), dof[i], dp);
             }
+            settle<DT>(s);
+            settle<DT>(dp);
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse2)) * (dp[i] - delta);
-            if (key0 < wall_lo || key0 + 32 > wall_hi) {
+            if (key0 < wr.all_lo || key0 + 32 > wr.all_hi) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int64_t key = key0 + 4 * (l >> 5) + 8 * (i >> 2) + (i & 3);
-                    if (key < mine.lo || key >= mine.hi) s[i] = 0.0f;
-                }
+                for (int i = 0; i < 16; ++i)
+                    if (!sees(key0, i, mine)) s[i] = 0.0f;
             }
             Packed<DT> ds;
             ds.set(s);
@@ -121,51 +115,64 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
         }
         __syncthreads();
     }
+#pragma unroll
+    for (int db = 0; db < ND; ++db) settle<DT>(acc[db]);
     if (live) store_rows<DT, ND>(a.dq.p + b * a.dq.sb + pos * a.dq.ss + head * a.dq.sh, acc, a.scale, a.D);
 }
 
 // dk and dv.  Scores as S = Q K^T: a lane owns a key.  Four waves of 32 keys
-// share tiles of BQ queries of one head, head after head.
+// share tiles of 32 queries of one head, head after head.  V stays in
+// registers as an operand, K in LDS: both in registers beside 128 sums a lane
+// would leave one wave a SIMD.
 template <int DT, int ND>
-__global__ __launch_bounds__(256, 1) void attention_dkv_kernel(AttnArgs a, int64_t key_tiles) {
+__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kernel(AttnArgs a, int64_t key_tiles) {
     using T = Tile<DT, ND>;
     constexpr int BQ = 32;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BQ * T::PITCH];
+    __shared__ __attribute__((aligned(16))) char ldk[128 * T::PITCH];
     __shared__ __attribute__((aligned(16))) float rowstat[2][2][BQ];
     const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
 
     const int64_t id = xcd_order(blockIdx.x, gridDim.x);
-    const int64_t tile = id % key_tiles;  // the first keys are seen by the most queries
+    const int tile = (int)(id % key_tiles);  // the first keys are seen by the most queries
     const int bh = (int)(id / key_tiles), b = bh / a.Hkv, hk = bh % a.Hkv;
-    const int64_t Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
-    const int64_t off = Lk - Lq;
-    const int64_t b0 = tile * 128, w0 = b0 + wave * 32, key = w0 + (l & 31);
+    const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
+    const int off = Lk - Lq;
+    const int b0 = tile * 128, w0 = b0 + wave * 32, key = w0 + (l & 31);
     const bool live = key < a.Sk;
 
     // positions that see some key of the workgroup (of the wave): [p0, p1) ([wp0, wp1))
-    int64_t p0 = 0, p1 = b0 < Lk ? Lq : 0, wp0 = 0, wp1 = w0 < Lk ? Lq : 0;
+    int p0 = 0, p1 = b0 < Lk ? Lq : 0, wp0 = 0, wp1 = w0 < Lk ? Lq : 0;
     if (a.causal) {
         if (b0 - off > p0) p0 = b0 - off;
         if (w0 - off > wp0) wp0 = w0 - off;
         if (a.window) {
-            const int64_t e = b0 + 127 - off + a.window, we = w0 + 31 - off + a.window;
+            const int e = b0 + 127 - off + a.window, we = w0 + 31 - off + a.window;
             if (e < p1) p1 = e;
             if (we < wp1) wp1 = we;
         }
     }
-    const int64_t n0 = p0 / BQ;
-    int64_t n1 = (p1 + BQ - 1) / BQ;
+    const int n0 = p0 / BQ;
+    int n1 = (p1 + BQ - 1) / BQ;
     if (n1 < n0) n1 = n0;
-    const int64_t per_head = n1 - n0, n = per_head * a.G;
+    const int64_t n = (int64_t)(n1 - n0) * a.G;
+    // positions that see this lane's key: [first, last)
+    int first = 0, last = key < Lk ? Lq : 0;
+    if (a.causal) {
+        if (key - off > first) first = key - off;
+        if (a.window && key - off + a.window < last) last = key - off + a.window;
+    }
+    if (last < first) last = first;
 
-    const bool seen = key < Lk;
-    uint4 kf[T::NS], vf[T::NS];
-    load_row_operand<DT, ND>(kf, a.k.p + b * a.k.sb + key * a.k.ss + hk * a.k.sh, seen, a.D);
-    load_row_operand<DT, ND>(vf, a.v.p + b * a.v.sb + key * a.v.ss + hk * a.v.sh, seen, a.D);
-    if (a.scale < 0.0f)
+    uint4 vf[T::NS];
+    load_row_operand<DT, ND>(vf, a.v.p + b * a.v.sb + key * a.v.ss + hk * a.v.sh, key < Lk, a.D);
 #pragma unroll
-        for (int s = 0; s < T::NS; ++s) kf[s] = negate16<DT>(kf[s]);
-    const float c = score_factor(a.scale);
+    for (int i = 0; i < 2; ++i) {
+        TileCopy<DT, ND, 64, 256> kc;
+        kc.fetch(a.k.p + b * a.k.sb + (b0 + 64 * i) * a.k.ss + hk * a.k.sh, (int)a.k.ss, Lk - b0 - 64 * i, a.D, tid);
+        kc.put(ldk + 64 * i * T::PITCH, tid);
+    }
+    const float c = score_factor(a.scale) * (a.scale < 0.0f ? -1.0f : 1.0f);
 
     f32x16 dk[ND], dv[ND];
 #pragma unroll
@@ -173,11 +180,10 @@ __global__ __launch_bounds__(256, 1) void attention_dkv_kernel(AttnArgs a, int64
 
     TileCopy<DT, ND, BQ, 256> qc, oc;
     float stat = 0.0f;
-    auto fetch = [&](int64_t g, int64_t t) {
-        const int head = hk * a.G + (int)g;
-        const int64_t q0 = t * BQ;
-        qc.fetch(a.q.p + b * a.q.sb + head * a.q.sh + q0 * a.q.ss, a.q.ss, Lq - q0, a.D, tid);
-        oc.fetch(a.dout.p + b * a.dout.sb + head * a.dout.sh + q0 * a.dout.ss, a.dout.ss, Lq - q0, a.D, tid);
+    auto fetch = [&](int g, int t) {
+        const int head = hk * a.G + g, q0 = t * BQ;
+        qc.fetch(a.q.p + b * a.q.sb + head * a.q.sh + q0 * a.q.ss, (int)a.q.ss, Lq - q0, a.D, tid);
+        oc.fetch(a.dout.p + b * a.dout.sb + head * a.dout.sh + q0 * a.dout.ss, (int)a.dout.ss, Lq - q0, a.D, tid);
         const int r = tid % BQ;
         const int64_t at = ((int64_t)b * a.H + head) * a.Sq + q0 + r;
         if (tid < BQ) {
@@ -192,7 +198,7 @@ __global__ __launch_bounds__(256, 1) void attention_dkv_kernel(AttnArgs a, int64
         oc.put(lds[buf][1], tid);
         if (tid < 2 * BQ) rowstat[buf][tid / BQ][tid % BQ] = stat;
     };
-    int64_t t = n0, g = 0;
+    int t = n0, g = 0;
     if (n > 0) {
         fetch(0, n0);
         put(0);
@@ -200,29 +206,23 @@ __global__ __launch_bounds__(256, 1) void attention_dkv_kernel(AttnArgs a, int64
     __syncthreads();
     int cur = 0;
     for (int64_t i = 0; i < n; ++i, cur ^= 1) {
-        int64_t tn = t + 1, gn = g;
+        int tn = t + 1, gn = g;
         if (tn == n1) tn = n0, ++gn;
         if (i + 1 < n) fetch(gn, tn);
-        const int64_t q0 = t * BQ;
+        const int q0 = t * BQ;
         if (q0 < wp1 && q0 + BQ > wp0) {
-            f32x16 s{}, dp{};
+            f32x16 s{};
 #pragma unroll
-            for (int x = 0; x < T::NS; ++x) {
-                s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], 0, x), kf[x], s);
-                dp = mma_step<DT>(row_operand<DT, ND>(lds[cur][1], 0, x), vf[x], dp);
-            }
-            const int first = 4 * (l >> 5);
+            for (int x = 0; x < T::NS; ++x)
+                s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], 0, x), row_operand<DT, ND>(ldk, wave * 32, x), s);
+            settle<DT>(s);
+            const int quad = 4 * (l >> 5);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                const float4 ls = *reinterpret_cast<const float4*>(&rowstat[cur][0][8 * y + first]);
-                const float4 de = *reinterpret_cast<const float4*>(&rowstat[cur][1][8 * y + first]);
-                const float lv[4] = {ls.x, ls.y, ls.z, ls.w}, dv4[4] = {de.x, de.y, de.z, de.w};
+                const float4 ls = *reinterpret_cast<const float4*>(&rowstat[cur][0][8 * y + quad]);
+                const float lv[4] = {ls.x, ls.y, ls.z, ls.w};
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int e = 4 * y + z;
-                    s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lv[z]));
-                    dp[e] = s[e] * (dp[e] - dv4[z]);
-                }
+                for (int z = 0; z < 4; ++z) s[4 * y + z] = __builtin_amdgcn_exp2f(fmaf(s[4 * y + z], c, -lv[z]));
             }
             // some pair of this block is masked?
             bool part = w0 + 32 > Lk || q0 + BQ > Lq;
@@ -230,24 +230,43 @@ __global__ __launch_bounds__(256, 1) void attention_dkv_kernel(AttnArgs a, int64
                 part = part || w0 + 31 > q0 + off;
                 if (a.window) part = part || w0 <= q0 + BQ - 1 + off - a.window;
             }
+            const KeyRange seen{first, last};
             if (part) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int64_t p = q0 + first + 8 * (e >> 2) + (e & 3);
-                    const KeyRange r = key_range(a, p, Lq, Lk);
-                    if (key < r.lo || key >= r.hi) s[e] = dp[e] = 0.0f;
-                }
+                for (int e = 0; e < 16; ++e)
+                    if (!sees(q0, e, seen)) s[e] = 0.0f;
             }
             Packed<DT> pk;
             pk.set(s);
             trans_product<DT, ND>(lds[cur][1], 0, pk, dv);
-            pk.set(dp);
+            f32x16 dp{};
+#pragma unroll
+            for (int x = 0; x < T::NS; ++x) dp = mma_step<DT>(row_operand<DT, ND>(lds[cur][1], 0, x), vf[x], dp);
+            settle<DT>(dp);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const float4 de = *reinterpret_cast<const float4*>(&rowstat[cur][1][8 * y + quad]);
+                const float ev[4] = {de.x, de.y, de.z, de.w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z) s[4 * y + z] *= dp[4 * y + z] - ev[z];
+            }
+            if (part) {  // P is 0 there; keep what is not finite out as well
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (!sees(q0, e, seen)) s[e] = 0.0f;
+            }
+            pk.set(s);
             trans_product<DT, ND>(lds[cur][0], 0, pk, dk);
         }
         if (i + 1 < n) put(cur ^ 1);
         __syncthreads();
         t = tn;
         g = gn;
+    }
+#pragma unroll
+    for (int db = 0; db < ND; ++db) {
+        settle<DT>(dk[db]);
+        settle<DT>(dv[db]);
     }
     if (live) {
         store_rows<DT, ND>(a.dk.p + b * a.dk.sb + key * a.dk.ss + hk * a.dk.sh, dk, a.scale, a.D);

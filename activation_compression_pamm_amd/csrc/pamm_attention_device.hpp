@@ -61,6 +61,20 @@ __device__ __forceinline__ f32x16 mma_step(const uint4& a, const uint4& b, f32x1
     }
 }
 
+// A result may be read by ordinary instructions only some wait states after its
+// last product (11 after the bf16 product's 8 passes, 18 after the fp32 one's
+// 16), which the compiler counts and fills.  Where a branch that may be skipped
+// lies between the two, ROCm 7.2's compiler was seen to count along the longer
+// way round only and to read results too early.  So each result is waited for
+// in the block that computed it, before any branch.
+template <int DT>
+__device__ __forceinline__ void settle(f32x16& d) {
+    if constexpr (DT == DT_BF16)
+        asm volatile("s_nop 10" : "+v"(d));
+    else
+        asm volatile("s_nop 15\n\ts_nop 1" : "+v"(d));
+}
+
 // 32 x 32 results as the B operand of a product that contracts over D's rows:
 // bf16 rounds each value once (nearest even) and packs, fp32 keeps them.
 template <int DT> struct Packed;
@@ -152,6 +166,22 @@ __device__ __forceinline__ float half_sum(float v) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// A bounded view of `rows` rows of D elements, `stride` bytes apart: what is
+// read through it past the last row's end is zero.  64 rows span less than
+// 2 GiB, so offsets into it are 32 bits; tiles move the base.
+struct RowView {
+    __amdgpu_buffer_rsrc_t rsrc;
+    __device__ __forceinline__ RowView(const char* base, int stride, int rows, int most, int row_bytes) {
+        const int n = rows < most ? rows : most;
+        const int bytes = n > 0 ? (n - 1) * stride + row_bytes : 0;
+        rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, bytes, 0x00020000);
+    }
+    __device__ __forceinline__ uint4 load(int offset) const {
+        return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, offset, 0, 0));
+    }
+};
+constexpr int kOutside = (int)0x80000000u;  // an offset past every view's end
+
 // Copies rows [0, ROWS) of a tile through registers: fetch() issues the
 // global loads, put() writes them to LDS.  NT threads take part.  Rows at or
 // past `rows` and elements past D become zero.
@@ -161,13 +191,12 @@ struct TileCopy {
     static constexpr int N = ROWS * T::CPR;
     static constexpr int PER = (N + NT - 1) / NT;
     uint4 r[PER];
-    __device__ __forceinline__ void fetch(const char* base, int64_t stride, int64_t rows, int D, int tid) {
+    __device__ __forceinline__ void fetch(const char* base, int stride, int rows, int D, int tid) {
+        const RowView v(base, stride, rows, ROWS, D * T::ES);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int id = tid + i * NT, row = id / T::CPR, c = id % T::CPR;
-            r[i] = make_uint4(0, 0, 0, 0);
-            if ((N % NT == 0 || id < N) && row < rows && c * T::PE < D)
-                r[i] = *reinterpret_cast<const uint4*>(base + row * stride + c * 16);
+            r[i] = v.load((N % NT == 0 || id < N) && c * T::PE < D ? row * stride + c * 16 : kOutside);
         }
     }
     __device__ __forceinline__ void put(char* tile, int tid) const {
@@ -180,15 +209,16 @@ struct TileCopy {
 };
 
 // Keys [lo, hi) that query position p sees, given the sequence's lengths.
+// Sequences hold fewer than 2^30 rows, so positions and their sums fit 32 bits.
 struct KeyRange {
-    int64_t lo, hi;
+    int lo, hi;
 };
-__device__ __forceinline__ KeyRange key_range(const AttnArgs& a, int64_t p, int64_t Lq, int64_t Lk) {
+__device__ __forceinline__ KeyRange key_range(const AttnArgs& a, int p, int Lq, int Lk) {
     KeyRange r{0, Lk};
     if (p >= Lq) {
         r.hi = 0;
     } else if (a.causal) {
-        const int64_t last = p + Lk - Lq;  // < Lk
+        const int last = p + (Lk - Lq);  // < Lk
         r.hi = last + 1;
         if (a.window) r.lo = last + 1 - a.window;
         if (r.hi < 0) r.hi = 0;
@@ -197,10 +227,32 @@ __device__ __forceinline__ KeyRange key_range(const AttnArgs& a, int64_t p, int6
     return r;
 }
 
-__device__ __forceinline__ int64_t valid_length(const int32_t* len, int b, int64_t most) {
+__device__ __forceinline__ int valid_length(const int32_t* len, int b, int most) {
     if (!len) return most;
-    const int64_t v = len[b];
+    const int v = len[b];
     return v < 0 ? 0 : v > most ? most : v;
+}
+
+// The keys that the rows [first, first + n) of one key/value head see between
+// them, [begin, end), and those that all of them see, [all_lo, all_hi).
+struct RowsRange {
+    int begin, end, all_lo, all_hi;
+};
+__device__ __forceinline__ RowsRange rows_range(const AttnArgs& a, int first, int n, int rows, int Lq, int Lk) {
+    const int p0 = first / a.G, p1 = (first + n <= rows ? first + n - 1 : rows - 1) / a.G;
+    RowsRange r;
+    r.begin = key_range(a, p0, Lq, Lk).lo;
+    r.end = p0 < Lq ? key_range(a, p1 < Lq ? p1 : Lq - 1, Lq, Lk).hi : 0;
+    r.all_lo = key_range(a, p1, Lq, Lk).lo;
+    r.all_hi = first + n <= rows && p1 < Lq ? key_range(a, p0, Lq, Lk).hi : 0;
+    return r;
+}
+
+// Is key0 + (the key of result element i) one of [lo, hi)?  One subtraction
+// and one unsigned comparison an element.
+__device__ __forceinline__ bool sees(int key0, int i, const KeyRange& r) {
+    const uint32_t k = (uint32_t)(key0 + 4 * (lane_id() >> 5) - r.lo) + (uint32_t)(8 * (i >> 2) + (i & 3));
+    return k < (uint32_t)(r.hi - r.lo);
 }
 
 // Workgroups are dealt to the 8 XCDs in turn; give each XCD one contiguous

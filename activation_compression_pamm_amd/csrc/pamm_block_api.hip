@@ -15,6 +15,7 @@
 namespace {
 
 constexpr int64_t kMaxSize = 2147483647LL;
+constexpr int64_t kMaxSequence = ((int64_t)1 << 30) - 512;  // positions and their sums fit 32 bits
 constexpr int64_t kMaxSpan = (int64_t)1 << 40;  // elements; far beyond any device's memory
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -40,8 +41,8 @@ int64_t mul(int64_t a, int64_t b) {
 int attention_sizes(const pamm_attention_t* a) {
     if (!a) return PAMM_ERR_NULL;
     if (!dtype_ok(a->dtype)) return PAMM_ERR_DTYPE;
-    if (a->batch < 0 || a->batch > kMaxSize || a->seq_q < 0 || a->seq_q > kMaxSize || a->seq_k < 0 ||
-        a->seq_k > kMaxSize || a->heads < 1 || a->heads > kMaxSize || a->heads_kv < 1 || a->heads_kv > a->heads ||
+    if (a->batch < 0 || a->batch > kMaxSize || a->seq_q < 0 || a->seq_q > kMaxSequence || a->seq_k < 0 ||
+        a->seq_k > kMaxSequence || a->heads < 1 || a->heads > kMaxSize || a->heads_kv < 1 || a->heads_kv > a->heads ||
         a->heads % a->heads_kv != 0 || a->head_dim < 1 || a->head_dim > PAMM_MAX_HEAD_DIM)
         return PAMM_ERR_SHAPE;
     if (a->head_dim % per16(a->dtype) != 0) return PAMM_ERR_ALIGN;
@@ -49,7 +50,7 @@ int attention_sizes(const pamm_attention_t* a) {
         return PAMM_ERR_VALUE;
     // rows of one key/value head, elements of lse, workgroups of either kernel
     const int64_t rows = mul(a->seq_q, a->heads / a->heads_kv);
-    if (rows > kMaxSize || mul(mul(a->batch, a->heads), a->seq_q) > kMaxSpan) return PAMM_ERR_SHAPE;
+    if (rows > kMaxSequence || mul(mul(a->batch, a->heads), a->seq_q) > kMaxSpan) return PAMM_ERR_SHAPE;
     const int64_t heads = mul(a->batch, a->heads_kv);
     if (mul(heads, 64) > kMaxSize || mul(heads, (rows + 127) / 128) > kMaxSize / 64 ||
         mul(heads, (a->seq_k + 127) / 128) > kMaxSize || mul(mul(a->batch, a->heads), a->seq_q) > 4 * kMaxSize)

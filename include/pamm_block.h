@@ -81,8 +81,8 @@ size_t pamm_attention_workspace_size(const pamm_attention_t *a_host);
  *
  * Errors: PAMM_ERR_NULL, _DTYPE, _SHAPE (sizes < 0, heads not a multiple of
  * heads_kv, head_dim out of range, a stride that is negative or spans 2^40
- * elements, a batch or sequence beyond 2^31 - 1, more workgroups than a grid
- * holds), _VALUE (scale not finite, causal not 0 or 1, window < 0, window > 0
+ * elements, seq_q, seq_k or seq_q * heads / heads_kv beyond
+ * 2^30 - 512, more workgroups than a grid holds), _VALUE (scale not finite, causal not 0 or 1, window < 0, window > 0
  * without causal), _ALIGN, _UNSUPPORTED (64 rows of one tensor span 2 GiB or
  * more), _WORKSPACE.  With no sequence or no query it does nothing.
  */
