@@ -78,17 +78,14 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_kernel(A
     __shared__ __attribute__((aligned(16))) char lds[2][2][BK * T::PITCH];
     const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
 
-    int64_t id = xcd_order(blockIdx.x, gridDim.x);
-    const int split = (int)(id % a.nsplit);
-    id /= a.nsplit;
-    // the last rows see the most keys: they start first
-    const int64_t tile = row_tiles - 1 - id % row_tiles;
-    const int bh = (int)(id / row_tiles), b = bh / a.Hkv, hk = bh % a.Hkv;
+    const WorkItem w = work_item(blockIdx.x, (int64_t)a.B * a.Hkv, row_tiles * a.nsplit, a.causal);
+    const int split = w.item % a.nsplit, b = w.head / a.Hkv, hk = w.head % a.Hkv;
+    const int tile = (int)row_tiles - 1 - w.item / a.nsplit;  // the last rows see the most keys: they start first
     const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
     const int rows = a.Sq * a.G;
 
     // what this lane's row, this wave's rows and this workgroup's rows see
-    const int r0 = (int)tile * 128, w0 = r0 + wave * 32, row = w0 + (l & 31);
+    const int r0 = tile * 128, w0 = r0 + wave * 32, row = w0 + (l & 31);
     const int pos = row / a.G, head = hk * a.G + row % a.G;
     const bool live = row < rows;
     KeyRange mine = key_range(a, live ? pos : Lq, Lq, Lk);
@@ -133,6 +130,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_kernel(A
             kc.fetch(kbase + (t + 1) * BK * a.k.ss, (int)a.k.ss, Lk - (t + 1) * BK, a.D, tid);
             vc.fetch(vbase + (t + 1) * BK * a.v.ss, (int)a.v.ss, Lk - (t + 1) * BK, a.D, tid);
         }
+        const int rb = opaque(row_base<DT, ND>()), tb = opaque(trans_base<DT, ND>());
 #pragma unroll
         for (int kb = 0; kb < BK / 32; ++kb) {
             const int key0 = t * BK + kb * 32;
@@ -140,13 +138,13 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_kernel(A
             f32x16 s{};
 #pragma unroll
             for (int i = 0; i < T::NS; ++i)
-                s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], kb * 32, i), qf[i], s);
+                s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], kb * 32, rb, i), qf[i], s);
             settle<DT>(s);
             if (key0 < wr.all_lo || key0 + 32 > wr.all_hi) mask_block(s, key0, mine);
             softmax_update<ND>(s, c, st, acc);
             Packed<DT> p;
             p.set(s);
-            trans_product<DT, ND>(lds[cur][1], kb * 32, p, acc);
+            trans_product<DT, ND>(lds[cur][1], kb * 32, tb, p, acc);
         }
         if (more) {
             kc.put(lds[cur ^ 1][0], tid);
@@ -189,10 +187,8 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_few_kern
     __shared__ float stat[4][2][32];
     const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
 
-    int64_t id = xcd_order(blockIdx.x, gridDim.x);
-    const int split = (int)(id % a.nsplit);
-    id /= a.nsplit;
-    const int b = (int)(id / a.Hkv), hk = (int)(id % a.Hkv);
+    const WorkItem w = work_item(blockIdx.x, (int64_t)a.B * a.Hkv, a.nsplit, false);
+    const int split = w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;
     const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
     const int rows = a.Sq * a.G;
     const int row = l & 31, pos = row / a.G, head = hk * a.G + row % a.G;
@@ -247,7 +243,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_few_kern
         softmax_update<ND>(s, c, st, acc);
         Packed<DT> p;
         p.set(s);
-        trans_product<DT, ND>(vt, 0, p, acc);
+        trans_product<DT, ND>(vt, 0, opaque(trans_base<DT, ND>()), p, acc);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 

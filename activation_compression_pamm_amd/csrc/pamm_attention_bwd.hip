@@ -34,12 +34,11 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
     __shared__ __attribute__((aligned(16))) char lds[2][2][BK * T::PITCH];
     const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
 
-    const int64_t id = xcd_order(blockIdx.x, gridDim.x);
-    const int64_t tile = row_tiles - 1 - id % row_tiles;
-    const int bh = (int)(id / row_tiles), b = bh / a.Hkv, hk = bh % a.Hkv;
+    const WorkItem w = work_item(blockIdx.x, (int64_t)a.B * a.Hkv, row_tiles, a.causal);
+    const int tile = (int)row_tiles - 1 - w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;
     const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
     const int rows = a.Sq * a.G;
-    const int r0 = (int)tile * 128, w0 = r0 + wave * 32, row = w0 + (l & 31);
+    const int r0 = tile * 128, w0 = r0 + wave * 32, row = w0 + (l & 31);
     const int pos = row / a.G, head = hk * a.G + row % a.G;
     const bool live = row < rows;
     KeyRange mine = key_range(a, live ? pos : Lq, Lq, Lk);
@@ -86,6 +85,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
             kc.fetch(kbase + (t + 1) * BK * a.k.ss, (int)a.k.ss, Lk - (t + 1) * BK, a.D, tid);
             vc.fetch(vbase + (t + 1) * BK * a.v.ss, (int)a.v.ss, Lk - (t + 1) * BK, a.D, tid);
         }
+        const int rb = opaque(row_base<DT, ND>()), tb = opaque(trans_base<DT, ND>());
 #pragma unroll
         for (int kb = 0; kb < BK / 32; ++kb) {
             const int key0 = t * BK + kb * 32;
@@ -93,8 +93,8 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
             f32x16 s{}, dp{};
 #pragma unroll
             for (int i = 0; i < T::NS; ++i) {
-                s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], kb * 32, i), qf[i], s);
-                dp = mma_step<DT>(row_operand<DT, ND>(lds[cur][1], kb * 32, i), dof[i], dp);
+                s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], kb * 32, rb, i), qf[i], s);
+                dp = mma_step<DT>(row_operand<DT, ND>(lds[cur][1], kb * 32, rb, i), dof[i], dp);
             }
             settle<DT>(s);
             settle<DT>(dp);
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
             }
             Packed<DT> ds;
             ds.set(s);
-            trans_product<DT, ND>(lds[cur][0], kb * 32, ds, acc);
+            trans_product<DT, ND>(lds[cur][0], kb * 32, tb, ds, acc);
         }
         if (more) {
             kc.put(lds[cur ^ 1][0], tid);
@@ -133,9 +133,8 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kern
     __shared__ __attribute__((aligned(16))) float rowstat[2][2][BQ];
     const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
 
-    const int64_t id = xcd_order(blockIdx.x, gridDim.x);
-    const int tile = (int)(id % key_tiles);  // the first keys are seen by the most queries
-    const int bh = (int)(id / key_tiles), b = bh / a.Hkv, hk = bh % a.Hkv;
+    const WorkItem w = work_item(blockIdx.x, (int64_t)a.B * a.Hkv, key_tiles, a.causal);
+    const int tile = w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;  // the first keys are seen by the most queries
     const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
     const int off = Lk - Lq;
     const int b0 = tile * 128, w0 = b0 + wave * 32, key = w0 + (l & 31);
@@ -186,16 +185,14 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kern
         oc.fetch(a.dout.p + b * a.dout.sb + head * a.dout.sh + q0 * a.dout.ss, (int)a.dout.ss, Lq - q0, a.D, tid);
         const int r = tid % BQ;
         const int64_t at = ((int64_t)b * a.H + head) * a.Sq + q0 + r;
-        if (tid < BQ) {
-            stat = q0 + r < Lq ? a.lse[at] * kLog2e : INFINITY;
-            if (stat == -INFINITY) stat = INFINITY;
-        } else if (tid < 2 * BQ) {
-            stat = q0 + r < Lq ? a.delta[at] : 0.0f;
-        }
+        stat = 0.0f;
+        if (tid < 2 * BQ && q0 + r < Lq) stat = tid < BQ ? a.lse[at] : a.delta[at];
     };
     auto put = [&](int buf) {
         qc.put(lds[buf][0], tid);
         oc.put(lds[buf][1], tid);
+        // lse in log2 units; a row that saw nothing has probabilities 2^(-infinity) = 0
+        if (tid < BQ) stat = stat == -INFINITY ? INFINITY : stat * kLog2e;
         if (tid < 2 * BQ) rowstat[buf][tid / BQ][tid % BQ] = stat;
     };
     int t = n0, g = 0;
@@ -211,10 +208,12 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kern
         if (i + 1 < n) fetch(gn, tn);
         const int q0 = t * BQ;
         if (q0 < wp1 && q0 + BQ > wp0) {
+            const int rb = opaque(row_base<DT, ND>()), tb = opaque(trans_base<DT, ND>());
             f32x16 s{};
 #pragma unroll
             for (int x = 0; x < T::NS; ++x)
-                s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], 0, x), row_operand<DT, ND>(ldk, wave * 32, x), s);
+                s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], 0, rb, x),
+                                 row_operand<DT, ND>(ldk, wave * 32, rb, x), s);
             settle<DT>(s);
             const int quad = 4 * (l >> 5);
 #pragma unroll
@@ -238,10 +237,10 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kern
             }
             Packed<DT> pk;
             pk.set(s);
-            trans_product<DT, ND>(lds[cur][1], 0, pk, dv);
+            trans_product<DT, ND>(lds[cur][1], 0, tb, pk, dv);
             f32x16 dp{};
 #pragma unroll
-            for (int x = 0; x < T::NS; ++x) dp = mma_step<DT>(row_operand<DT, ND>(lds[cur][1], 0, x), vf[x], dp);
+            for (int x = 0; x < T::NS; ++x) dp = mma_step<DT>(row_operand<DT, ND>(lds[cur][1], 0, rb, x), vf[x], dp);
             settle<DT>(dp);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -256,7 +255,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kern
                     if (!sees(q0, e, seen)) s[e] = 0.0f;
             }
             pk.set(s);
-            trans_product<DT, ND>(lds[cur][0], 0, pk, dk);
+            trans_product<DT, ND>(lds[cur][0], 0, tb, pk, dk);
         }
         if (i + 1 < n) put(cur ^ 1);
         __syncthreads();

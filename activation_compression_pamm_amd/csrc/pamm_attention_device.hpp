@@ -36,7 +36,7 @@ struct Tile {
     static constexpr int PITCH = (ND <= 2 ? 64 : 128) * ES;
     static constexpr int NS = ND * ES;        // 32-byte contraction steps of a row
     static constexpr int CPR = 2 * NS;        // 16-byte groups of a row that are used
-    __device__ static __forceinline__ int key(int r) {
+    __host__ __device__ static constexpr int key(int r) {
         if constexpr (PITCH == 128) {
             const int r2 = r >> 1;
             return ((r2 & 1) << 2) | ((r2 >> 1) & 3);
@@ -46,6 +46,32 @@ struct Tile {
     }
     __device__ static __forceinline__ int offset(int r, int c) { return r * PITCH + ((c ^ key(r)) << 4); }
 };
+
+// Lane-dependent parts of LDS addresses.  The group index only ever meets the
+// key by exclusive or, so the address of group c + 2 s is base ^ (s << 5).
+// Hidden from the compiler once an iteration, the base stays one register and
+// each address costs one instruction; left alone, all of them are kept in
+// registers over the loop, and what does not fit is spilled.
+__device__ __forceinline__ int opaque(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+// Row operand: row l % 32, group l / 32.
+template <int DT, int ND>
+__device__ __forceinline__ int row_base() {
+    const int l = lane_id();
+    return Tile<DT, ND>::offset(l & 31, l >> 5);
+}
+// Transposed bf16 operand: rows 4 (l / 32) + (l % 16) / 4, and 8 more (the key
+// of row + 8 is the key of row with one bit flipped).
+template <int DT, int ND>
+__device__ __forceinline__ int trans_base() {
+    const int l = lane_id();
+    if constexpr (DT == DT_BF16)
+        return Tile<DT, ND>::offset(4 * (l >> 5) + ((l & 15) >> 2), ((l >> 4) & 1) * 2 + ((l & 3) >> 1)) + (l & 1) * 8;
+    else
+        return 0;
+}
 
 // One 32 x 32 product step; a and b are 16 bytes of A and B.
 template <int DT>
@@ -95,27 +121,26 @@ template <> struct Packed<DT_F32> {
 // bf16 reads its operand with the transposing LDS load: the 16 lanes of a
 // group point at four rows of 32 bytes and each gets one column of the four.
 template <int DT, int ND>
-__device__ __forceinline__ void trans_product(const char* tile, int r0, const Packed<DT>& b, f32x16* acc) {
+__device__ __forceinline__ void trans_product(const char* tile, int r0, int base, const Packed<DT>& b, f32x16* acc) {
     using T = Tile<DT, ND>;
-    const int l = lane_id(), h = l >> 5;
     if constexpr (DT == DT_BF16) {
-        const int row = 4 * h + ((l & 15) >> 2);
-        const int c = ((l >> 4) & 1) * 2 + ((l & 3) >> 1), sub = (l & 1) * 8;
+        constexpr int flip = (T::key(8) ^ T::key(0)) << 4;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
             for (int db = 0; db < ND; ++db) {
                 typedef __attribute__((address_space(3))) s16x4* lds_s4;
-                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (lds_s4)(tile + (r0 + 16 * t) * T::PITCH + T::offset(row, 4 * db + c) + sub));
-                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (lds_s4)(tile + (r0 + 16 * t) * T::PITCH + T::offset(row + 8, 4 * db + c) + sub));
+                const char* at = tile + (r0 + 16 * t) * T::PITCH;
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(at + (base ^ (db << 6))));
+                const s16x4 hi =
+                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(at + 8 * T::PITCH + (base ^ (db << 6) ^ flip)));
                 typedef short s16x8 __attribute__((ext_vector_type(8)));
                 const s16x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
                 acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), b.v[t], acc[db], 0, 0, 0);
             }
         }
     } else {
+        const int l = lane_id(), h = l >> 5;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int row = r0 + 8 * (i >> 2) + 4 * h + (i & 3);
@@ -129,11 +154,10 @@ __device__ __forceinline__ void trans_product(const char* tile, int r0, const Pa
     }
 }
 
-// Row operand of step s: 16 bytes of row r0 + l % 32.
+// Row operand of step s: 16 bytes of row r0 + l % 32 (r0 a multiple of 32).
 template <int DT, int ND>
-__device__ __forceinline__ uint4 row_operand(const char* tile, int r0, int s) {
-    const int l = lane_id();
-    return *reinterpret_cast<const uint4*>(tile + Tile<DT, ND>::offset(r0 + (l & 31), 2 * s + (l >> 5)));
+__device__ __forceinline__ uint4 row_operand(const char* tile, int r0, int base, int s) {
+    return *reinterpret_cast<const uint4*>(tile + r0 * Tile<DT, ND>::PITCH + (base ^ (s << 5)));
 }
 
 // This lane's 16-byte groups of one global row (zero where !ok or past D).
@@ -255,11 +279,30 @@ __device__ __forceinline__ bool sees(int key0, int i, const KeyRange& r) {
     return k < (uint32_t)(r.hi - r.lo);
 }
 
-// Workgroups are dealt to the 8 XCDs in turn; give each XCD one contiguous
-// piece of the work list, so that the workgroups that share keys share an L2.
-__device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
-    const int64_t x = id % 8, s = id / 8, q = total / 8, r = total % 8;
-    return x * q + (x < r ? x : r) + s;
+// Workgroup id -> (head of the batch, item of the head).  Workgroups are dealt
+// to the 8 XCDs in turn, each with an L2 of its own: a head's items stay on one
+// XCD where the heads divide evenly.  Items of falling cost (causal masks) are
+// started in that order over all heads of the XCD, so that the longest do not
+// start last; items of equal cost head after head, which shares the L2 best.
+struct WorkItem {
+    int head, item;
+};
+__device__ __forceinline__ WorkItem work_item(int64_t id, int64_t heads, int64_t items, bool falling) {
+    WorkItem w;
+    if (heads % 8 == 0) {
+        const int64_t x = id % 8, s = id / 8, n = heads / 8;
+        w.item = (int)(falling ? s / n : s % items);
+        w.head = (int)(x + 8 * (falling ? s % n : s / items));
+    } else if (falling) {
+        w.item = (int)(id / heads);
+        w.head = (int)(id % heads);
+    } else {
+        const int64_t total = heads * items, x = id % 8, s = id / 8, q = total / 8, r = total % 8;
+        const int64_t at = x * q + (x < r ? x : r) + s;
+        w.item = (int)(at % items);
+        w.head = (int)(at / items);
+    }
+    return w;
 }
 
 // Writes ND blocks of 32 x 32 results that are transposed rows: this lane's
