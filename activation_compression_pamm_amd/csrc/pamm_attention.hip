@@ -72,15 +72,15 @@ __device__ __forceinline__ float score_factor(float scale) { return fmaxf(fabsf(
 // buffers hold: while one is used, the next tile travels through registers
 // into the other.
 template <int DT, int ND>
-__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_kernel(AttnArgs a, int64_t row_tiles) {
+__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_kernel(AttnArgs a, int row_tiles) {
     using T = Tile<DT, ND>;
     constexpr int BK = DT == DT_BF16 ? 64 : 32;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BK * T::PITCH];
     const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
 
-    const WorkItem w = work_item(blockIdx.x, (int64_t)a.B * a.Hkv, row_tiles * a.nsplit, a.causal);
+    const WorkItem w = work_item(blockIdx.x, a.B * a.Hkv, row_tiles * a.nsplit, a.causal);
     const int split = w.item % a.nsplit, b = w.head / a.Hkv, hk = w.head % a.Hkv;
-    const int tile = (int)row_tiles - 1 - w.item / a.nsplit;  // the last rows see the most keys: they start first
+    const int tile = row_tiles - 1 - w.item / a.nsplit;  // the last rows see the most keys: they start first
     const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
     const int rows = a.Sq * a.G;
 
@@ -108,6 +108,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_kernel(A
     if (a.scale < 0.0f)
 #pragma unroll
         for (int s = 0; s < T::NS; ++s) qf[s] = negate16<DT>(qf[s]);
+    arrived(qf);
     const float c = score_factor(a.scale);
 
     f32x16 acc[ND];
@@ -187,7 +188,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_few_kern
     __shared__ float stat[4][2][32];
     const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
 
-    const WorkItem w = work_item(blockIdx.x, (int64_t)a.B * a.Hkv, a.nsplit, false);
+    const WorkItem w = work_item(blockIdx.x, a.B * a.Hkv, a.nsplit, false);
     const int split = w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;
     const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
     const int rows = a.Sq * a.G;
@@ -209,6 +210,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_few_kern
     if (a.scale < 0.0f)
 #pragma unroll
         for (int s = 0; s < T::NS; ++s) qf[s] = negate16<DT>(qf[s]);
+    arrived(qf);
     const float c = score_factor(a.scale);
     f32x16 acc[ND];
 #pragma unroll
@@ -354,7 +356,7 @@ static void launch_attention(const AttnArgs& a, hipStream_t st) {
     } else {
         const int64_t tiles = (rows + 127) / 128;
         const dim3 grid((unsigned)((int64_t)a.B * a.Hkv * tiles * a.nsplit));
-        hipLaunchKernelGGL((attention_kernel<DT, ND>), grid, dim3(256), 0, st, a, tiles);
+        hipLaunchKernelGGL((attention_kernel<DT, ND>), grid, dim3(256), 0, st, a, (int)tiles);
     }
     if (a.nsplit > 1) {
         const dim3 grid((unsigned)(((int64_t)a.B * a.H * a.Sq + 3) / 4));

@@ -28,14 +28,14 @@ __device__ __forceinline__ float dot16(const uint4& x, const uint4& y) {
 
 // dq.  Laid out as the forward pass: transposed scores, a lane owns a query.
 template <int DT, int ND>
-__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kernel(AttnArgs a, int64_t row_tiles) {
+__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kernel(AttnArgs a, int row_tiles) {
     using T = Tile<DT, ND>;
     constexpr int BK = DT == DT_BF16 ? 64 : 32;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BK * T::PITCH];
     const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
 
-    const WorkItem w = work_item(blockIdx.x, (int64_t)a.B * a.Hkv, row_tiles, a.causal);
-    const int tile = (int)row_tiles - 1 - w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;
+    const WorkItem w = work_item(blockIdx.x, a.B * a.Hkv, row_tiles, a.causal);
+    const int tile = row_tiles - 1 - w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;
     const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
     const int rows = a.Sq * a.G;
     const int r0 = tile * 128, w0 = r0 + wave * 32, row = w0 + (l & 31);
@@ -62,10 +62,13 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
     if (a.scale < 0.0f)
 #pragma unroll
         for (int s = 0; s < T::NS; ++s) qf[s] = negate16<DT>(qf[s]);
+    arrived(qf);
+    arrived(dof);
     const float c = score_factor(a.scale);
     // a row that saw nothing (lse = -infinity) has probabilities 2^(-infinity) = 0
     float lse2 = live ? a.lse[at] * kLog2e : 0.0f;
     if (lse2 == -INFINITY) lse2 = INFINITY;
+    asm volatile("" : "+v"(lse2));
 
     f32x16 acc[ND];
 #pragma unroll
@@ -125,7 +128,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
 // registers as an operand, K in LDS: both in registers beside 128 sums a lane
 // would leave one wave a SIMD.
 template <int DT, int ND>
-__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kernel(AttnArgs a, int64_t key_tiles) {
+__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kernel(AttnArgs a, int key_tiles) {
     using T = Tile<DT, ND>;
     constexpr int BQ = 32;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BQ * T::PITCH];
@@ -133,7 +136,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kern
     __shared__ __attribute__((aligned(16))) float rowstat[2][2][BQ];
     const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
 
-    const WorkItem w = work_item(blockIdx.x, (int64_t)a.B * a.Hkv, key_tiles, a.causal);
+    const WorkItem w = work_item(blockIdx.x, a.B * a.Hkv, key_tiles, a.causal);
     const int tile = w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;  // the first keys are seen by the most queries
     const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
     const int off = Lk - Lq;
@@ -171,6 +174,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kern
         kc.fetch(a.k.p + b * a.k.sb + (b0 + 64 * i) * a.k.ss + hk * a.k.sh, (int)a.k.ss, Lk - b0 - 64 * i, a.D, tid);
         kc.put(ldk + 64 * i * T::PITCH, tid);
     }
+    arrived(vf);
     const float c = score_factor(a.scale) * (a.scale < 0.0f ? -1.0f : 1.0f);
 
     f32x16 dk[ND], dv[ND];
@@ -278,10 +282,10 @@ static void launch_backward(const AttnArgs& a, hipStream_t st) {
     const int64_t tiles = ((int64_t)a.Sq * a.G + 127) / 128, key_tiles = ((int64_t)a.Sk + 127) / 128;
     const int64_t heads = (int64_t)a.B * a.Hkv;
     if (tiles > 0)
-        hipLaunchKernelGGL((attention_dq_kernel<DT, ND>), dim3((unsigned)(heads * tiles)), dim3(256), 0, st, a, tiles);
+        hipLaunchKernelGGL((attention_dq_kernel<DT, ND>), dim3((unsigned)(heads * tiles)), dim3(256), 0, st, a, (int)tiles);
     if (key_tiles > 0)
         hipLaunchKernelGGL((attention_dkv_kernel<DT, ND>), dim3((unsigned)(heads * key_tiles)), dim3(256), 0, st, a,
-                           key_tiles);
+                           (int)key_tiles);
 }
 
 hipError_t run_attention_backward(const AttnArgs& a, int dtype, hipStream_t st) {

@@ -172,6 +172,15 @@ __device__ __forceinline__ void load_row_operand(uint4* f, const char* row, bool
     }
 }
 
+// Waits for operands loaded before a loop.  Left to the compiler, the wait
+// stands at their first use inside the loop, where it also waits for the next
+// tile's loads, every time round.
+template <int N>
+__device__ __forceinline__ void arrived(uint4 (&f)[N]) {
+#pragma unroll
+    for (int s = 0; s < N; ++s) asm volatile("" : "+v"(f[s].x), "+v"(f[s].y), "+v"(f[s].z), "+v"(f[s].w));
+}
+
 // Flip the sign of every element (exact).
 template <int DT>
 __device__ __forceinline__ uint4 negate16(uint4 v) {
@@ -287,20 +296,23 @@ __device__ __forceinline__ bool sees(int key0, int i, const KeyRange& r) {
 struct WorkItem {
     int head, item;
 };
-__device__ __forceinline__ WorkItem work_item(int64_t id, int64_t heads, int64_t items, bool falling) {
+__device__ __forceinline__ WorkItem work_item(uint32_t id, uint32_t heads, uint32_t items, bool falling) {
     WorkItem w;
     if (heads % 8 == 0) {
-        const int64_t x = id % 8, s = id / 8, n = heads / 8;
-        w.item = (int)(falling ? s / n : s % items);
-        w.head = (int)(x + 8 * (falling ? s % n : s / items));
-    } else if (falling) {
-        w.item = (int)(id / heads);
-        w.head = (int)(id % heads);
+        const uint32_t x = id % 8, s = id / 8, n = heads / 8, d = falling ? n : items;
+        const uint32_t hi = s / d, lo = s - hi * d;
+        w.item = (int)(falling ? hi : lo);
+        w.head = (int)(x + 8 * (falling ? lo : hi));
     } else {
-        const int64_t total = heads * items, x = id % 8, s = id / 8, q = total / 8, r = total % 8;
-        const int64_t at = x * q + (x < r ? x : r) + s;
-        w.item = (int)(at % items);
-        w.head = (int)(at / items);
+        uint32_t at = id, d = heads;
+        if (!falling) {
+            const uint32_t total = heads * items, x = id % 8, q = total / 8, r = total % 8;
+            at = x * q + (x < r ? x : r) + id / 8;
+            d = items;
+        }
+        const uint32_t hi = at / d, lo = at - hi * d;
+        w.item = (int)(falling ? hi : lo);
+        w.head = (int)(falling ? lo : hi);
     }
     return w;
 }
