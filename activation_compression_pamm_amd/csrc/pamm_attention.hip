@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_kernel(A
     using T = Tile<DT, ND>;
     constexpr int BK = DT == DT_BF16 ? 64 : 32;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BK * T::PITCH];
-    const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, l = tid & 63, wave = wave_id();
 
     const WorkItem w = work_item(blockIdx.x, a.B * a.Hkv, row_tiles * a.nsplit, a.causal);
     const int split = w.item % a.nsplit, b = w.head / a.Hkv, hk = w.head % a.Hkv;
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_few_kern
     constexpr int SH = 4 * VT > 32 * OP * 4 ? 4 * VT : 32 * OP * 4;
     __shared__ __attribute__((aligned(16))) char lds[SH];
     __shared__ float stat[4][2][32];
-    const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, l = tid & 63, wave = wave_id();
 
     const WorkItem w = work_item(blockIdx.x, a.B * a.Hkv, a.nsplit, false);
     const int split = w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;

@@ -5,6 +5,10 @@
 //   dv_j = sum_i P_ij do_i,  dk_j = scale sum_i dS_ij q_i,
 //   dq_i = scale sum_j dS_ij k_j
 //
+// The products that form s and <do, v> start from -lse / scale and -delta, so
+// what comes out needs one multiplication and an exponential to be P, and one
+// more multiplication to be dS.
+//
 // Two kernels, each with its sums in registers and in a fixed order: one owns
 // queries and runs over keys (dq, and delta on the way), one owns keys and
 // runs over the queries of every head that shares them (dk, dv).  Forming P
@@ -15,6 +19,13 @@
 namespace pamm {
 
 __device__ __forceinline__ float score_factor(float scale) { return fmaxf(fabsf(scale) * kLog2e, 1e-36f); }
+
+// What a score starts from: -lse in units of the raw products, so that
+// 2^(c (start + <q, k>)) is the probability.  A row that saw nothing (lse =
+// -infinity) starts from what makes its probabilities 2^(-infinity) = 0.
+__device__ __forceinline__ float start_of(float lse, float c) {
+    return lse == -INFINITY ? (c < 0.0f ? INFINITY : -INFINITY) : -lse * kLog2e / c;
+}
 
 template <int DT>
 __device__ __forceinline__ float dot16(const uint4& x, const uint4& y) {
@@ -32,7 +43,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
     using T = Tile<DT, ND>;
     constexpr int BK = DT == DT_BF16 ? 64 : 32;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BK * T::PITCH];
-    const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, l = tid & 63, wave = wave_id();
 
     const WorkItem w = work_item(blockIdx.x, a.B * a.Hkv, row_tiles, a.causal);
     const int tile = row_tiles - 1 - w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;
@@ -65,10 +76,8 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
     arrived(qf);
     arrived(dof);
     const float c = score_factor(a.scale);
-    // a row that saw nothing (lse = -infinity) has probabilities 2^(-infinity) = 0
-    float lse2 = live ? a.lse[at] * kLog2e : 0.0f;
-    if (lse2 == -INFINITY) lse2 = INFINITY;
-    asm volatile("" : "+v"(lse2));
+    float start = start_of(live ? a.lse[at] : 0.0f, c);
+    asm volatile("" : "+v"(start));  // as for the operands
 
     f32x16 acc[ND];
 #pragma unroll
@@ -93,7 +102,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
         for (int kb = 0; kb < BK / 32; ++kb) {
             const int key0 = t * BK + kb * 32;
             if (key0 >= wr.end || key0 + 32 <= wr.begin) continue;
-            f32x16 s{}, dp{};
+            f32x16 s = splat(start), dp = splat(-delta);
 #pragma unroll
             for (int i = 0; i < T::NS; ++i) {
                 s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], kb * 32, rb, i), qf[i], s);
@@ -102,7 +111,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
             settle<DT>(s);
             settle<DT>(dp);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -lse2)) * (dp[i] - delta);
+            for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(s[i] * c) * dp[i];
             if (key0 < wr.all_lo || key0 + 32 > wr.all_hi) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -126,18 +135,24 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
 // dk and dv.  Scores as S = Q K^T: a lane owns a key.  Four waves of 32 keys
 // share tiles of 32 queries of one head, head after head.  V stays in
 // registers as an operand, K in LDS: both in registers beside 128 sums a lane
-// would leave one wave a SIMD.
+// would leave one wave a SIMD, and at the longest bf16 rows even V's last
+// 96 bytes are kept in LDS (spilled, their reload waited for the next tile's
+// loads every time round).  Where there are few key tiles and many queries,
+// the queries of a tile are cut into parts whose sums a second kernel joins.
 template <int DT, int ND>
-__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kernel(AttnArgs a, int key_tiles) {
+__global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void attention_dkv_kernel(AttnArgs a, int key_tiles) {
     using T = Tile<DT, ND>;
     constexpr int BQ = 32;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BQ * T::PITCH];
     __shared__ __attribute__((aligned(16))) char ldk[128 * T::PITCH];
+    constexpr int VL = DT == DT_BF16 && ND == 4 ? 3 : 0, VR = T::NS - VL;  // steps of V in LDS and in registers
+    __shared__ __attribute__((aligned(16))) char ldv[VL ? VL * 128 * 32 : 16];
     __shared__ __attribute__((aligned(16))) float rowstat[2][2][BQ];
-    const int tid = threadIdx.x, l = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, l = tid & 63, wave = wave_id();
 
-    const WorkItem w = work_item(blockIdx.x, a.B * a.Hkv, key_tiles, a.causal);
-    const int tile = w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;  // the first keys are seen by the most queries
+    const WorkItem w = work_item(blockIdx.x, a.B * a.Hkv, key_tiles * a.nsplit_kv, a.causal);
+    const int tile = w.item / a.nsplit_kv, part_id = w.item % a.nsplit_kv;  // the first keys are seen by the most queries
+    const int b = w.head / a.Hkv, hk = w.head % a.Hkv;
     const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
     const int off = Lk - Lq;
     const int b0 = tile * 128, w0 = b0 + wave * 32, key = w0 + (l & 31);
@@ -157,14 +172,19 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kern
     const int n0 = p0 / BQ;
     int n1 = (p1 + BQ - 1) / BQ;
     if (n1 < n0) n1 = n0;
-    const int64_t n = (int64_t)(n1 - n0) * a.G;
-    // positions that see this lane's key: [first, last)
-    int first = 0, last = key < Lk ? Lq : 0;
-    if (a.causal) {
-        if (key - off > first) first = key - off;
-        if (a.window && key - off + a.window < last) last = key - off + a.window;
-    }
-    if (last < first) last = first;
+    const int per_head = n1 - n0;  // heads x tiles fit 32 bits as rows do
+    const int per = (per_head * a.G + a.nsplit_kv - 1) / a.nsplit_kv, i0 = part_id * per;
+    const int i1 = i0 + per < per_head * a.G ? i0 + per : per_head * a.G;
+    // positions that see a key: [lo, hi)
+    auto positions = [&](int k) {
+        KeyRange r{0, k < Lk ? Lq : 0};
+        if (a.causal) {
+            if (k - off > 0) r.lo = k - off;
+            if (a.window && k - off + a.window < r.hi) r.hi = k - off + a.window;
+        }
+        if (r.hi < r.lo) r.hi = r.lo;
+        return r;
+    };
 
     uint4 vf[T::NS];
     load_row_operand<DT, ND>(vf, a.v.p + b * a.v.sb + key * a.v.ss + hk * a.v.sh, key < Lk, a.D);
@@ -175,6 +195,9 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kern
         kc.put(ldk + 64 * i * T::PITCH, tid);
     }
     arrived(vf);
+    char* vl = ldv + (wave * 32 + (l & 31)) * 32 + (l >> 5) * 16;
+#pragma unroll
+    for (int x = VR; x < T::NS; ++x) *reinterpret_cast<uint4*>(vl + (x - VR) * 128 * 32) = vf[x];
     const float c = score_factor(a.scale) * (a.scale < 0.0f ? -1.0f : 1.0f);
 
     f32x16 dk[ND], dv[ND];
@@ -195,46 +218,52 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kern
     auto put = [&](int buf) {
         qc.put(lds[buf][0], tid);
         oc.put(lds[buf][1], tid);
-        // lse in log2 units; a row that saw nothing has probabilities 2^(-infinity) = 0
-        if (tid < BQ) stat = stat == -INFINITY ? INFINITY : stat * kLog2e;
-        if (tid < 2 * BQ) rowstat[buf][tid / BQ][tid % BQ] = stat;
+        if (tid < 2 * BQ) rowstat[buf][tid / BQ][tid % BQ] = tid < BQ ? start_of(stat, c) : -stat;
     };
     int t = n0, g = 0;
-    if (n > 0) {
-        fetch(0, n0);
+    if (i0 < i1) {
+        g = i0 / per_head;
+        t = n0 + i0 % per_head;
+        fetch(g, t);
         put(0);
     }
     __syncthreads();
     int cur = 0;
-    for (int64_t i = 0; i < n; ++i, cur ^= 1) {
+    for (int i = i0; i < i1; ++i, cur ^= 1) {
         int tn = t + 1, gn = g;
         if (tn == n1) tn = n0, ++gn;
-        if (i + 1 < n) fetch(gn, tn);
+        if (i + 1 < i1) fetch(gn, tn);
         const int q0 = t * BQ;
         if (q0 < wp1 && q0 + BQ > wp0) {
             const int rb = opaque(row_base<DT, ND>()), tb = opaque(trans_base<DT, ND>());
-            f32x16 s{};
+            const int quad = 4 * (l >> 5);
+            // results' rows 8 y + quad + (0..3) of this tile's starts
+            auto starts = [&](int which) {
+                f32x16 d;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(&rowstat[cur][which][8 * y + quad]);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) d[4 * y + z] = v[z];
+                }
+                return d;
+            };
+            f32x16 s = starts(0);
 #pragma unroll
             for (int x = 0; x < T::NS; ++x)
                 s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], 0, rb, x),
                                  row_operand<DT, ND>(ldk, wave * 32, rb, x), s);
             settle<DT>(s);
-            const int quad = 4 * (l >> 5);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const float4 ls = *reinterpret_cast<const float4*>(&rowstat[cur][0][8 * y + quad]);
-                const float lv[4] = {ls.x, ls.y, ls.z, ls.w};
-#pragma unroll
-                for (int z = 0; z < 4; ++z) s[4 * y + z] = __builtin_amdgcn_exp2f(fmaf(s[4 * y + z], c, -lv[z]));
-            }
+            for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(s[e] * c);
             // some pair of this block is masked?
             bool part = w0 + 32 > Lk || q0 + BQ > Lq;
             if (a.causal) {
                 part = part || w0 + 31 > q0 + off;
                 if (a.window) part = part || w0 <= q0 + BQ - 1 + off - a.window;
             }
-            const KeyRange seen{first, last};
             if (part) {
+                const KeyRange seen = positions(opaque(key));
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     if (!sees(q0, e, seen)) s[e] = 0.0f;
@@ -242,18 +271,17 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kern
             Packed<DT> pk;
             pk.set(s);
             trans_product<DT, ND>(lds[cur][1], 0, tb, pk, dv);
-            f32x16 dp{};
+            f32x16 dp = starts(1);
 #pragma unroll
-            for (int x = 0; x < T::NS; ++x) dp = mma_step<DT>(row_operand<DT, ND>(lds[cur][1], 0, rb, x), vf[x], dp);
+            for (int x = 0; x < T::NS; ++x) {
+                const uint4 v = x < VR ? vf[x] : *reinterpret_cast<const uint4*>(vl + (x - VR) * 128 * 32);
+                dp = mma_step<DT>(row_operand<DT, ND>(lds[cur][1], 0, rb, x), v, dp);
+            }
             settle<DT>(dp);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const float4 de = *reinterpret_cast<const float4*>(&rowstat[cur][1][8 * y + quad]);
-                const float ev[4] = {de.x, de.y, de.z, de.w};
-#pragma unroll
-                for (int z = 0; z < 4; ++z) s[4 * y + z] *= dp[4 * y + z] - ev[z];
-            }
+            for (int e = 0; e < 16; ++e) s[e] *= dp[e];
             if (part) {  // P is 0 there; keep what is not finite out as well
+                const KeyRange seen = positions(opaque(key));
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     if (!sees(q0, e, seen)) s[e] = 0.0f;
@@ -261,7 +289,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kern
             pk.set(s);
             trans_product<DT, ND>(lds[cur][0], 0, tb, pk, dk);
         }
-        if (i + 1 < n) put(cur ^ 1);
+        if (i + 1 < i1) put(cur ^ 1);
         __syncthreads();
         t = tn;
         g = gn;
@@ -271,10 +299,56 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dkv_kern
         settle<DT>(dk[db]);
         settle<DT>(dv[db]);
     }
-    if (live) {
+    if (!live) return;
+    if (a.nsplit_kv > 1) {
+        const int64_t at = ((((int64_t)part_id * a.B + b) * a.Hkv + hk) * a.Sk + key) * a.D;
+        store_rows<DT_F32, ND>(reinterpret_cast<char*>(a.part_dk + at), dk, a.scale, a.D);
+        store_rows<DT_F32, ND>(reinterpret_cast<char*>(a.part_dv + at), dv, 1.0f, a.D);
+    } else {
         store_rows<DT, ND>(a.dk.p + b * a.dk.sb + key * a.dk.ss + hk * a.dk.sh, dk, a.scale, a.D);
         store_rows<DT, ND>(a.dv.p + b * a.dv.sb + key * a.dv.ss + hk * a.dv.sh, dv, 1.0f, a.D);
     }
+}
+
+// Adds the parts of dk and dv in order, four elements a thread.
+template <int DT>
+__global__ __launch_bounds__(256) void attention_dkv_join_kernel(AttnArgs a) {
+    const int64_t quads = (int64_t)a.B * a.Hkv * a.Sk * (a.D / 4), i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= 2 * quads) return;
+    const bool second = i >= quads;
+    const int64_t at = second ? i - quads : i, row = at / (a.D / 4);
+    const int e = (int)(at % (a.D / 4)) * 4;
+    const float* from = (second ? a.part_dv : a.part_dk) + at * 4;
+    float4 s = *reinterpret_cast<const float4*>(from);
+    for (int p = 1; p < a.nsplit_kv; ++p) {
+        const float4 x = *reinterpret_cast<const float4*>(from + p * quads * 4);
+        s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+    }
+    const int key = (int)(row % a.Sk);
+    const int64_t bh = row / a.Sk;
+    const HeadsArg& t = second ? a.dv : a.dk;
+    char* to = t.p + (bh / a.Hkv) * t.sb + key * t.ss + (bh % a.Hkv) * t.sh;
+    if constexpr (DT == DT_BF16) {
+        bf16x2 u, v;
+        u[0] = (__bf16)s.x, u[1] = (__bf16)s.y, v[0] = (__bf16)s.z, v[1] = (__bf16)s.w;
+        *reinterpret_cast<uint2*>(to + 2 * e) =
+            make_uint2(__builtin_bit_cast(uint32_t, u), __builtin_bit_cast(uint32_t, v));
+    } else {
+        *reinterpret_cast<float4*>(to + 4 * e) = s;
+    }
+}
+
+// A part costs a write and a read of fp32 sums for its keys, 16 n D bytes a
+// key, against 8 D Sq G operations: with 4096 rows or more a part, under 6% of
+// the time at the rates both reach (2 PFLOP/s products apart, see the figures
+// at run time), so only then are parts made, up to 8 workgroups a unit in all.
+int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int num_cus) {
+    const int64_t blocks = B * Hkv * ((Sk + 127) / 128), want = 8 * (int64_t)num_cus;
+    if (blocks == 0 || blocks >= want) return 1;
+    int64_t n = (want + blocks - 1) / blocks;
+    if (n > Sq * G / 4096) n = Sq * G / 4096;
+    if (n > 8) n = 8;
+    return n < 1 ? 1 : (int)n;
 }
 
 template <int DT, int ND>
@@ -282,10 +356,16 @@ static void launch_backward(const AttnArgs& a, hipStream_t st) {
     const int64_t tiles = ((int64_t)a.Sq * a.G + 127) / 128, key_tiles = ((int64_t)a.Sk + 127) / 128;
     const int64_t heads = (int64_t)a.B * a.Hkv;
     if (tiles > 0)
-        hipLaunchKernelGGL((attention_dq_kernel<DT, ND>), dim3((unsigned)(heads * tiles)), dim3(256), 0, st, a, (int)tiles);
+        hipLaunchKernelGGL((attention_dq_kernel<DT, ND>), dim3((unsigned)(heads * tiles)), dim3(256), 0, st, a,
+                           (int)tiles);
     if (key_tiles > 0)
-        hipLaunchKernelGGL((attention_dkv_kernel<DT, ND>), dim3((unsigned)(heads * key_tiles)), dim3(256), 0, st, a,
-                           (int)key_tiles);
+        hipLaunchKernelGGL((attention_dkv_kernel<DT, ND>), dim3((unsigned)(heads * key_tiles * a.nsplit_kv)), dim3(256),
+                           0, st, a, (int)key_tiles);
+    if (a.nsplit_kv > 1) {
+        const int64_t quads = heads * a.Sk * (a.D / 4);
+        hipLaunchKernelGGL((attention_dkv_join_kernel<DT>), dim3((unsigned)((2 * quads + 255) / 256)), dim3(256), 0, st,
+                           a);
+    }
 }
 
 hipError_t run_attention_backward(const AttnArgs& a, int dtype, hipStream_t st) {

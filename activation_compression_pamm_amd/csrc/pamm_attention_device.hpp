@@ -47,6 +47,10 @@ struct Tile {
     __device__ static __forceinline__ int offset(int r, int c) { return r * PITCH + ((c ^ key(r)) << 4); }
 };
 
+// The wave's number as a value the compiler knows to be the same in all lanes:
+// what follows from it stays in scalar registers and branches.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // Lane-dependent parts of LDS addresses.  The group index only ever meets the
 // key by exclusive or, so the address of group c + 2 s is base ^ (s << 5).
 // Hidden from the compiler once an iteration, the base stays one register and
@@ -172,6 +176,14 @@ __device__ __forceinline__ void load_row_operand(uint4* f, const char* row, bool
     }
 }
 
+// A result that starts from v instead of 0.
+__device__ __forceinline__ f32x16 splat(float v) {
+    f32x16 d;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) d[i] = v;
+    return d;
+}
+
 // Waits for operands loaded before a loop.  Left to the compiler, the wait
 // stands at their first use inside the loop, where it also waits for the next
 // tile's loads, every time round.
@@ -223,20 +235,38 @@ struct TileCopy {
     using T = Tile<DT, ND>;
     static constexpr int N = ROWS * T::CPR;
     static constexpr int PER = (N + NT - 1) / NT;
+    // rows between a thread's vectors, where that is a whole number: one offset
+    // then serves all of them, in memory from a base of their own, in LDS with
+    // an immediate (the key repeats every 16 rows)
+    static constexpr bool EVEN = NT % T::CPR == 0 && (NT / T::CPR) % 16 == 0 && N % NT == 0;
+    static constexpr int RPI = NT / T::CPR;
     uint4 r[PER];
     __device__ __forceinline__ void fetch(const char* base, int stride, int rows, int D, int tid) {
-        const RowView v(base, stride, rows, ROWS, D * T::ES);
+        if constexpr (EVEN) {
+            const int row = tid / T::CPR, c = tid % T::CPR, at = c * T::PE < D ? row * stride + c * 16 : kOutside;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int id = tid + i * NT, row = id / T::CPR, c = id % T::CPR;
-            r[i] = v.load((N % NT == 0 || id < N) && c * T::PE < D ? row * stride + c * 16 : kOutside);
+            for (int i = 0; i < PER; ++i)
+                r[i] = RowView(base + (int64_t)i * RPI * stride, stride, rows - i * RPI, RPI, D * T::ES).load(at);
+        } else {
+            const RowView v(base, stride, rows, ROWS, D * T::ES);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int id = tid + i * NT, row = id / T::CPR, c = id % T::CPR;
+                r[i] = v.load((N % NT == 0 || id < N) && c * T::PE < D ? row * stride + c * 16 : kOutside);
+            }
         }
     }
     __device__ __forceinline__ void put(char* tile, int tid) const {
+        if constexpr (EVEN) {
+            const int at = T::offset(tid / T::CPR, tid % T::CPR);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int id = tid + i * NT, row = id / T::CPR, c = id % T::CPR;
-            if (N % NT == 0 || id < N) *reinterpret_cast<uint4*>(tile + T::offset(row, c)) = r[i];
+            for (int i = 0; i < PER; ++i) *reinterpret_cast<uint4*>(tile + at + i * RPI * T::PITCH) = r[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int id = tid + i * NT, row = id / T::CPR, c = id % T::CPR;
+                if (N % NT == 0 || id < N) *reinterpret_cast<uint4*>(tile + T::offset(row, c)) = r[i];
+            }
         }
     }
 };

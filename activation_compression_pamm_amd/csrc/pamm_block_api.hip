@@ -53,7 +53,7 @@ int attention_sizes(const pamm_attention_t* a) {
     if (rows > kMaxSequence || mul(mul(a->batch, a->heads), a->seq_q) > kMaxSpan) return PAMM_ERR_SHAPE;
     const int64_t heads = mul(a->batch, a->heads_kv);
     if (mul(heads, 64) > kMaxSize || mul(heads, (rows + 127) / 128) > kMaxSize / 64 ||
-        mul(heads, (a->seq_k + 127) / 128) > kMaxSize || mul(mul(a->batch, a->heads), a->seq_q) > 4 * kMaxSize)
+        mul(heads, (a->seq_k + 127) / 128) > kMaxSize / 8 || mul(heads, a->seq_k) > 4 * kMaxSize || mul(mul(a->batch, a->heads), a->seq_q) > 4 * kMaxSize)
         return PAMM_ERR_SHAPE;
     return PAMM_OK;
 }
@@ -113,12 +113,16 @@ pamm::AttnArgs attention_args(const pamm_attention_t* a) {
     r.window = a->window >= a->seq_k ? 0 : (int)a->window;  // a window as long as the keys hides none
     r.scale = a->scale;
     r.num_cus = num_cus();
-    r.nsplit = 1;
+    r.nsplit = r.nsplit_kv = 1;
     return r;
 }
 
 int splits_of(const pamm_attention_t* a) {
     return pamm::attention_splits(a->batch, a->seq_q, a->seq_k, a->heads_kv, a->heads / a->heads_kv, num_cus());
+}
+
+int dkv_splits_of(const pamm_attention_t* a) {
+    return pamm::attention_dkv_splits(a->batch, a->seq_q, a->seq_k, a->heads_kv, a->heads / a->heads_kv, num_cus());
 }
 
 int ws_check(const void* ws, size_t ws_bytes, size_t need) {
@@ -175,7 +179,9 @@ int pamm_attention(const pamm_attention_t* a, void* ws, size_t ws_bytes, void* s
 
 size_t pamm_attention_backward_workspace_size(const pamm_attention_t* a) {
     if (attention_sizes(a) != PAMM_OK) return 0;
-    return up256((size_t)(a->batch * a->heads * a->seq_q) * sizeof(float));
+    const size_t n = (size_t)dkv_splits_of(a);
+    const size_t part = n > 1 ? up256(n * (size_t)(a->batch * a->heads_kv * a->seq_k * a->head_dim) * sizeof(float)) : 0;
+    return up256((size_t)(a->batch * a->heads * a->seq_q) * sizeof(float)) + 2 * part;
 }
 
 int pamm_attention_backward(const pamm_attention_t* a, const pamm_heads_t* dout, const pamm_heads_t* dq,
@@ -195,6 +201,13 @@ int pamm_attention_backward(const pamm_attention_t* a, const pamm_heads_t* dout,
     r.dk = heads_arg(*dk, a->dtype);
     r.dv = heads_arg(*dv, a->dtype);
     r.delta = reinterpret_cast<float*>(ws);
+    r.nsplit_kv = dkv_splits_of(a);
+    if (r.nsplit_kv > 1) {
+        const size_t part = (size_t)r.nsplit_kv * (size_t)(a->batch * a->heads_kv * a->seq_k * a->head_dim);
+        char* at = reinterpret_cast<char*>(ws) + up256((size_t)(a->batch * a->heads * a->seq_q) * sizeof(float));
+        r.part_dk = reinterpret_cast<float*>(at);
+        r.part_dv = reinterpret_cast<float*>(at + up256(part * sizeof(float)));
+    }
     return status(pamm::run_attention_backward(r, a->dtype, reinterpret_cast<hipStream_t>(stream)));
 }
 

@@ -28,6 +28,9 @@ struct AttnArgs {
     int nsplit;             // parts of the key axis (forward)
     float* part_o;          // [B x H x Sq x nsplit x D] when nsplit > 1
     float* part_lse;        // [B x H x Sq x nsplit], log2 units
+    int nsplit_kv;          // parts of the query axis (dk and dv)
+    float* part_dk;         // [nsplit_kv x B x Hkv x Sk x D] when nsplit_kv > 1
+    float* part_dv;
     int num_cus;
 };
 
@@ -37,6 +40,8 @@ constexpr int kFewRows = 32;
 
 // Parts into which the forward pass cuts the key axis.
 int attention_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int num_cus);
+// Parts into which the dk/dv pass cuts the queries of a key tile.
+int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int num_cus);
 hipError_t run_attention(const AttnArgs& a, int dtype, hipStream_t st);
 hipError_t run_attention_backward(const AttnArgs& a, int dtype, hipStream_t st);
 
