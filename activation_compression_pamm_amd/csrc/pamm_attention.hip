@@ -72,9 +72,9 @@ __device__ __forceinline__ float score_factor(float scale) { return fmaxf(fabsf(
 // buffers hold: while one is used, the next tile travels through registers
 // into the other.
 template <int DT, int ND>
-__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_kernel(AttnArgs a, int row_tiles) {
+__global__ __launch_bounds__(256, DT == DT_BF16 ? 3 : 1) void attention_kernel(AttnArgs a, int row_tiles) {
     using T = Tile<DT, ND>;
-    constexpr int BK = DT == DT_BF16 ? 64 : 32;
+    constexpr int BK = DT == DT_BF16 && ND <= 2 ? 64 : 32;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BK * T::PITCH];
     const int tid = threadIdx.x, l = tid & 63, wave = wave_id();
 

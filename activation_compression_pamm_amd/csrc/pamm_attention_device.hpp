@@ -120,30 +120,73 @@ template <> struct Packed<DT_F32> {
     __device__ __forceinline__ void set(const f32x16& d) { v = d; }
 };
 
+// The operands of one block of 32 tile rows, all of them: rows (for products
+// that contract over a row's elements) and transposed (for products that
+// contract over the rows).  A load from LDS takes several products' time, so
+// a block's operands are all requested before the first is used; `fence` keeps
+// the compiler from moving them back to their uses.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// Row operand of step s: 16 bytes of row r0 + l % 32 (r0 a multiple of 32).
+template <int DT, int ND>
+__device__ __forceinline__ uint4 row_operand(const char* tile, int r0, int base, int s) {
+    return *reinterpret_cast<const uint4*>(tile + r0 * Tile<DT, ND>::PITCH + (base ^ (s << 5)));
+}
+
+template <int DT, int ND>
+struct Rows {
+    static constexpr int NS = Tile<DT, ND>::NS;
+    uint4 v[NS];
+    __device__ __forceinline__ void load(const char* tile, int r0, int base) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s) v[s] = row_operand<DT, ND>(tile, r0, base, s);
+    }
+    // c + rows x b
+    __device__ __forceinline__ f32x16 product(const uint4* b, f32x16 c) const {
+#pragma unroll
+        for (int s = 0; s < NS; ++s) c = mma_step<DT>(v[s], b[s], c);
+        return c;
+    }
+};
+
 // acc[db] += (the 32 rows of `tile` from row r0, transposed) x b, for the ND
 // 32-element column blocks db: acc[db][e][col] += sum_r tile[r][32 db + e] b[r][col].
 // bf16 reads its operand with the transposing LDS load: the 16 lanes of a
 // group point at four rows of 32 bytes and each gets one column of the four.
-template <int DT, int ND>
-__device__ __forceinline__ void trans_product(const char* tile, int r0, int base, const Packed<DT>& b, f32x16* acc) {
-    using T = Tile<DT, ND>;
-    if constexpr (DT == DT_BF16) {
+template <int DT, int ND> struct Columns;
+template <int ND>
+struct Columns<DT_BF16, ND> {
+    using T = Tile<DT_BF16, ND>;
+    bf16x8 v[2][ND];
+    __device__ __forceinline__ void load(const char* tile, int r0, int base) {
         constexpr int flip = (T::key(8) ^ T::key(0)) << 4;
+        typedef __attribute__((address_space(3))) s16x4* lds_s4;
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int db = 0; db < ND; ++db) {
-                typedef __attribute__((address_space(3))) s16x4* lds_s4;
                 const char* at = tile + (r0 + 16 * t) * T::PITCH;
                 const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(at + (base ^ (db << 6))));
                 const s16x4 hi =
                     __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(at + 8 * T::PITCH + (base ^ (db << 6) ^ flip)));
-                typedef short s16x8 __attribute__((ext_vector_type(8)));
                 const s16x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), b.v[t], acc[db], 0, 0, 0);
+                v[t][db] = __builtin_bit_cast(bf16x8, a);
             }
-        }
-    } else {
+    }
+    __device__ __forceinline__ void product(const Packed<DT_BF16>& b, f32x16* acc) const {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int db = 0; db < ND; ++db)
+                acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[t][db], b.v[t], acc[db], 0, 0, 0);
+    }
+};
+template <int ND>
+struct Columns<DT_F32, ND> {
+    using T = Tile<DT_F32, ND>;
+    float v[16][ND];
+    __device__ __forceinline__ void load(const char* tile, int r0, int) {
         const int l = lane_id(), h = l >> 5;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -151,17 +194,23 @@ __device__ __forceinline__ void trans_product(const char* tile, int r0, int base
 #pragma unroll
             for (int db = 0; db < ND; ++db) {
                 const int e = 32 * db + (l & 31);
-                const float a = *reinterpret_cast<const float*>(tile + T::offset(row, e >> 2) + (e & 3) * 4);
-                acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, b.v[i], acc[db], 0, 0, 0);
+                v[i][db] = *reinterpret_cast<const float*>(tile + T::offset(row, e >> 2) + (e & 3) * 4);
             }
         }
     }
-}
-
-// Row operand of step s: 16 bytes of row r0 + l % 32 (r0 a multiple of 32).
+    __device__ __forceinline__ void product(const Packed<DT_F32>& b, f32x16* acc) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int db = 0; db < ND; ++db)
+                acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(v[i][db], b.v[i], acc[db], 0, 0, 0);
+    }
+};
 template <int DT, int ND>
-__device__ __forceinline__ uint4 row_operand(const char* tile, int r0, int base, int s) {
-    return *reinterpret_cast<const uint4*>(tile + r0 * Tile<DT, ND>::PITCH + (base ^ (s << 5)));
+__device__ __forceinline__ void trans_product(const char* tile, int r0, int base, const Packed<DT>& b, f32x16* acc) {
+    Columns<DT, ND> c;
+    c.load(tile, r0, base);
+    c.product(b, acc);
 }
 
 // This lane's 16-byte groups of one global row (zero where !ok or past D).
