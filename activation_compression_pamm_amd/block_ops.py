@@ -16,11 +16,11 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
-from . import (BF16, F32, _check, _dtype_code, _empty_rows, _on_gpu, _ptr, _rows, _stream_ptr, _check_workspace,
-               load_library)
+from . import BF16, F32, PammError, _check, _check_workspace, _empty_rows, _on_gpu, _ptr, load_library
 
 __all__ = ["attention", "attention_backward", "attention_workspace_size", "attention_backward_workspace_size",
            "add_rms_norm", "add_rms_norm_fp8", "add_rms_norm_backward", "clip_grad_norm", "MAX_HEAD_DIM"]
@@ -31,10 +31,12 @@ _i32, _i64, _f32, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, cty
 
 
 class _Heads(ctypes.Structure):
+    """pamm_heads_t"""
     _fields_ = [("data", _vp), ("stride_b", _i64), ("stride_s", _i64), ("stride_h", _i64)]
 
 
 class _Attention(ctypes.Structure):
+    """pamm_attention_t"""
     _fields_ = [("dtype", _i32), ("causal", _i32), ("batch", _i64), ("seq_q", _i64), ("seq_k", _i64),
                 ("heads", _i64), ("heads_kv", _i64), ("head_dim", _i64), ("window", _i64), ("scale", _f32),
                 ("q_len", _vp), ("kv_len", _vp), ("q", _Heads), ("k", _Heads), ("v", _Heads), ("o", _Heads),
@@ -42,9 +44,17 @@ class _Attention(ctypes.Structure):
 
 
 class _Grad(ctypes.Structure):
+    """pamm_grad_t"""
     _fields_ = [("data", _vp), ("out", _vp), ("rows", _i64), ("cols", _i64), ("ld", _i64), ("ld_out", _i64),
                 ("dtype", _i32), ("out_dtype", _i32)]
 
+
+# The same layouts for struct.pack, which builds one in a fraction of the time
+# of a ctypes structure: these calls are as short as single tokens.
+_HEADS = "Pqqq"
+_pack_attention = struct.Struct("@ii7qf4xPP" + 4 * _HEADS + "P").pack
+_pack_heads = struct.Struct("@" + _HEADS).pack
+_GRAD = "PP4qii"
 
 _BLOCK_EXPORTS = {
     "pamm_attention_workspace_size": (_sz, [_vp]),
@@ -73,6 +83,17 @@ def _lib():
     return _bound
 
 
+_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _code(where, t):
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{where}: float32 and bfloat16 tensors are supported, got {t.dtype}")
+    return code
+
+
 def _ws(nbytes, device, workspace, where):
     if nbytes == 0:
         return None, 0
@@ -80,29 +101,32 @@ def _ws(nbytes, device, workspace, where):
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     elif workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError(f"{where}: workspace needs {nbytes} bytes")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-class _on_device:
-    """The tensors' GPU as the current one (nothing to do where it already is):
-    kernels are launched on the device their memory and stream belong to."""
-
-    def __init__(self, device):
-        self.device, self.before = device.index, None
-
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if self.device is not None and self.device != now:
-            self.before = now
-            torch.cuda.set_device(self.device)
-
-    def __exit__(self, *exc):
-        if self.before is not None:
-            torch.cuda.set_device(self.before)
+def _stream_of(stream, index):
+    """The stream's handle; torch's current one on that GPU by default."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(index)
+    return torch.cuda.current_stream(index).cuda_stream
 
 
-def _stream_of(stream, device):
-    return _stream_ptr(stream if stream is not None else torch.cuda.current_stream(device))
+def _launch(where, index, fn, *args):
+    """fn(*args) with the tensors' GPU as the current one: kernels are launched
+    on the device that their memory and stream belong to."""
+    now = torch.cuda.current_device()
+    if now == index:
+        status = fn(*args)
+    else:
+        torch.cuda.set_device(index)
+        try:
+            status = fn(*args)
+        finally:
+            torch.cuda.set_device(now)
+    if status != 0:
+        _check(status, where)
 
 
 # ------------------------------------------------------------------- attention
@@ -111,76 +135,73 @@ def _heads_tensor(where, name, t):
     if t.dim() != 4:
         raise ValueError(f"{where}: {name} must be 4-D [batch x sequence x heads x head_dim], "
                          f"got shape {tuple(t.shape)}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    stride = t.stride()
+    if stride[3] != 1 and t.shape[3] > 1:
         raise ValueError(f"{where}: {name} must have contiguous head rows (stride 1 in the last dimension)")
+    return t.data_ptr(), stride[0], stride[1], stride[2]
 
 
-def _heads(t):
-    return _Heads(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
-
-
-def _lengths(where, name, t, batch, like):
+def _lengths(where, name, t, batch):
     if t is None:
-        return None
+        return 0
     if t.dim() != 1 or t.shape[0] != batch:
         raise ValueError(f"{where}: {name} must have shape {(batch,)}, got {tuple(t.shape)}")
     if t.dtype != torch.int32:
         raise TypeError(f"{where}: {name} must be int32, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be contiguous")
-    return t
+    return t.data_ptr()
 
 
-def _problem(where, q, k, v, o, lse, causal, window, scale, q_len, kv_len):
-    for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):
-        if t is not None:
-            _heads_tensor(where, name, t)
-            if t.dtype != q.dtype:
-                raise TypeError(f"{where}: q, k, v and o must share a dtype, got {q.dtype} and {t.dtype}")
+def _problem(where, q, k, v, o, lse, causal, window, scale, q_len, kv_len, **others):
+    """The checked arguments as a packed pamm_attention_t."""
+    qh, kh, vh = _heads_tensor(where, "q", q), _heads_tensor(where, "k", k), _heads_tensor(where, "v", v)
+    oh = _heads_tensor(where, "o", o) if o is not None else (0, 0, 0, 0)
+    dtype = q.dtype
+    if k.dtype != dtype or v.dtype != dtype or (o is not None and o.dtype != dtype):
+        raise TypeError(f"{where}: q, k, v and o must share a dtype, got {dtype}, {k.dtype}, {v.dtype}"
+                        + (f" and {o.dtype}" if o is not None else ""))
     B, Sq, H, D = q.shape
-    Sk, Hkv = k.shape[1], k.shape[2]
-    if k.shape[0] != B or k.shape[3] != D or tuple(v.shape) != tuple(k.shape):
+    kshape = k.shape
+    Bk, Sk, Hkv, Dk = kshape
+    if Bk != B or Dk != D or v.shape != kshape:
         raise ValueError(f"{where}: k and v must be [{B} x sequence x heads x {D}], got {tuple(k.shape)} and "
                          f"{tuple(v.shape)}")
     if Hkv < 1 or H % Hkv:
         raise ValueError(f"{where}: {H} query heads do not share {Hkv} key/value heads evenly")
-    _on_gpu(where, q=q, k=k, v=v, o=o, lse=lse, q_len=q_len, kv_len=kv_len)
-    q_len = _lengths(where, "q_len", q_len, B, q)
-    kv_len = _lengths(where, "kv_len", kv_len, B, q)
-    if o is not None and tuple(o.shape) != (B, Sq, H, D):
+    _on_gpu(where, q=q, k=k, v=v, o=o, lse=lse, q_len=q_len, kv_len=kv_len, **others)
+    if o is not None and o.shape != q.shape:
         raise ValueError(f"{where}: o must have shape {(B, Sq, H, D)}, got {tuple(o.shape)}")
-    if lse is not None:
-        if tuple(lse.shape) != (B, H, Sq) or lse.dtype != torch.float32 or not lse.is_contiguous():
-            raise ValueError(f"{where}: lse must be contiguous float32 of shape {(B, H, Sq)}")
-    return _Attention(dtype=_dtype_code(q), causal=1 if causal else 0, batch=B, seq_q=Sq, seq_k=Sk, heads=H,
-                      heads_kv=Hkv, head_dim=D, window=int(window or 0),
-                      scale=float(1.0 / math.sqrt(max(D, 1)) if scale is None else scale),
-                      q_len=q_len.data_ptr() if q_len is not None else None,
-                      kv_len=kv_len.data_ptr() if kv_len is not None else None,
-                      q=_heads(q), k=_heads(k), v=_heads(v))
+    if lse is not None and (lse.shape != (B, H, Sq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError(f"{where}: lse must be contiguous float32 of shape {(B, H, Sq)}")
+    return _pack_attention(
+        _code(where, q), 1 if causal else 0, B, Sq, Sk, H, Hkv, D, int(window or 0),
+        1.0 / math.sqrt(max(D, 1)) if scale is None else float(scale), _lengths(where, "q_len", q_len, B),
+        _lengths(where, "kv_len", kv_len, B), *qh, *kh, *vh, *oh, lse.data_ptr() if lse is not None else 0)
 
 
 def attention_workspace_size(q, k, *, causal=False) -> int:
     """Bytes of workspace ``attention`` needs for tensors of these shapes."""
     p = _problem("attention_workspace_size", q, k, k, None, None, causal, 0, None, None, None)
-    return int(_lib().pamm_attention_workspace_size(ctypes.byref(p)))
+    return int(_lib().pamm_attention_workspace_size(p))
 
 
 def attention_backward_workspace_size(q, k, *, causal=False) -> int:
     """Bytes of workspace ``attention_backward`` needs for tensors of these shapes."""
     p = _problem("attention_backward_workspace_size", q, k, k, None, None, causal, 0, None, None, None)
-    return int(_lib().pamm_attention_backward_workspace_size(ctypes.byref(p)))
+    return int(_lib().pamm_attention_backward_workspace_size(p))
 
 
 def _not_overlapping(where, name, t):
     """A written tensor must give every element an address of its own."""
+    if t.is_contiguous():
+        return
     need = 1
     for stride, size in sorted((t.stride(i), t.shape[i]) for i in range(t.dim()) if t.shape[i] > 1):
         if stride < need:
             raise ValueError(f"{where}: {name} is written and must not overlap itself, got strides {t.stride()} "
                              f"for shape {tuple(t.shape)}")
         need = stride * (size - 1) + need
-    return t
 
 
 def attention(q, k, v, *, causal: bool = False, window: int = 0, scale=None, q_len=None, kv_len=None, o=None,
@@ -199,20 +220,21 @@ def attention(q, k, v, *, causal: bool = False, window: int = 0, scale=None, q_l
     One query per sequence (or few) splits the keys over the whole device.
     Returns (o [B x Sq x H x D], lse [B x H x Sq] fp32); a query that sees no
     key has o = 0 and lse = -inf.  attention_backward takes both."""
-    p = _problem("attention", q, k, v, o, lse, causal, window, scale, q_len, kv_len)
+    where = "attention"
+    if q.dim() != 4:
+        _heads_tensor(where, "q", q)
     if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        o = torch.empty_like(q) if q.stride(3) == 1 else None
     else:
-        _not_overlapping("attention", "o", o)
+        _heads_tensor(where, "o", o)
+        _not_overlapping(where, "o", o)
     if lse is None:
         lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=q.device)
-    p.o, p.lse = _heads(o), lse.data_ptr()
-    _check_workspace("attention", workspace)
-    _on_gpu("attention", q=q, workspace=workspace)
-    lib = _lib()
-    with _on_device(q.device):
-        ws, nbytes = _ws(lib.pamm_attention_workspace_size(ctypes.byref(p)), q.device, workspace, "attention")
-        _check(lib.pamm_attention(ctypes.byref(p), _ptr(ws), nbytes, _stream_of(stream, q.device)), "pamm_attention")
+    p = _problem(where, q, k, v, o, lse, causal, window, scale, q_len, kv_len, workspace=workspace)
+    _check_workspace(where, workspace)
+    lib, index = _lib(), q.get_device()
+    ws, nbytes = _ws(lib.pamm_attention_workspace_size(p), q.device, workspace, where)
+    _launch("pamm_attention", index, lib.pamm_attention, p, ws, nbytes, _stream_of(stream, index))
     return o, lse
 
 
@@ -227,50 +249,61 @@ def attention_backward(do, q, k, v, o, lse, *, causal: bool = False, window: int
     packed gradient); they are written whole, with zeros past the lengths.
     Bitwise deterministic."""
     where = "attention_backward"
-    p = _problem(where, q, k, v, o, lse, causal, window, scale, q_len, kv_len)
-    _heads_tensor(where, "do", do)
-    if tuple(do.shape) != tuple(q.shape) or do.dtype != q.dtype:
+    doh = _heads_tensor(where, "do", do)
+    if do.shape != q.shape or do.dtype != q.dtype:
         raise ValueError(f"{where}: do must be {q.dtype} of shape {tuple(q.shape)}, got {tuple(do.shape)} {do.dtype}")
-    outs = []
+    outs, packed = [], [_pack_heads(*doh)]
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if t is None:
-            t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+            # like's own order if it is dense, else contiguous
+            t = torch.empty_like(like)
+            if t.stride(3) != 1 and t.shape[3] > 1:
+                _heads_tensor(where, name[1:], like)
+            _not_overlapping(where, name, t)
         else:
             _heads_tensor(where, name, t)
-            if tuple(t.shape) != tuple(like.shape) or t.dtype != like.dtype:
+            if t.shape != like.shape or t.dtype != like.dtype:
                 raise ValueError(f"{where}: {name} must be {like.dtype} of shape {tuple(like.shape)}, "
                                  f"got {tuple(t.shape)} {t.dtype}")
             _not_overlapping(where, name, t)
         outs.append(t)
-    p.o, p.lse = _heads(o), lse.data_ptr()
+        packed.append(_pack_heads(*_heads_tensor(where, name, t)))
+    p = _problem(where, q, k, v, o, lse, causal, window, scale, q_len, kv_len, do=do, dq=outs[0], dk=outs[1],
+                 dv=outs[2], workspace=workspace)
     _check_workspace(where, workspace)
-    _on_gpu(where, q=q, do=do, dq=outs[0], dk=outs[1], dv=outs[2], workspace=workspace)
-    lib = _lib()
-    h = [_heads(t) for t in (do, *outs)]
-    with _on_device(q.device):
-        ws, nbytes = _ws(lib.pamm_attention_backward_workspace_size(ctypes.byref(p)), q.device, workspace, where)
-        _check(lib.pamm_attention_backward(ctypes.byref(p), ctypes.byref(h[0]), ctypes.byref(h[1]), ctypes.byref(h[2]),
-                                           ctypes.byref(h[3]), _ptr(ws), nbytes, _stream_of(stream, q.device)),
-               "pamm_attention_backward")
+    lib, index = _lib(), q.get_device()
+    ws, nbytes = _ws(lib.pamm_attention_backward_workspace_size(p), q.device, workspace, where)
+    _launch("pamm_attention_backward", index, lib.pamm_attention_backward, p, *packed, ws, nbytes,
+            _stream_of(stream, index))
     return tuple(outs)
 
 
 # ------------------------------------------------------------------------ norm
 
 def _row_major(where, name, t, n, d, dtype):
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    """The leading dimension of an [n x d] tensor."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
         raise ValueError(f"{where}: {name} must be a 2-D tensor with contiguous rows")
-    if tuple(t.shape) != (n, d):
+    if t.shape != (n, d):
         raise ValueError(f"{where}: {name} must have shape {(n, d)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
     # a single row has no distance to the next
-    return t.stride(0) if n > 1 else _padded(d, t.element_size())
+    return t.stride(0) if n > 1 else (d + 15) // 16 * 16
 
 
-def _padded(d, size):
-    per = max(1, (8 if size == 1 else 16) // size)
-    return (d + per - 1) // per * per
+def _written_rows(where, name, t, n, d, dtype):
+    ld = _row_major(where, name, t, n, d, dtype)
+    if n > 1 and ld < d:
+        raise ValueError(f"{where}: {name} is written and must not overlap itself, got strides {t.stride()}")
+    return ld
+
+
+def _rows_like(t):
+    """Uninitialised rows of t's shape and dtype, a multiple of 16 bytes apart."""
+    if t.is_contiguous() and t.shape[1] * t.element_size() % 16 == 0:
+        return torch.empty_like(t)
+    return _empty_rows(t.shape[0], t.shape[1], t.dtype, t.device)
 
 
 def _vector(where, name, t, d, dtype):
@@ -279,41 +312,45 @@ def _vector(where, name, t, d, dtype):
 
 
 def _norm_forward(where, x, weight, residual, eps, h, y, q, qscale, want_q, stream):
-    n, d, _ = _rows(x, "x")
-    dt = _dtype_code(x)
-    ldx = _row_major(where, "x", x, n, d, x.dtype)
-    _vector(where, "weight", weight, d, x.dtype)
+    if x.dim() != 2:
+        raise ValueError(f"{where}: x must be a 2-D tensor with contiguous rows")
+    n, d = x.shape
+    dtype, device = x.dtype, x.device
+    dt = _code(where, x)
+    ldx = _row_major(where, "x", x, n, d, dtype)
+    _vector(where, "weight", weight, d, dtype)
     _on_gpu(where, x=x, weight=weight, residual=residual, h=h, y=y, q=q, qscale=qscale)
-    ldr = _row_major(where, "residual", residual, n, d, x.dtype) if residual is not None else 0
-    if h is not None and residual is None:
-        raise ValueError(f"{where}: h is x itself without a residual")
     if residual is None:
-        h_out, ldh = x, 0
+        if h is not None:
+            raise ValueError(f"{where}: h is x itself without a residual")
+        h_out, ldh, ldr, rp, hp = x, 0, 0, None, None
     else:
-        h_out = h if h is not None else _empty_rows(n, d, x.dtype, x.device)
-        ldh = _row_major(where, "h", h_out, n, d, x.dtype)
-        _not_overlapping(where, "h", h_out)
+        ldr = _row_major(where, "residual", residual, n, d, dtype)
+        h_out = h if h is not None else _rows_like(x)
+        ldh = _written_rows(where, "h", h_out, n, d, dtype)
+        rp, hp = residual.data_ptr(), h_out.data_ptr()
     ldy = ldq = 0
+    yp = qp = sp = None
     if want_q:
         if q is None:
-            q = torch.empty((n, _padded(d, 1)), dtype=torch.float8_e4m3fn, device=x.device)[:, :d]
-        ldq = _row_major(where, "q", q, n, d, torch.float8_e4m3fn)
-        _not_overlapping(where, "q", q)
+            wide = (d + 7) // 8 * 8
+            q = torch.empty((n, wide), dtype=torch.float8_e4m3fn, device=device)
+            if wide != d:
+                q = q[:, :d]
+        ldq = _written_rows(where, "q", q, n, d, torch.float8_e4m3fn)
         if qscale is None:
-            qscale = torch.empty(n, dtype=torch.float32, device=x.device)
-        _vector(where, "qscale", qscale, n, torch.float32)
+            qscale = torch.empty(n, dtype=torch.float32, device=device)
+        else:
+            _vector(where, "qscale", qscale, n, torch.float32)
+        qp, sp = q.data_ptr(), qscale.data_ptr()
     else:
-        y = y if y is not None else _empty_rows(n, d, x.dtype, x.device)
-        ldy = _row_major(where, "y", y, n, d, x.dtype)
-        _not_overlapping(where, "y", y)
-    rstd = torch.empty(n, dtype=torch.float32, device=x.device)
-    with _on_device(x.device):
-        st = _lib().pamm_add_rms_norm(
-            _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), n, d, dt, float(eps),
-            _ptr(h_out) if residual is not None else None, ldh, None if want_q else _ptr(y), ldy,
-            _ptr(q) if want_q else None, ldq, _ptr(qscale) if want_q else None, _ptr(rstd),
-            _stream_of(stream, x.device))
-        _check(st, "pamm_add_rms_norm")
+        y = y if y is not None else _rows_like(x)
+        ldy = _written_rows(where, "y", y, n, d, dtype)
+        yp = y.data_ptr()
+    rstd = torch.empty(n, dtype=torch.float32, device=device)
+    index = x.get_device()
+    _launch("pamm_add_rms_norm", index, _lib().pamm_add_rms_norm, x.data_ptr(), ldx, rp, ldr, weight.data_ptr(), n, d,
+            dt, eps, hp, ldh, yp, ldy, qp, ldq, sp, rstd.data_ptr(), _stream_of(stream, index))
     return (q, qscale, h_out, rstd) if want_q else (y, h_out, rstd)
 
 
@@ -343,27 +380,29 @@ def add_rms_norm_backward(dy, h, weight, rstd, *, dh=None, dx=None, dweight=None
     Returns (dx [n x d], the gradient of x and of residual alike,
     dweight [d] fp32).  dx may be dy or dh itself.  Bitwise deterministic."""
     where = "add_rms_norm_backward"
-    n, d, _ = _rows(h, "h")
-    dt = _dtype_code(h)
-    ldh = _row_major(where, "h", h, n, d, h.dtype)
-    lddy = _row_major(where, "dy", dy, n, d, h.dtype)
-    lddh = _row_major(where, "dh", dh, n, d, h.dtype) if dh is not None else 0
-    _vector(where, "weight", weight, d, h.dtype)
+    if h.dim() != 2:
+        raise ValueError(f"{where}: h must be a 2-D tensor with contiguous rows")
+    n, d = h.shape
+    dtype = h.dtype
+    dt = _code(where, h)
+    ldh = _row_major(where, "h", h, n, d, dtype)
+    lddy = _row_major(where, "dy", dy, n, d, dtype)
+    lddh = _row_major(where, "dh", dh, n, d, dtype) if dh is not None else 0
+    _vector(where, "weight", weight, d, dtype)
     _vector(where, "rstd", rstd, n, torch.float32)
     _on_gpu(where, h=h, dy=dy, dh=dh, weight=weight, rstd=rstd, dx=dx, dweight=dweight, workspace=workspace)
     _check_workspace(where, workspace)
-    dx = dx if dx is not None else _empty_rows(n, d, h.dtype, h.device)
-    lddx = _row_major(where, "dx", dx, n, d, h.dtype)
-    _not_overlapping(where, "dx", dx)
+    dx = dx if dx is not None else _rows_like(h)
+    lddx = _written_rows(where, "dx", dx, n, d, dtype)
     if dweight is None:
         dweight = torch.empty(d, dtype=torch.float32, device=h.device)
-    _vector(where, "dweight", dweight, d, torch.float32)
-    lib = _lib()
-    with _on_device(h.device):
-        ws, nbytes = _ws(lib.pamm_add_rms_norm_backward_workspace_size(n, d, dt), h.device, workspace, where)
-        _check(lib.pamm_add_rms_norm_backward(_ptr(dy), lddy, _ptr(h), ldh, _ptr(weight), _ptr(rstd), _ptr(dh), lddh,
-                                              n, d, dt, _ptr(dx), lddx, _ptr(dweight), _ptr(ws), nbytes,
-                                              _stream_of(stream, h.device)), "pamm_add_rms_norm_backward")
+    else:
+        _vector(where, "dweight", dweight, d, torch.float32)
+    lib, index = _lib(), h.get_device()
+    ws, nbytes = _ws(lib.pamm_add_rms_norm_backward_workspace_size(n, d, dt), h.device, workspace, where)
+    _launch("pamm_add_rms_norm_backward", index, lib.pamm_add_rms_norm_backward, dy.data_ptr(), lddy, h.data_ptr(),
+            ldh, weight.data_ptr(), rstd.data_ptr(), dh.data_ptr() if dh is not None else None, lddh, n, d, dt,
+            dx.data_ptr(), lddx, dweight.data_ptr(), ws, nbytes, _stream_of(stream, index))
     return dx, dweight
 
 
@@ -386,36 +425,6 @@ def _grad_layout(where, name, t):
     return 1, n, n
 
 
-def _written_apart(where, grads, outs, layouts, out_layouts):
-    """No written range may meet another tensor's: each element is scaled once."""
-    spans = []
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        rows, cols, ld = out_layouts[i]
-        if rows * cols:
-            spans.append((o.data_ptr(), o.data_ptr() + ((rows - 1) * ld + cols) * o.element_size(), i, True))
-        if o is not g and layouts[i][0] * layouts[i][1]:
-            rows, cols, ld = layouts[i]
-            spans.append((g.data_ptr(), g.data_ptr() + ((rows - 1) * ld + cols) * g.element_size(), i, False))
-    spans.sort()
-    active = []  # earlier spans that reach past the current one's start
-    for span in spans:
-        b1, _, j, w1 = span
-        active = [s for s in active if s[1] > b1]
-        for b0, _, i, w0 in active:
-            if not (w0 or w1):
-                continue
-            # columns of one wider matrix interleave without meeting
-            a, b = (outs if w0 else grads)[i], (outs if w1 else grads)[j]
-            la, lb = (out_layouts if w0 else layouts)[i], (out_layouts if w1 else layouts)[j]
-            size = a.element_size()
-            if la[0] > 1 and lb[0] > 1 and la[2] == lb[2] and size == b.element_size() and (b1 - b0) % size == 0:
-                shift = (b1 - b0) // size % la[2]
-                if shift >= la[1] and shift + lb[1] <= la[2]:
-                    continue
-            raise ValueError(f"{where}: gradients {i} and {j} share memory that is written")
-        active.append(span)
-
-
 def clip_grad_norm(grads, max_norm=None, *, eps: float = 1e-6, out=None, workspace=None, stream=None):
     """The 2-norm of all gradients together (a 0-D fp32 tensor on the GPU), and
     their scaling by min(1, max_norm / (norm + eps)), in place or into ``out``.
@@ -436,46 +445,56 @@ def clip_grad_norm(grads, max_norm=None, *, eps: float = 1e-6, out=None, workspa
         raise ValueError(f"{where}: {len(grads)} gradients and {len(outs)} outputs")
     if out is not None and max_norm is None:
         raise ValueError(f"{where}: out needs a max_norm")
-    pairs = [(g, o) for g, o in zip(grads, outs) if g is not None]
-    if not pairs:
+    first = next((g for g in grads if g is not None), None)
+    if first is None:
         raise ValueError(f"{where}: no gradient given")
-    grads, outs = [g for g, _ in pairs], [o for _, o in pairs]
-    device = grads[0].device
-    flat, layouts, out_layouts = [], [], []
-    for i, (g, o) in enumerate(pairs):
-        if not g.is_cuda or g.device != device:
+    index, device, codes, flat = first.get_device(), first.device, _CODES, []
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if g is None:
+            continue
+        if index < 0 or g.get_device() != index:
             raise ValueError(f"{where}: gradient {i} must be on one GPU with the others, got device {g.device}")
-        lay = _grad_layout(where, f"gradient {i}", g)
-        layouts.append(lay)
-        code = _dtype_code(g)
+        code = codes.get(g.dtype)
+        if code is None:
+            _code(where, g)
         if o is g:
-            lay_o, code_o = lay, code
-        else:
-            if o is None or o.shape != g.shape or o.device != device:
-                raise ValueError(f"{where}: output {i} must have shape {tuple(g.shape)} on {device}")
-            lay_o, code_o = _grad_layout(where, f"output {i}", o), _dtype_code(o)
-            if g.stride() != o.stride() and (lay[0] == 1) != (lay_o[0] == 1):
-                # one dense, one with padded rows: describe both as rows
-                if g.dim() == 2 and g.is_contiguous():
-                    lay = layouts[-1] = (g.shape[0], g.shape[1], g.shape[1])
-                elif o.dim() == 2 and o.is_contiguous():
-                    lay_o = (o.shape[0], o.shape[1], o.shape[1])
-                else:
-                    raise ValueError(f"{where}: output {i} must be laid out as its gradient")
-            elif lay[0] == 1 and g.stride() != o.stride() and not (g.is_contiguous() and o.is_contiguous()):
-                raise ValueError(f"{where}: output {i} must be laid out as its gradient")
-        out_layouts.append(lay_o)
-        flat.append((g.data_ptr(), o.data_ptr(), lay[0], lay[1], lay[2], lay_o[2], code, code_o))
-    if max_norm is not None:
-        _written_apart(where, grads, outs, layouts, out_layouts)
-    arr = (_Grad * len(flat))(*flat)
-    _check_workspace(where, workspace)
-    _on_gpu(where, grads=grads[0], workspace=workspace)
+            if g.is_contiguous():
+                n, p = g.numel(), g.data_ptr()
+                flat += (p, p, 1, n, n, n, code, code)
+            else:
+                rows, cols, ld = _grad_layout(where, f"gradient {i}", g)
+                flat += (g.data_ptr(), g.data_ptr(), rows, cols, ld, ld, code, code)
+            continue
+        if o is None or o.shape != g.shape or o.get_device() != index:
+            raise ValueError(f"{where}: output {i} must have shape {tuple(g.shape)} on {device}")
+        code_o = codes.get(o.dtype)
+        if code_o is None:
+            _code(where, o)
+        if g.is_contiguous() and o.is_contiguous():
+            n = g.numel()
+            flat += (g.data_ptr(), o.data_ptr(), 1, n, n, n, code, code_o)
+            continue
+        lay, lay_o = _grad_layout(where, f"gradient {i}", g), _grad_layout(where, f"output {i}", o)
+        if (lay[0] == 1) != (lay_o[0] == 1) and g.dim() == 2 and (g.is_contiguous() or o.is_contiguous()):
+            # one dense, one with padded rows: both as rows
+            lay, lay_o = ((t.shape[0], t.shape[1], t.stride(0)) for t in (g, o))
+        elif lay[:2] != lay_o[:2] or (lay[0] == 1 and g.stride() != o.stride()):
+            raise ValueError(f"{where}: output {i} must be laid out as its gradient")
+        flat += (g.data_ptr(), o.data_ptr(), lay[0], lay[1], lay[2], lay_o[2], code, code_o)
+    count = len(flat) // 8
+    arr = struct.pack("@" + _GRAD * count, *flat)
+    if workspace is not None:
+        _check_workspace(where, workspace)
+        _on_gpu(where, gradients=first, workspace=workspace)
     norm = torch.empty((), dtype=torch.float32, device=device)
     lib = _lib()
-    with _on_device(device):
-        ws, nbytes = _ws(lib.pamm_clip_grad_norm_workspace_size(arr, len(flat)), device, workspace, where)
-        _check(lib.pamm_clip_grad_norm(arr, len(flat), math.inf if max_norm is None else float(max_norm), float(eps),
-                                       _ptr(norm), _ptr(ws), nbytes, _stream_of(stream, device)),
-               "pamm_clip_grad_norm")
+    ws, nbytes = _ws(lib.pamm_clip_grad_norm_workspace_size(arr, count), device, workspace, where)
+    try:
+        _launch("pamm_clip_grad_norm", index, lib.pamm_clip_grad_norm, arr, count,
+                math.inf if max_norm is None else float(max_norm), float(eps), norm.data_ptr(), ws, nbytes,
+                _stream_of(stream, index))
+    except PammError as e:
+        if e.status == 10:  # PAMM_ERR_OVERLAP
+            raise ValueError(f"{where}: two gradients share memory that is written") from e
+        raise
     return norm

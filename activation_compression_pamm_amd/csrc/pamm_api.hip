@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "pamm.h"
+#include "pamm_block.h"
 #include "pamm_kernels.hpp"
 
 namespace {
@@ -91,6 +92,7 @@ const char* pamm_status_string(int status) {
         case PAMM_ERR_HIP: return "HIP runtime error at launch";
         case PAMM_ERR_VALUE: return "a scalar argument is out of range";
         case PAMM_ERR_TOO_LARGE: return "the problem needs more memory than is available (the fixed no-allocation scratch array, or host memory for sampling)";
+        case PAMM_ERR_OVERLAP: return "written ranges share memory";
         default: return "unknown status";
     }
 }

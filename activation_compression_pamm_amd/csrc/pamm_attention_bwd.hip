@@ -14,6 +14,8 @@
 // runs over the queries of every head that shares them (dk, dv).  Forming P
 // and dS in both costs 7 products instead of 5, and buys sums without atomics:
 // the results are bitwise repeatable and no fp32 copy of dq is kept.
+#include <algorithm>
+
 #include "pamm_attention_device.hpp"
 
 namespace pamm {
@@ -338,17 +340,20 @@ __global__ __launch_bounds__(256) void attention_dkv_join_kernel(AttnArgs a) {
     }
 }
 
-// A part costs a write and a read of fp32 sums for its keys, 16 n D bytes a
-// key, against 8 D Sq G operations: with 4096 rows or more a part, under 6% of
-// the time at the rates both reach (2 PFLOP/s products apart, see the figures
-// at run time), so only then are parts made, up to 8 workgroups a unit in all.
-int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int num_cus) {
-    const int64_t blocks = B * Hkv * ((Sk + 127) / 128), want = 8 * (int64_t)num_cus;
-    if (blocks == 0 || blocks >= want) return 1;
-    int64_t n = (want + blocks - 1) / blocks;
-    if (n > Sq * G / 4096) n = Sq * G / 4096;
-    if (n > 8) n = 8;
-    return n < 1 ? 1 : (int)n;
+// Two reasons to cut a key tile's queries into parts, up to 8.  Many queries
+// share few keys: the workgroups of a causal mask are then few and uneven.  A
+// part costs a write and a read of fp32 sums, 16 bytes an element of its keys,
+// against 8 Sq G operations, so with 4096 rows or more a part it is lost in
+// the rest (8192 tokens, 32/8 heads of 64: dk/dv 1298 us whole, 808 + 25 us in
+// 4 parts).  Or the device is not full: then parts run side by side, and the
+// joining launch is paid for by a tile of 32 rows in fp32 (4 us) or 8 such
+// tiles in bf16.
+int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int dtype, int num_cus) {
+    const int64_t blocks = B * Hkv * ((Sk + 127) / 128), rows = Sq * G, least = dtype == DT_BF16 ? 256 : 64;
+    if (blocks == 0 || blocks >= 8 * (int64_t)num_cus) return 1;
+    int64_t n = std::min<int64_t>((8 * (int64_t)num_cus + blocks - 1) / blocks, rows / 4096);
+    if (blocks < num_cus) n = std::max<int64_t>(n, std::min<int64_t>((2 * num_cus + blocks - 1) / blocks, rows / least));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(n, 8));
 }
 
 template <int DT, int ND>

@@ -122,7 +122,8 @@ int splits_of(const pamm_attention_t* a) {
 }
 
 int dkv_splits_of(const pamm_attention_t* a) {
-    return pamm::attention_dkv_splits(a->batch, a->seq_q, a->seq_k, a->heads_kv, a->heads / a->heads_kv, num_cus());
+    return pamm::attention_dkv_splits(a->batch, a->seq_q, a->seq_k, a->heads_kv, a->heads / a->heads_kv, a->dtype,
+                                      num_cus());
 }
 
 int ws_check(const void* ws, size_t ws_bytes, size_t need) {
@@ -328,6 +329,47 @@ int clip_list(const pamm_grad_t* g, int64_t count, bool write, std::vector<pamm:
     return PAMM_OK;
 }
 
+// Whether a written range meets another tensor's: each element is scaled once.
+bool clip_overlap(const pamm_grad_t* g, int64_t count) {
+    struct Span {
+        uintptr_t begin, end;
+        int64_t rows, cols, ld;
+        int size;
+        bool written;
+    };
+    std::vector<Span> spans, active;
+    spans.reserve(2 * (size_t)count);
+    for (int64_t i = 0; i < count; ++i) {
+        const pamm_grad_t& t = g[i];
+        if (t.rows == 0 || t.cols == 0) continue;
+        auto add = [&](const void* p, int64_t ld, int dtype, bool written) {
+            const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+            const int e = elem_size(dtype);
+            spans.push_back({b, b + (uintptr_t)((t.rows > 1 ? (t.rows - 1) * ld : 0) + t.cols) * (uintptr_t)e, t.rows,
+                             t.cols, ld, e, written});
+        };
+        add(t.out, t.ld_out, t.out_dtype, true);
+        if (t.out != t.data) add(t.data, t.ld, t.dtype, false);
+    }
+    std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+    for (const Span& s : spans) {
+        active.erase(std::remove_if(active.begin(), active.end(), [&](const Span& a) { return a.end <= s.begin; }),
+                     active.end());
+        for (const Span& a : active) {
+            if (!a.written && !s.written) continue;
+            // columns of one wider matrix interleave without meeting
+            const uintptr_t gap = s.begin - a.begin;
+            if (a.rows > 1 && s.rows > 1 && a.ld == s.ld && a.size == s.size && gap % (uintptr_t)a.size == 0) {
+                const int64_t shift = (int64_t)(gap / (uintptr_t)a.size) % a.ld;
+                if (shift >= a.cols && shift + s.cols <= a.ld) continue;
+            }
+            return true;
+        }
+        active.push_back(s);
+    }
+    return false;
+}
+
 size_t clip_ws(size_t tensors) {
     const size_t launches = (tensors + pamm::kClipTensors - 1) / pamm::kClipTensors;
     return up256(launches * pamm::kClipBlocks * sizeof(double));
@@ -354,6 +396,7 @@ int pamm_clip_grad_norm(const pamm_grad_t* grads, int64_t count, float max_norm,
     try {
         list.reserve((size_t)count);
         if (int e = clip_list(grads, count, write, list)) return e;
+        if (write && clip_overlap(grads, count)) return PAMM_ERR_OVERLAP;
     } catch (...) {
         return PAMM_ERR_TOO_LARGE;
     }
@@ -362,6 +405,8 @@ int pamm_clip_grad_norm(const pamm_grad_t* grads, int64_t count, float max_norm,
     const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     double* part = reinterpret_cast<double*>(ws);
     pamm::ClipArgs a;
+    bool in_place = true;
+    for (const pamm::ClipTensor& t : list) in_place = in_place && t.out == t.data;
     auto fill = [&](size_t first) {
         memset(&a, 0, sizeof a);
         const size_t n = std::min<size_t>(pamm::kClipTensors, list.size() - first);
@@ -373,6 +418,7 @@ int pamm_clip_grad_norm(const pamm_grad_t* grads, int64_t count, float max_norm,
         a.count = (int)n;
         a.max_norm = max_norm;
         a.eps = eps;
+        a.in_place = in_place;
     };
     int parts = 0;
     for (size_t first = 0; first < list.size(); first += pamm::kClipTensors) {

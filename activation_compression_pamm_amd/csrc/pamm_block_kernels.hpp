@@ -41,7 +41,7 @@ constexpr int kFewRows = 32;
 // Parts into which the forward pass cuts the key axis.
 int attention_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int num_cus);
 // Parts into which the dk/dv pass cuts the queries of a key tile.
-int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int num_cus);
+int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int dtype, int num_cus);
 hipError_t run_attention(const AttnArgs& a, int dtype, hipStream_t st);
 hipError_t run_attention_backward(const AttnArgs& a, int dtype, hipStream_t st);
 
@@ -84,6 +84,7 @@ struct ClipArgs {
     int count;
     int parts;        // partial sums of this launch (forward) or of all (scaling)
     int64_t chunks;   // of this launch
+    int in_place;     // every output of the call is its input
     double* part;
     float* norm;
     float max_norm, eps;

@@ -178,6 +178,7 @@ __global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipArgs a) {
     if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
     float coef = a.max_norm / (norm + a.eps);
     if (coef > 1.0f) coef = 1.0f;  // NaN stays
+    if (coef == 1.0f && a.in_place) return;
     for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
         const ClipTensor& t = a.t[clip_tensor(a, c)];
         if (coef == 1.0f && t.out == t.data) continue;

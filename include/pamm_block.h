@@ -26,6 +26,9 @@
 extern "C" {
 #endif
 
+/* A further pamm_status_t: written ranges of one call share memory. */
+#define PAMM_ERR_OVERLAP 10
+
 /* Largest head dimension of the attention calls. */
 #define PAMM_MAX_HEAD_DIM 128
 
@@ -180,10 +183,13 @@ size_t pamm_clip_grad_norm_workspace_size(const pamm_grad_t *grads_host, int64_t
  *   max_norm    >= 0; +infinity: the norm alone, nothing is written to out
  *   norm        one fp32 (written)
  *
- * The written ranges must not overlap each other or another gradient's data.
+ * The written ranges must not meet each other or another gradient's data
+ * (column ranges of one wider matrix may interleave).
+ *
  * Errors: PAMM_ERR_NULL, _SHAPE, _DTYPE, _VALUE (max_norm or eps negative or
- * NaN; in place with another out_dtype or ld; count < 0), _ALIGN (an address
- * that is not a multiple of its element's size), _WORKSPACE.
+ * NaN; in place with another out_dtype or ld), _ALIGN (an address that is not
+ * a multiple of its element's size), PAMM_ERR_OVERLAP, _WORKSPACE,
+ * _TOO_LARGE (no host memory for the list).
  */
 int pamm_clip_grad_norm(const pamm_grad_t *grads_host, int64_t count, float max_norm, float eps, float *norm,
                         void *ws, size_t ws_bytes, void *stream);
