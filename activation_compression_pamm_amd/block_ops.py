@@ -180,9 +180,10 @@ def _problem(where, q, k, v, o, lse, causal, window, scale, q_len, kv_len, **oth
         _lengths(where, "kv_len", kv_len, B), *qh, *kh, *vh, *oh, lse.data_ptr() if lse is not None else 0)
 
 
-def attention_workspace_size(q, k, *, causal=False) -> int:
-    """Bytes of workspace ``attention`` needs for tensors of these shapes."""
-    p = _problem("attention_workspace_size", q, k, k, None, None, causal, 0, None, None, None)
+def attention_workspace_size(q, k, *, causal=False, kv_len=None) -> int:
+    """Bytes of workspace ``attention`` needs for tensors of these shapes
+    (more where the keys' lengths are given: they are cut finer)."""
+    p = _problem("attention_workspace_size", q, k, k, None, None, causal, 0, None, None, kv_len)
     return int(_lib().pamm_attention_workspace_size(p))
 
 

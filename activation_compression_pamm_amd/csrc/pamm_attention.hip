@@ -14,6 +14,8 @@
 //
 // Queries of the heads that share a key/value head are rows of one problem:
 // row r is position r / G of head r % G.
+#include <algorithm>
+
 #include "pamm_attention_device.hpp"
 
 namespace pamm {
@@ -303,48 +305,68 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_few_kern
     }
 }
 
-// Joins the parts of one row: weights 2^(lse_part - lse).  One wave a row.
+// Joins the parts of one row: weights 2^(lse_part - lse).  One wave a row; lane
+// s holds part s's weight (there are at most 64 parts), then every lane adds up
+// two columns, eight parts' loads at a time.
 template <int DT>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
-    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t at = (int64_t)blockIdx.x * 4 + wave_id();
     if (at >= (int64_t)a.B * a.H * a.Sq) return;
     const int l = threadIdx.x & 63;
-    const float* lse = a.part_lse + at * a.nsplit;
     const float* po = a.part_o + at * a.nsplit * a.D;
-    float m = -INFINITY, total = 0.0f, v0 = 0.0f, v1 = 0.0f;
-    for (int s = 0; s < a.nsplit; ++s) m = fmaxf(m, lse[s]);
-    const float ref = m == -INFINITY ? 0.0f : m;
-    for (int s = 0; s < a.nsplit; ++s) {
-        const float w = __builtin_amdgcn_exp2f(lse[s] - ref);
-        total += w;
-        if (w == 0.0f) continue;
-        if (l < a.D) v0 += w * po[s * a.D + l];
-        if (l + 64 < a.D) v1 += w * po[s * a.D + l + 64];
+    const float lse = l < a.nsplit ? a.part_lse[at * a.nsplit + l] : -INFINITY;
+    float m = lse;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, shfl_xor(m, x));
+    const float w = __builtin_amdgcn_exp2f(lse - (m == -INFINITY ? 0.0f : m));
+    float total = w;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) total += shfl_xor(total, x);
+    // parts that saw nothing hold zeros
+    const bool c0 = l < a.D, c1 = l + 64 < a.D;
+    float v0 = 0.0f, v1 = 0.0f;
+    for (int s = 0; s < a.nsplit; s += 8) {
+        float x0[8], x1[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x0[i] = c0 && s + i < a.nsplit ? po[(s + i) * a.D + l] : 0.0f;
+            x1[i] = c1 && s + i < a.nsplit ? po[(s + i) * a.D + l + 64] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = __shfl(w, (s + i) & 63, 64);
+            v0 = fmaf(u, x0[i], v0);
+            v1 = fmaf(u, x1[i], v1);
+        }
     }
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     const int64_t pos = at % a.Sq, bh = at / a.Sq;
     char* o = a.o.p + (bh / a.H) * a.o.sb + pos * a.o.ss + (bh % a.H) * a.o.sh;
     if constexpr (DT == DT_BF16) {
-        if (l < a.D) reinterpret_cast<__bf16*>(o)[l] = (__bf16)(v0 * inv);
-        if (l + 64 < a.D) reinterpret_cast<__bf16*>(o)[l + 64] = (__bf16)(v1 * inv);
+        if (c0) reinterpret_cast<__bf16*>(o)[l] = (__bf16)(v0 * inv);
+        if (c1) reinterpret_cast<__bf16*>(o)[l + 64] = (__bf16)(v1 * inv);
     } else {
-        if (l < a.D) reinterpret_cast<float*>(o)[l] = v0 * inv;
-        if (l + 64 < a.D) reinterpret_cast<float*>(o)[l + 64] = v1 * inv;
+        if (c0) reinterpret_cast<float*>(o)[l] = v0 * inv;
+        if (c1) reinterpret_cast<float*>(o)[l + 64] = v1 * inv;
     }
     if (l == 0) a.lse[at] = total == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
-int attention_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int num_cus) {
+// Single tokens are bound by reading K and V once.  Where the keys' lengths are
+// given they differ, unknown to the host, so the parts are made small enough to
+// even them out: 8 workgroups a unit (64 sequences of up to 8192, 8 heads of
+// 128: 229 us, against 245 with 4 and 272 with 2).  Equal lengths need no more
+// than fill the device (369 us with 2, 389 with 4, 394 with 8).  A part is at
+// least 256 keys, two blocks a wave; 512 for a tile of many rows.
+int attention_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, bool lengths, int num_cus) {
     const int64_t rows = Sq * G;
     const bool few = rows <= kFewRows;
     const int64_t tiles = few ? 1 : (rows + 127) / 128;
-    const int64_t blocks = B * Hkv * tiles, want = few ? 4 * num_cus : 2 * num_cus, least = few ? 256 : 512;
+    const int64_t blocks = B * Hkv * tiles, want = (few && lengths ? 8 : 2) * (int64_t)num_cus, least = few ? 256 : 512;
     if (blocks == 0 || blocks >= want) return 1;
-    const int64_t by_keys = (Sk + least - 1) / least;
     int64_t n = (want + blocks - 1) / blocks;
-    if (n > by_keys) n = by_keys;
-    if (n > 64) n = 64;
-    return n < 1 ? 1 : (int)n;
+    n = std::min(n, (Sk + least - 1) / least);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(n, kMaxSplits));
 }
 
 template <int DT, int ND>

@@ -118,7 +118,8 @@ pamm::AttnArgs attention_args(const pamm_attention_t* a) {
 }
 
 int splits_of(const pamm_attention_t* a) {
-    return pamm::attention_splits(a->batch, a->seq_q, a->seq_k, a->heads_kv, a->heads / a->heads_kv, num_cus());
+    return pamm::attention_splits(a->batch, a->seq_q, a->seq_k, a->heads_kv, a->heads / a->heads_kv,
+                                  a->kv_len != nullptr, num_cus());
 }
 
 int dkv_splits_of(const pamm_attention_t* a) {

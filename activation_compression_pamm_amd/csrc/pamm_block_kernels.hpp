@@ -38,8 +38,9 @@ struct AttnArgs {
 // kernel gives each wave keys of its own instead of rows of its own.
 constexpr int kFewRows = 32;
 
-// Parts into which the forward pass cuts the key axis.
-int attention_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int num_cus);
+// Parts into which the forward pass cuts the key axis, at most kMaxSplits.
+constexpr int kMaxSplits = 64;
+int attention_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, bool lengths, int num_cus);
 // Parts into which the dk/dv pass cuts the queries of a key tile.
 int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int dtype, int num_cus);
 hipError_t run_attention(const AttnArgs& a, int dtype, hipStream_t st);

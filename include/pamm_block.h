@@ -70,7 +70,8 @@ typedef struct {
 } pamm_attention_t;
 
 /* Bytes of workspace pamm_attention needs: 0 unless the keys are split over
- * workgroups because there are few queries (the partial results of each part). */
+ * workgroups because there are few queries (the partial results of each part).
+ * Pointers are not looked at, except whether kv_len is given. */
 size_t pamm_attention_workspace_size(const pamm_attention_t *a_host);
 
 /*
