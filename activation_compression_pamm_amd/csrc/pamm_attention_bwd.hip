@@ -43,7 +43,7 @@ __device__ __forceinline__ float dot16(const uint4& x, const uint4& y) {
 template <int DT, int ND>
 __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kernel(AttnArgs a, int row_tiles) {
     using T = Tile<DT, ND>;
-    constexpr int BK = DT == DT_BF16 ? 64 : 32;
+    constexpr int BK = 32;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BK * T::PITCH];
     const int tid = threadIdx.x, l = tid & 63, wave = wave_id();
 
