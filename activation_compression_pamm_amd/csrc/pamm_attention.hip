@@ -74,13 +74,19 @@ __device__ __forceinline__ float score_factor(float scale) { return fmaxf(fabsf(
 // buffers hold: while one is used, the next tile travels through registers
 // into the other.
 template <int DT, int ND>
-__global__ __launch_bounds__(256, DT == DT_BF16 ? 3 : 1) void attention_kernel(AttnArgs a, int row_tiles) {
+struct RowsShared {
+    static constexpr int BK = DT == DT_BF16 && ND <= 2 ? 64 : 32;
+    char tile[2][2][BK * Tile<DT, ND>::PITCH];
+};
+
+template <int DT, int ND, bool SAFE>
+__device__ __forceinline__ void attention_rows(const AttnArgs& a, int id, int row_tiles, RowsShared<DT, ND>& shared) {
     using T = Tile<DT, ND>;
-    constexpr int BK = DT == DT_BF16 && ND <= 2 ? 64 : 32;
-    __shared__ __attribute__((aligned(16))) char lds[2][2][BK * T::PITCH];
+    constexpr int BK = RowsShared<DT, ND>::BK;
+    auto& lds = shared.tile;
     const int tid = threadIdx.x, l = tid & 63, wave = wave_id();
 
-    const WorkItem w = work_item(blockIdx.x, a.B * a.Hkv, row_tiles * a.nsplit, a.causal);
+    const WorkItem w = work_item(id, a.B * a.Hkv, row_tiles * a.nsplit, a.causal);
     const int split = w.item % a.nsplit, b = w.head / a.Hkv, hk = w.head % a.Hkv;
     const int tile = row_tiles - 1 - w.item / a.nsplit;  // the last rows see the most keys: they start first
     const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
@@ -143,11 +149,12 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 3 : 1) void attention_kernel(A
             for (int i = 0; i < T::NS; ++i)
                 s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], kb * 32, rb, i), qf[i], s);
             settle<DT>(s);
-            if (key0 < wr.all_lo || key0 + 32 > wr.all_hi) mask_block(s, key0, mine);
+            const bool part = key0 < wr.all_lo || key0 + 32 > wr.all_hi;
+            if (part) mask_block(s, key0, mine);
             softmax_update<ND>(s, c, st, acc);
             Packed<DT> p;
             p.set(s);
-            trans_product<DT, ND>(lds[cur][1], kb * 32, tb, p, acc);
+            trans_product<DT, ND, true, SAFE>(lds[cur][1], kb * 32, tb, p, part, key0, mine, acc);
         }
         if (more) {
             kc.put(lds[cur ^ 1][0], tid);
@@ -158,10 +165,12 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 3 : 1) void attention_kernel(A
 
 #pragma unroll
     for (int db = 0; db < ND; ++db) settle<DT>(acc[db]);
+    const bool marked = !SAFE && a.causal && !sums_finite<ND>(acc);
     if (!live) return;
     const float sum = half_sum(st.l);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const float lse2 = sum == 0.0f ? -INFINITY : st.m + __builtin_amdgcn_logf(sum);
+    float lse2 = sum == 0.0f ? -INFINITY : st.m + __builtin_amdgcn_logf(sum);
+    if (marked) lse2 = NAN;
     const int64_t at = ((int64_t)b * a.H + head) * a.Sq + pos;
     if (a.nsplit > 1) {
         store_rows<DT_F32, ND>(reinterpret_cast<char*>(a.part_o + (at * a.nsplit + split) * a.D), acc, inv, a.D);
@@ -170,6 +179,38 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 3 : 1) void attention_kernel(A
         store_rows<DT, ND>(a.o.p + b * a.o.sb + pos * a.o.ss + head * a.o.sh, acc, inv, a.D);
         if (l < 32) a.lse[at] = lse2 * kLn2;
     }
+}
+
+template <int DT, int ND>
+__global__ __launch_bounds__(256, DT == DT_BF16 ? 3 : 1) void attention_kernel(AttnArgs a, int row_tiles) {
+    __shared__ __attribute__((aligned(16))) RowsShared<DT, ND> shared;
+    attention_rows<DT, ND, false>(a, blockIdx.x, row_tiles, shared);
+}
+
+// The mark of a wave is the lse of its first row: NaN.  (One that is NaN by
+// itself is computed twice, with the same result.)
+__device__ __forceinline__ bool is_marked(const AttnArgs& a, const WorkItem& w, int row, int split) {
+    if (row >= a.Sq * a.G) return false;
+    const int b = w.head / a.Hkv, head = w.head % a.Hkv * a.G + row % a.G, pos = row / a.G;
+    const int64_t at = ((int64_t)b * a.H + head) * a.Sq + pos;
+    const float v = a.nsplit > 1 ? a.part_lse[at * a.nsplit + split] : a.lse[at];
+    return v != v;
+}
+
+template <int DT, int ND>
+__global__ __launch_bounds__(256, 1) void attention_again_kernel(AttnArgs a, int row_tiles, int items) {
+    __shared__ __attribute__((aligned(16))) RowsShared<DT, ND> shared;
+    each_marked(
+        items,
+        [&](int id) {
+            const WorkItem w = work_item(id, a.B * a.Hkv, row_tiles * a.nsplit, a.causal);
+            const int row = (row_tiles - 1 - w.item / a.nsplit) * 128, split = w.item % a.nsplit;
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) any |= is_marked(a, w, row + 32 * i, split);
+            return any;
+        },
+        [&](int id) { attention_rows<DT, ND, true>(a, __builtin_amdgcn_readfirstlane(id), row_tiles, shared); });
 }
 
 // ----------------------------------------------------------------- few rows
@@ -181,16 +222,23 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 3 : 1) void attention_kernel(A
 // the wave's own LDS tile; the next block's loads are issued as soon as the
 // registers of the current one are used.
 template <int DT, int ND>
-__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_few_kernel(AttnArgs a) {
+struct FewShared {
+    static constexpr int OP = ND * 32 + 4;  // floats between rows of the merged result
+    static constexpr int VT = 32 * Tile<DT, ND>::PITCH;
+    static constexpr int SH = 4 * VT > 32 * OP * 4 ? 4 * VT : 32 * OP * 4;
+    char lds[SH];
+    float stat[4][2][32];
+};
+
+template <int DT, int ND, bool SAFE>
+__device__ __forceinline__ void attention_few(const AttnArgs& a, int id, FewShared<DT, ND>& shared) {
     using T = Tile<DT, ND>;
-    constexpr int OP = ND * 32 + 4;  // floats between rows of the merged result
-    constexpr int VT = 32 * T::PITCH;
-    constexpr int SH = 4 * VT > 32 * OP * 4 ? 4 * VT : 32 * OP * 4;
-    __shared__ __attribute__((aligned(16))) char lds[SH];
-    __shared__ float stat[4][2][32];
+    constexpr int OP = FewShared<DT, ND>::OP, VT = FewShared<DT, ND>::VT;
+    char* lds = shared.lds;
+    auto& stat = shared.stat;
     const int tid = threadIdx.x, l = tid & 63, wave = wave_id();
 
-    const WorkItem w = work_item(blockIdx.x, a.B * a.Hkv, a.nsplit, false);
+    const WorkItem w = work_item(id, a.B * a.Hkv, a.nsplit, false);
     const int split = w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;
     const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
     const int rows = a.Sq * a.G;
@@ -243,19 +291,22 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_few_kern
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         if (t + 4 < p1) fetch(key0 + 128);
-        if (key0 < br.all_lo || key0 + 32 > br.all_hi) mask_block(s, key0, mine);
+        const bool part = key0 < br.all_lo || key0 + 32 > br.all_hi;
+        if (part) mask_block(s, key0, mine);
         softmax_update<ND>(s, c, st, acc);
         Packed<DT> p;
         p.set(s);
-        trans_product<DT, ND>(vt, 0, opaque(trans_base<DT, ND>()), p, acc);
+        trans_product<DT, ND, true, SAFE>(vt, 0, opaque(trans_base<DT, ND>()), p, part, key0, mine, acc);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 
 #pragma unroll
     for (int db = 0; db < ND; ++db) settle<DT>(acc[db]);
+    // one query has no key hidden between others
+    const bool marked = !SAFE && a.causal && a.Sq > 1 && !sums_finite<ND>(acc);
 
     // join the four waves: the common reference first, then the sums in order
-    const float sum = half_sum(st.l);
+    const float sum = marked ? NAN : half_sum(st.l);  // makes the joined lse NaN
     if (l < 32) {
         stat[wave][0][l] = sum == 0.0f ? -INFINITY : st.m;
         stat[wave][1][l] = sum;
@@ -303,6 +354,24 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_few_kern
                 reinterpret_cast<float*>(o)[x] = v;
         }
     }
+}
+
+template <int DT, int ND>
+__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_few_kernel(AttnArgs a) {
+    __shared__ __attribute__((aligned(16))) FewShared<DT, ND> shared;
+    attention_few<DT, ND, false>(a, blockIdx.x, shared);
+}
+
+template <int DT, int ND>
+__global__ __launch_bounds__(256, 1) void attention_few_again_kernel(AttnArgs a, int items) {
+    __shared__ __attribute__((aligned(16))) FewShared<DT, ND> shared;
+    each_marked(
+        items,
+        [&](int id) {
+            const WorkItem w = work_item(id, a.B * a.Hkv, a.nsplit, false);
+            return is_marked(a, w, 0, w.item);
+        },
+        [&](int id) { attention_few<DT, ND, true>(a, __builtin_amdgcn_readfirstlane(id), shared); });
 }
 
 // Joins the parts of one row: weights 2^(lse_part - lse).  One wave a row; lane
@@ -371,14 +440,17 @@ int attention_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, 
 
 template <int DT, int ND>
 static void launch_attention(const AttnArgs& a, hipStream_t st) {
-    const int64_t rows = (int64_t)a.Sq * a.G;
+    const int64_t rows = (int64_t)a.Sq * a.G, tiles = rows <= kFewRows ? 1 : (rows + 127) / 128;
+    const int items = (int)((int64_t)a.B * a.Hkv * tiles * a.nsplit);
+    const dim3 grid((unsigned)items), again((unsigned)std::min(items, a.num_cus));
+    // only a causal mask hides keys of one query between those of others
+    const bool hides = a.causal && a.Sq > 1;
     if (rows <= kFewRows) {
-        const dim3 grid((unsigned)((int64_t)a.B * a.Hkv * a.nsplit));
         hipLaunchKernelGGL((attention_few_kernel<DT, ND>), grid, dim3(256), 0, st, a);
+        if (hides) hipLaunchKernelGGL((attention_few_again_kernel<DT, ND>), again, dim3(256), 0, st, a, items);
     } else {
-        const int64_t tiles = (rows + 127) / 128;
-        const dim3 grid((unsigned)((int64_t)a.B * a.Hkv * tiles * a.nsplit));
         hipLaunchKernelGGL((attention_kernel<DT, ND>), grid, dim3(256), 0, st, a, (int)tiles);
+        if (hides) hipLaunchKernelGGL((attention_again_kernel<DT, ND>), again, dim3(256), 0, st, a, (int)tiles, items);
     }
     if (a.nsplit > 1) {
         const dim3 grid((unsigned)(((int64_t)a.B * a.H * a.Sq + 3) / 4));

@@ -41,13 +41,19 @@ __device__ __forceinline__ float dot16(const uint4& x, const uint4& y) {
 
 // dq.  Laid out as the forward pass: transposed scores, a lane owns a query.
 template <int DT, int ND>
-__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kernel(AttnArgs a, int row_tiles) {
+struct DqShared {
+    static constexpr int BK = 32;
+    char tile[2][2][BK * Tile<DT, ND>::PITCH];
+};
+
+template <int DT, int ND, bool SAFE>
+__device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_tiles, DqShared<DT, ND>& shared) {
     using T = Tile<DT, ND>;
-    constexpr int BK = 32;
-    __shared__ __attribute__((aligned(16))) char lds[2][2][BK * T::PITCH];
+    constexpr int BK = DqShared<DT, ND>::BK;
+    auto& lds = shared.tile;
     const int tid = threadIdx.x, l = tid & 63, wave = wave_id();
 
-    const WorkItem w = work_item(blockIdx.x, a.B * a.Hkv, row_tiles, a.causal);
+    const WorkItem w = work_item(id, a.B * a.Hkv, row_tiles, a.causal);
     const int tile = row_tiles - 1 - w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;
     const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
     const int rows = a.Sq * a.G;
@@ -114,14 +120,15 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
             settle<DT>(dp);
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(s[i] * c) * dp[i];
-            if (key0 < wr.all_lo || key0 + 32 > wr.all_hi) {
+            const bool part = key0 < wr.all_lo || key0 + 32 > wr.all_hi;
+            if (part) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (!sees(key0, i, mine)) s[i] = 0.0f;
             }
             Packed<DT> ds;
             ds.set(s);
-            trans_product<DT, ND>(lds[cur][0], kb * 32, tb, ds, acc);
+            trans_product<DT, ND, false, SAFE>(lds[cur][0], kb * 32, tb, ds, part, key0, mine, acc);
         }
         if (more) {
             kc.put(lds[cur ^ 1][0], tid);
@@ -131,28 +138,46 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
     }
 #pragma unroll
     for (int db = 0; db < ND; ++db) settle<DT>(acc[db]);
+    if (!SAFE && a.causal) {
+        const bool ok = sums_finite<ND>(acc);
+        if (l == 0) a.marks[id * 4 + wave] = !ok;
+    }
     if (live) store_rows<DT, ND>(a.dq.p + b * a.dq.sb + pos * a.dq.ss + head * a.dq.sh, acc, a.scale, a.D);
+}
+
+template <int DT, int ND>
+__global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kernel(AttnArgs a, int row_tiles) {
+    __shared__ __attribute__((aligned(16))) DqShared<DT, ND> shared;
+    attention_dq<DT, ND, false>(a, blockIdx.x, row_tiles, shared);
 }
 
 // dk and dv.  Scores as S = Q K^T: a lane owns a key.  Four waves of 32 keys
 // share tiles of 32 queries of one head, head after head.  V stays in
 // registers as an operand, K in LDS: both in registers beside 128 sums a lane
-// would leave one wave a SIMD, and at the longest bf16 rows even V's last
-// 96 bytes are kept in LDS (spilled, their reload waited for the next tile's
-// loads every time round).  Where there are few key tiles and many queries,
+// would leave one wave a SIMD, and where registers still do not suffice V's last
+// 32-byte steps are kept in LDS (spilled, their reload waited for the next
+// tile's loads every time round).  Where there are few key tiles and many queries,
 // the queries of a tile are cut into parts whose sums a second kernel joins.
 template <int DT, int ND>
-__global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void attention_dkv_kernel(AttnArgs a, int key_tiles) {
+struct DkvShared {
+    static constexpr int BQ = 32;
+    static constexpr int VL = DT != DT_BF16 ? 0 : ND == 4 ? 3 : ND == 2 ? 1 : 0;  // steps of V in LDS
+    char tile[2][2][BQ * Tile<DT, ND>::PITCH];
+    char k[128 * Tile<DT, ND>::PITCH];
+    char v[VL ? VL * 128 * 32 : 16];
+    float rowstat[2][2][BQ];
+};
+
+template <int DT, int ND, bool SAFE>
+__device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key_tiles, DkvShared<DT, ND>& shared) {
     using T = Tile<DT, ND>;
-    constexpr int BQ = 32;
-    __shared__ __attribute__((aligned(16))) char lds[2][2][BQ * T::PITCH];
-    __shared__ __attribute__((aligned(16))) char ldk[128 * T::PITCH];
-    constexpr int VL = DT == DT_BF16 && ND == 4 ? 3 : 0, VR = T::NS - VL;  // steps of V in LDS and in registers
-    __shared__ __attribute__((aligned(16))) char ldv[VL ? VL * 128 * 32 : 16];
-    __shared__ __attribute__((aligned(16))) float rowstat[2][2][BQ];
+    constexpr int BQ = DkvShared<DT, ND>::BQ, VR = T::NS - DkvShared<DT, ND>::VL;
+    auto& lds = shared.tile;
+    auto& rowstat = shared.rowstat;
+    char *ldk = shared.k, *ldv = shared.v;
     const int tid = threadIdx.x, l = tid & 63, wave = wave_id();
 
-    const WorkItem w = work_item(blockIdx.x, a.B * a.Hkv, key_tiles * a.nsplit_kv, a.causal);
+    const WorkItem w = work_item(id, a.B * a.Hkv, key_tiles * a.nsplit_kv, a.causal);
     const int tile = w.item / a.nsplit_kv, part_id = w.item % a.nsplit_kv;  // the first keys are seen by the most queries
     const int b = w.head / a.Hkv, hk = w.head % a.Hkv;
     const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk);
@@ -272,7 +297,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void at
             }
             Packed<DT> pk;
             pk.set(s);
-            trans_product<DT, ND>(lds[cur][1], 0, tb, pk, dv);
+            trans_product<DT, ND, false, SAFE>(lds[cur][1], 0, tb, pk, part, q0, positions(opaque(key)), dv);
             f32x16 dp = starts(1);
 #pragma unroll
             for (int x = 0; x < T::NS; ++x) {
@@ -289,7 +314,7 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void at
                     if (!sees(q0, e, seen)) s[e] = 0.0f;
             }
             pk.set(s);
-            trans_product<DT, ND>(lds[cur][0], 0, tb, pk, dk);
+            trans_product<DT, ND, false, SAFE>(lds[cur][0], 0, tb, pk, part, q0, positions(opaque(key)), dk);
         }
         if (i + 1 < i1) put(cur ^ 1);
         __syncthreads();
@@ -301,6 +326,10 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void at
         settle<DT>(dk[db]);
         settle<DT>(dv[db]);
     }
+    if (!SAFE && a.causal) {
+        const bool ok = sums_finite<ND>(dk) && sums_finite<ND>(dv);
+        if (l == 0) a.marks[(a.dq_items + id) * 4 + wave] = !ok;
+    }
     if (!live) return;
     if (a.nsplit_kv > 1) {
         const int64_t at = ((((int64_t)part_id * a.B + b) * a.Hkv + hk) * a.Sk + key) * a.D;
@@ -310,6 +339,35 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void at
         store_rows<DT, ND>(a.dk.p + b * a.dk.sb + key * a.dk.ss + hk * a.dk.sh, dk, a.scale, a.D);
         store_rows<DT, ND>(a.dv.p + b * a.dv.sb + key * a.dv.ss + hk * a.dv.sh, dv, 1.0f, a.D);
     }
+}
+
+template <int DT, int ND>
+__global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void attention_dkv_kernel(AttnArgs a,
+                                                                                                  int key_tiles) {
+    __shared__ __attribute__((aligned(16))) DkvShared<DT, ND> shared;
+    attention_dkv<DT, ND, false>(a, blockIdx.x, key_tiles, shared);
+}
+
+// The marked items of both kernels.
+template <int DT, int ND>
+__global__ __launch_bounds__(256, 1) void attention_backward_again_kernel(AttnArgs a, int row_tiles, int key_tiles,
+                                                                          int items) {
+    constexpr int BYTES = sizeof(DqShared<DT, ND>) > sizeof(DkvShared<DT, ND>) ? sizeof(DqShared<DT, ND>)
+                                                                              : sizeof(DkvShared<DT, ND>);
+    __shared__ __attribute__((aligned(16))) char shared[BYTES];
+    each_marked(
+        items,
+        [&](int i) {
+            const int4 m = reinterpret_cast<const int4*>(a.marks)[i];
+            return (m.x | m.y | m.z | m.w) != 0;
+        },
+        [&](int i) {
+            i = __builtin_amdgcn_readfirstlane(i);
+            if (i < a.dq_items)
+                attention_dq<DT, ND, true>(a, i, row_tiles, *reinterpret_cast<DqShared<DT, ND>*>(shared));
+            else
+                attention_dkv<DT, ND, true>(a, i - a.dq_items, key_tiles, *reinterpret_cast<DkvShared<DT, ND>*>(shared));
+        });
 }
 
 // Adds the parts of dk and dv in order, four elements a thread.
@@ -360,12 +418,15 @@ template <int DT, int ND>
 static void launch_backward(const AttnArgs& a, hipStream_t st) {
     const int64_t tiles = ((int64_t)a.Sq * a.G + 127) / 128, key_tiles = ((int64_t)a.Sk + 127) / 128;
     const int64_t heads = (int64_t)a.B * a.Hkv;
+    const int dq_items = (int)(heads * tiles), items = dq_items + (int)(heads * key_tiles * a.nsplit_kv);
     if (tiles > 0)
-        hipLaunchKernelGGL((attention_dq_kernel<DT, ND>), dim3((unsigned)(heads * tiles)), dim3(256), 0, st, a,
-                           (int)tiles);
+        hipLaunchKernelGGL((attention_dq_kernel<DT, ND>), dim3((unsigned)dq_items), dim3(256), 0, st, a, (int)tiles);
     if (key_tiles > 0)
-        hipLaunchKernelGGL((attention_dkv_kernel<DT, ND>), dim3((unsigned)(heads * key_tiles * a.nsplit_kv)), dim3(256),
-                           0, st, a, (int)key_tiles);
+        hipLaunchKernelGGL((attention_dkv_kernel<DT, ND>), dim3((unsigned)(items - dq_items)), dim3(256), 0, st, a,
+                           (int)key_tiles);
+    if (a.causal && items > 0)
+        hipLaunchKernelGGL((attention_backward_again_kernel<DT, ND>), dim3((unsigned)std::min(items, a.num_cus)),
+                           dim3(256), 0, st, a, (int)tiles, (int)key_tiles, items);
     if (a.nsplit_kv > 1) {
         const int64_t quads = heads * a.Sk * (a.D / 4);
         hipLaunchKernelGGL((attention_dkv_join_kernel<DT>), dim3((unsigned)((2 * quads + 255) / 256)), dim3(256), 0, st,

@@ -74,7 +74,7 @@ __device__ __forceinline__ int trans_base() {
     if constexpr (DT == DT_BF16)
         return Tile<DT, ND>::offset(4 * (l >> 5) + ((l & 15) >> 2), ((l >> 4) & 1) * 2 + ((l & 3) >> 1)) + (l & 1) * 8;
     else
-        return 0;
+        return l;  // the fp32 operand's address is formed from the lane
 }
 
 // One 32 x 32 product step; a and b are 16 bytes of A and B.
@@ -157,22 +157,26 @@ template <int DT, int ND> struct Columns;
 template <int ND>
 struct Columns<DT_BF16, ND> {
     using T = Tile<DT_BF16, ND>;
-    bf16x8 v[2][ND];
-    __device__ __forceinline__ void load(const char* tile, int r0, int base) {
+    static constexpr int STEPS = 2;
+    bf16x8 v[STEPS][ND];
+    __device__ static __forceinline__ bf16x8 one(const char* tile, int r0, int base, int t, int db) {
         constexpr int flip = (T::key(8) ^ T::key(0)) << 4;
         typedef __attribute__((address_space(3))) s16x4* lds_s4;
         typedef short s16x8 __attribute__((ext_vector_type(8)));
+        const char* at = tile + (r0 + 16 * t) * T::PITCH;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(at + (base ^ (db << 6))));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(at + 8 * T::PITCH + (base ^ (db << 6) ^ flip)));
+        const s16x8 x = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        return __builtin_bit_cast(bf16x8, x);
+    }
+    __device__ __forceinline__ void load(const char* tile, int r0, int base) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < STEPS; ++t)
 #pragma unroll
-            for (int db = 0; db < ND; ++db) {
-                const char* at = tile + (r0 + 16 * t) * T::PITCH;
-                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(at + (base ^ (db << 6))));
-                const s16x4 hi =
-                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(at + 8 * T::PITCH + (base ^ (db << 6) ^ flip)));
-                const s16x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                v[t][db] = __builtin_bit_cast(bf16x8, a);
-            }
+            for (int db = 0; db < ND; ++db) v[t][db] = one(tile, r0, base, t, db);
+    }
+    __device__ static __forceinline__ f32x16 step(const bf16x8& x, const Packed<DT_BF16>& b, int t, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, b.v[t], c, 0, 0, 0);
     }
     __device__ __forceinline__ void product(const Packed<DT_BF16>& b, f32x16* acc) const {
 #pragma unroll
@@ -181,36 +185,87 @@ struct Columns<DT_BF16, ND> {
             for (int db = 0; db < ND; ++db)
                 acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[t][db], b.v[t], acc[db], 0, 0, 0);
     }
+    template <typename F>
+    __device__ static __forceinline__ bf16x8 each(const bf16x8& x, F&& f) {
+        bf16x8 y;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = (__bf16)f((float)x[i]);
+        return y;
+    }
+    __device__ static __forceinline__ bool finite(const bf16x8& x) {
+        const uint4 w = __builtin_bit_cast(uint4, x);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        bool ok = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ok &= ((u[i] & 0x7f80u) != 0x7f80u) & ((u[i] & 0x7f800000u) != 0x7f800000u);
+        return ok;
+    }
 };
 template <int ND>
 struct Columns<DT_F32, ND> {
     using T = Tile<DT_F32, ND>;
-    float v[16][ND];
-    __device__ __forceinline__ void load(const char* tile, int r0, int) {
-        const int l = lane_id(), h = l >> 5;
+    static constexpr int STEPS = 16;
+    float v[STEPS][ND];
+    __device__ static __forceinline__ float one(const char* tile, int r0, int base, int t, int db) {
+        const int l = base, row = r0 + 8 * (t >> 2) + 4 * (l >> 5) + (t & 3), e = 32 * db + (l & 31);
+        return *reinterpret_cast<const float*>(tile + T::offset(row, e >> 2) + (e & 3) * 4);
+    }
+    __device__ __forceinline__ void load(const char* tile, int r0, int base) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int row = r0 + 8 * (i >> 2) + 4 * h + (i & 3);
+        for (int t = 0; t < STEPS; ++t)
 #pragma unroll
-            for (int db = 0; db < ND; ++db) {
-                const int e = 32 * db + (l & 31);
-                v[i][db] = *reinterpret_cast<const float*>(tile + T::offset(row, e >> 2) + (e & 3) * 4);
-            }
-        }
+            for (int db = 0; db < ND; ++db) v[t][db] = one(tile, r0, base, t, db);
+    }
+    __device__ static __forceinline__ f32x16 step(float x, const Packed<DT_F32>& b, int t, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x2f32(x, b.v[t], c, 0, 0, 0);
     }
     __device__ __forceinline__ void product(const Packed<DT_F32>& b, f32x16* acc) const {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int t = 0; t < STEPS; ++t)
 #pragma unroll
-            for (int db = 0; db < ND; ++db)
-                acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(v[i][db], b.v[i], acc[db], 0, 0, 0);
+            for (int db = 0; db < ND; ++db) acc[db] = step(v[t][db], b, t, acc[db]);
     }
+    template <typename F>
+    __device__ static __forceinline__ float each(float x, F&& f) {
+        return f(x);
+    }
+    __device__ static __forceinline__ bool finite(float x) { return isfinite(x); }
 };
+
+// Whether all 32 rows' elements are finite.  One operand at a time: only
+// blocks with masked pairs are looked through, and what they need in registers
+// must not be more than the plain product's.
 template <int DT, int ND>
-__device__ __forceinline__ void trans_product(const char* tile, int r0, int base, const Packed<DT>& b, f32x16* acc) {
-    Columns<DT, ND> c;
-    c.load(tile, r0, base);
-    c.product(b, acc);
+__device__ __forceinline__ bool rows_finite(const char* tile, int r0, int base) {
+    using C = Columns<DT, ND>;
+    const int at = opaque(base);  // loads of its own: shared ones would be held for the product
+    bool ok = true;
+#pragma unroll
+    for (int t = 0; t < C::STEPS; ++t)
+#pragma unroll
+        for (int db = 0; db < ND; ++db) {
+            ok &= C::finite(C::one(tile, r0, at, t, db));  // no branch: all lanes take part in each load
+            fence();
+        }
+    return __all(ok);
+}
+
+// The clean part of a product with a block that holds something not finite:
+// those elements count as 0.
+template <int DT, int ND>
+__device__ __forceinline__ void finite_product(const char* tile, int r0, int base, const Packed<DT>& b, f32x16* acc) {
+    using C = Columns<DT, ND>;
+    const int at = opaque(base);
+#pragma unroll
+    for (int db = 0; db < ND; ++db)
+#pragma unroll
+        for (int t = 0; t < C::STEPS; ++t) {
+            acc[db] = C::step(C::each(C::one(tile, r0, at, t, db), [](float x) { return isfinite(x) ? x : 0.0f; }), b, t,
+                              acc[db]);
+            fence();
+        }
+#pragma unroll
+    for (int db = 0; db < ND; ++db) settle<DT>(acc[db]);
 }
 
 // This lane's 16-byte groups of one global row (zero where !ok or past D).
@@ -365,6 +420,94 @@ __device__ __forceinline__ RowsRange rows_range(const AttnArgs& a, int first, in
 __device__ __forceinline__ bool sees(int key0, int i, const KeyRange& r) {
     const uint32_t k = (uint32_t)(key0 + 4 * (lane_id() >> 5) - r.lo) + (uint32_t)(8 * (i >> 2) + (i & 3));
     return k < (uint32_t)(r.hi - r.lo);
+}
+
+// acc += (32 rows of `tile` from r0, transposed) x b.  Where `part`, some pairs
+// are masked (the edge of a causal mask or a window): tile row k is seen by
+// this lane's column if row0 + k lies in [r.lo, r.hi).
+//
+// What a mask hides must not come through, but 0 x infinity is NaN.  A
+// workgroup whose sums are not all finite therefore leaves its item marked, and a
+// second kernel goes over the marked ones with SAFE: blocks with a masked pair
+// are then looked through, and one that holds something not finite is multiplied
+// without it, after which the results that do see such an element take it up
+// (its infinity if SIGNED, where b is not negative, else NaN).  In one kernel the
+// two would share registers: forward at head dimension 128 172 -> 196 us for
+// 4 x 2048 tokens, where the second kernel's look at the marks takes 2 us.
+template <int DT, int ND, bool SIGNED, bool SAFE>
+__device__ __forceinline__ void trans_product(const char* tile, int r0, int base, const Packed<DT>& b, bool part,
+                                              int row0, const KeyRange& r, f32x16* acc) {
+    if (SAFE && part && !rows_finite<DT, ND>(tile, r0, base)) {
+        finite_product<DT, ND>(tile, r0, base, b, acc);
+        const int h = opaque(lane_id() >> 5);  // nothing of this is worth registers over the kernel's loop
+        const uint32_t from = (uint32_t)opaque(row0 - r.lo), many = (uint32_t)(r.hi - r.lo);
+#pragma unroll 1
+        for (int k = 0; k < 32; ++k) {
+            const float take = from + (uint32_t)k < many ? 1.0f : 0.0f;
+#pragma unroll
+            for (int db = 0; db < ND; ++db)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float x[4];
+                    if constexpr (DT == DT_BF16) {
+                        const uint2 w =
+                            *reinterpret_cast<const uint2*>(tile + Tile<DT, ND>::offset(r0 + k, 4 * db + g) + 8 * h);
+                        x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xffff0000u);
+                        x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xffff0000u);
+                    } else {
+                        const float4 w =
+                            *reinterpret_cast<const float4*>(tile + Tile<DT, ND>::offset(r0 + k, 8 * db + 2 * g + h));
+                        x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool hit = !isfinite(x[i]) & (take != 0.0f);
+                        acc[db][4 * g + i] += hit ? (SIGNED ? x[i] : NAN) : 0.0f;
+                    }
+                    fence();
+                }
+        }
+    } else {
+        Columns<DT, ND> c;
+        c.load(tile, r0, base);
+        c.product(b, acc);
+    }
+}
+
+// Whether the wave's sums are finite, which nothing hidden can have touched then.
+template <int ND>
+__device__ __forceinline__ bool sums_finite(const f32x16* acc) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int db = 0; db < ND; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(acc[db][i]) & 0x7fffffffu);
+    return __all(top < 0x7f800000u);
+}
+
+// Runs f(item) for the items of [0, items) that marked(item) picks, the same for
+// the whole workgroup, item by item.  The picks of 256 items of this workgroup
+// are looked at together, so where there is none the kernel ends after one load.
+template <typename M, typename F>
+__device__ __forceinline__ void each_marked(int items, M&& marked, F&& f) {
+    __shared__ uint64_t picks[4];
+    for (int64_t first = blockIdx.x; first < items; first += (int64_t)gridDim.x * 256) {
+        const int64_t mine = first + (int64_t)threadIdx.x * gridDim.x;
+        const uint64_t found = __ballot(mine < items && marked((int)mine));
+        if (!__syncthreads_or(found != 0)) continue;
+        if ((threadIdx.x & 63) == 0) picks[threadIdx.x >> 6] = found;
+        __syncthreads();
+        for (int w = 0; w < 4; ++w) {
+            uint64_t left = picks[w];
+            while (left) {
+                const int lane = __builtin_ctzll(left);
+                left &= left - 1;
+                f((int)(first + (int64_t)(w * 64 + lane) * gridDim.x));
+                __syncthreads();  // the next item uses the same LDS
+            }
+        }
+        __syncthreads();
+    }
 }
 
 // Workgroup id -> (head of the batch, item of the head).  Workgroups are dealt

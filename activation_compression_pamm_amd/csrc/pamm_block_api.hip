@@ -53,7 +53,8 @@ int attention_sizes(const pamm_attention_t* a) {
     if (rows > kMaxSequence || mul(mul(a->batch, a->heads), a->seq_q) > kMaxSpan) return PAMM_ERR_SHAPE;
     const int64_t heads = mul(a->batch, a->heads_kv);
     if (mul(heads, 64) > kMaxSize || mul(heads, (rows + 127) / 128) > kMaxSize / 64 ||
-        mul(heads, (a->seq_k + 127) / 128) > kMaxSize / 8 || mul(heads, a->seq_k) > 4 * kMaxSize || mul(mul(a->batch, a->heads), a->seq_q) > 4 * kMaxSize)
+        mul(heads, (a->seq_k + 127) / 128) > kMaxSize / 64 || mul(heads, a->seq_k) > 4 * kMaxSize ||
+        mul(mul(a->batch, a->heads), a->seq_q) > 4 * kMaxSize)
         return PAMM_ERR_SHAPE;
     return PAMM_OK;
 }
@@ -127,6 +128,26 @@ int dkv_splits_of(const pamm_attention_t* a) {
                                       num_cus());
 }
 
+// Workspace of the backward pass: delta, the items' marks, parts of dk and dv.
+struct BackwardLayout {
+    size_t marks, part_dk, part_dv, total;
+    int64_t dq_items;
+    int parts;
+};
+BackwardLayout backward_layout(const pamm_attention_t* a) {
+    const int64_t heads = a->batch * a->heads_kv, rows = a->seq_q * (a->heads / a->heads_kv);
+    BackwardLayout L;
+    L.parts = dkv_splits_of(a);
+    L.dq_items = heads * ((rows + 127) / 128);
+    const int64_t items = L.dq_items + heads * ((a->seq_k + 127) / 128) * L.parts;
+    const size_t part = L.parts > 1 ? up256((size_t)L.parts * (size_t)(heads * a->seq_k * a->head_dim) * sizeof(float)) : 0;
+    L.marks = up256((size_t)(a->batch * a->heads * a->seq_q) * sizeof(float));
+    L.part_dk = L.marks + up256((size_t)items * 4 * sizeof(int32_t));
+    L.part_dv = L.part_dk + part;
+    L.total = L.part_dv + part;
+    return L;
+}
+
 int ws_check(const void* ws, size_t ws_bytes, size_t need) {
     if (need == 0) return PAMM_OK;
     if (!ws || ws_bytes < need) return PAMM_ERR_WORKSPACE;
@@ -180,10 +201,7 @@ int pamm_attention(const pamm_attention_t* a, void* ws, size_t ws_bytes, void* s
 }
 
 size_t pamm_attention_backward_workspace_size(const pamm_attention_t* a) {
-    if (attention_sizes(a) != PAMM_OK) return 0;
-    const size_t n = (size_t)dkv_splits_of(a);
-    const size_t part = n > 1 ? up256(n * (size_t)(a->batch * a->heads_kv * a->seq_k * a->head_dim) * sizeof(float)) : 0;
-    return up256((size_t)(a->batch * a->heads * a->seq_q) * sizeof(float)) + 2 * part;
+    return attention_sizes(a) == PAMM_OK ? backward_layout(a).total : 0;
 }
 
 int pamm_attention_backward(const pamm_attention_t* a, const pamm_heads_t* dout, const pamm_heads_t* dq,
@@ -202,14 +220,14 @@ int pamm_attention_backward(const pamm_attention_t* a, const pamm_heads_t* dout,
     r.dq = heads_arg(*dq, a->dtype);
     r.dk = heads_arg(*dk, a->dtype);
     r.dv = heads_arg(*dv, a->dtype);
-    r.delta = reinterpret_cast<float*>(ws);
-    r.nsplit_kv = dkv_splits_of(a);
-    if (r.nsplit_kv > 1) {
-        const size_t part = (size_t)r.nsplit_kv * (size_t)(a->batch * a->heads_kv * a->seq_k * a->head_dim);
-        char* at = reinterpret_cast<char*>(ws) + up256((size_t)(a->batch * a->heads * a->seq_q) * sizeof(float));
-        r.part_dk = reinterpret_cast<float*>(at);
-        r.part_dv = reinterpret_cast<float*>(at + up256(part * sizeof(float)));
-    }
+    const BackwardLayout L = backward_layout(a);
+    char* at = reinterpret_cast<char*>(ws);
+    r.delta = reinterpret_cast<float*>(at);
+    r.marks = reinterpret_cast<int32_t*>(at + L.marks);
+    r.dq_items = (int)L.dq_items;
+    r.nsplit_kv = L.parts;
+    r.part_dk = reinterpret_cast<float*>(at + L.part_dk);
+    r.part_dv = reinterpret_cast<float*>(at + L.part_dv);
     return status(pamm::run_attention_backward(r, a->dtype, reinterpret_cast<hipStream_t>(stream)));
 }
 

@@ -31,6 +31,8 @@ struct AttnArgs {
     int nsplit_kv;          // parts of the query axis (dk and dv)
     float* part_dk;         // [nsplit_kv x B x Hkv x Sk x D] when nsplit_kv > 1
     float* part_dv;
+    int32_t* marks;         // [dq items, dk/dv items][4 waves]: 1 if it has to be computed again
+    int dq_items;
     int num_cus;
 };
 

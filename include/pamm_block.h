@@ -78,6 +78,7 @@ size_t pamm_attention_workspace_size(const pamm_attention_t *a_host);
  *   lse[b, h, i] = log sum_j exp(s_ij)            s_ij = scale * <q_i, k_j>
  *   o[b, i, h]   = sum_j exp(s_ij - lse_i) v_j    over the keys i sees
  *
+ * What a mask hides does not come through, not even a NaN or an infinity.
  * A query that sees no key (and every i >= q_len[b]) gets o = 0 and
  * lse = -infinity; so does one whose every score is -infinity.  bf16: products
  * of bf16 values summed in fp32, probabilities rounded to bf16 for the
@@ -92,8 +93,9 @@ size_t pamm_attention_workspace_size(const pamm_attention_t *a_host);
  */
 int pamm_attention(const pamm_attention_t *a_host, void *ws, size_t ws_bytes, void *stream);
 
-/* Bytes of workspace pamm_attention_backward needs: <do, o> of every row, and
- * partial sums of dk and dv where few keys are shared by many queries. */
+/* Bytes of workspace pamm_attention_backward needs: <do, o> of every row, a
+ * mark for every workgroup, and partial sums of dk and dv where few keys are
+ * shared by many queries or the device would not be full. */
 size_t pamm_attention_backward_workspace_size(const pamm_attention_t *a_host);
 
 /*

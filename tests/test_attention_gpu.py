@@ -313,3 +313,67 @@ def test_empty_sizes():
         assert not o.any() and bool((lse == -float("inf")).all())
         dq, dk, dv = pamm.attention_backward(torch.ones_like(o), q, k, k, o, lse)
         assert not dq.any() and not dk.any() and not dv.any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Sq,Sk,D,window", [(150, 150, 64, 0), (150, 150, 128, 40), (100, 230, 40, 0), (9, 200, 96, 0),
+                                            (9, 200, 64, 5), (40, 3000, 64, 0)])
+def test_hidden_infinities_and_nans(dtype, Sq, Sk, D, window):
+    """Something not finite in a key or query reaches what sees it, and nothing else."""
+    rng = np.random.default_rng(8)
+    H, Hkv = 4, 2
+    kw = {"causal": True, "window": window}
+    x = {n: values(rng, s, dtype) for n, s in (("q", (1, Sq, H, D)), ("k", (1, Sk, Hkv, D)), ("v", (1, Sk, Hkv, D)),
+                                               ("do", (1, Sq, H, D)))}
+    ref = bo.attention(x["q"], x["k"], x["v"], x["do"], dtype=dtype, **kw)
+    m = bo.visible(Sq, Sk, Sq, Sk, True, window)
+
+    def run(changes):
+        d = {n: dev(t, dtype) for n, t in x.items()}
+        for name, at, head, value in changes:
+            d[name][0, at, head, D // 2] = value
+        o, lse = pamm.attention(d["q"], d["k"], d["v"], **kw)
+        return dict(zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *pamm.attention_backward(
+            d["do"], d["q"], d["k"], d["v"], o, lse, **kw))))
+
+    def clean(got, name, where, heads):
+        a, b = host(got[name])[0][where][:, heads], ref[name][0][where][:, heads]
+        close(name, a, b, ref[name + "_tol"][0][where][:, heads])
+
+    nan, inf = float("nan"), float("inf")
+    for j0 in sorted({0, Sk - Sq // 2 - 1, Sk - 1}):
+        hit = m[:, j0]
+        touched = m[hit].any(0)
+        for changes in ([("v", j0, 0, inf)], [("v", j0, 0, -inf)], [("v", j0, 0, nan)], [("k", j0, 0, nan), ("v", j0, 0, nan)]):
+            say("hidden key", j0, changes)
+            got = run(changes)
+            every, group = slice(None), slice(0, H // Hkv)  # the other heads are not touched at all
+            rest = slice(H // Hkv, H)
+            for n in ("o", "dq"):
+                clean(got, n, slice(None), rest)
+                clean(got, n, ~hit, group)
+            for n in ("dk", "dv"):
+                clean(got, n, slice(None), slice(1, Hkv))
+            for n in ("dk", "dv"):
+                clean(got, n, ~touched, slice(0, 1))
+            seen = host(got["o"])[0][hit][:, group, D // 2]
+            want = changes[0][3] if len(changes) == 1 else nan
+            assert np.array_equal(seen, np.full(seen.shape, want), equal_nan=True), (j0, changes)
+            if len(changes) == 1:  # only that column of the output
+                other = np.arange(D) != D // 2
+                close("o", host(got["o"])[0][hit][:, group][..., other], ref["o"][0][hit][:, group][..., other],
+                      ref["o_tol"][0][hit][:, group][..., other])
+                close("lse", got["lse"], ref["lse"], ref["lse_tol"])
+    for i0 in sorted({0, Sq // 3, Sq - 1}):
+        others = np.arange(Sq) != i0
+        for changes in ([("do", i0, 1, nan)], [("do", i0, 1, inf)], [("q", i0, 1, nan)]):
+            say("hidden query", i0, changes)
+            got = run(changes)
+            for n in ("o", "dq"):
+                clean(got, n, others, slice(None))
+            for n in ("dk", "dv"):
+                clean(got, n, ~m[i0], slice(None))
+                clean(got, n, slice(None), slice(1, Hkv))
+            keys = m[i0]
+            bad = host(got["dv"])[0][keys][:, 0, D // 2]
+            assert not np.isfinite(bad).any(), (i0, changes)
