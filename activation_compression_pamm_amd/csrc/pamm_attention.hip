@@ -173,10 +173,10 @@ __device__ __forceinline__ void attention_rows(const AttnArgs& a, int id, int ro
     if (marked) lse2 = NAN;
     const int64_t at = ((int64_t)b * a.H + head) * a.Sq + pos;
     if (a.nsplit > 1) {
-        store_rows<DT_F32, ND>(reinterpret_cast<char*>(a.part_o + (at * a.nsplit + split) * a.D), acc, inv, a.D);
+        store_rows<DT_F32, ND>(reinterpret_cast<char*>(a.part_o + (at * a.nsplit + split) * a.D), acc, inv, sum == 0.0f, a.D);
         if (l < 32) a.part_lse[at * a.nsplit + split] = lse2;
     } else {
-        store_rows<DT, ND>(a.o.p + b * a.o.sb + pos * a.o.ss + head * a.o.sh, acc, inv, a.D);
+        store_rows<DT, ND>(a.o.p + b * a.o.sb + pos * a.o.ss + head * a.o.sh, acc, inv, sum == 0.0f, a.D);
         if (l < 32) a.lse[at] = lse2 * kLn2;
     }
 }
@@ -327,7 +327,7 @@ __device__ __forceinline__ void attention_few(const AttnArgs& a, int id, FewShar
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     float* to = merged + row * OP + 32 * db + 8 * (i >> 2) + 4 * (l >> 5) + (i & 3);
-                    const float x = acc[db][i] * f;
+                    const float x = sum == 0.0f ? 0.0f : acc[db][i] * f;
                     *to = w == 0 ? x : *to + x;
                 }
         }

@@ -142,7 +142,7 @@ __device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_
         const bool ok = sums_finite<ND>(acc);
         if (l == 0) a.marks[id * 4 + wave] = !ok;
     }
-    if (live) store_rows<DT, ND>(a.dq.p + b * a.dq.sb + pos * a.dq.ss + head * a.dq.sh, acc, a.scale, a.D);
+    if (live) store_rows<DT, ND>(a.dq.p + b * a.dq.sb + pos * a.dq.ss + head * a.dq.sh, acc, a.scale, mine.hi == mine.lo, a.D);
 }
 
 template <int DT, int ND>
@@ -331,13 +331,15 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
         if (l == 0) a.marks[(a.dq_items + id) * 4 + wave] = !ok;
     }
     if (!live) return;
+    const KeyRange used = positions(key);
+    const bool empty = used.lo == used.hi;
     if (a.nsplit_kv > 1) {
         const int64_t at = ((((int64_t)part_id * a.B + b) * a.Hkv + hk) * a.Sk + key) * a.D;
-        store_rows<DT_F32, ND>(reinterpret_cast<char*>(a.part_dk + at), dk, a.scale, a.D);
-        store_rows<DT_F32, ND>(reinterpret_cast<char*>(a.part_dv + at), dv, 1.0f, a.D);
+        store_rows<DT_F32, ND>(reinterpret_cast<char*>(a.part_dk + at), dk, a.scale, empty, a.D);
+        store_rows<DT_F32, ND>(reinterpret_cast<char*>(a.part_dv + at), dv, 1.0f, empty, a.D);
     } else {
-        store_rows<DT, ND>(a.dk.p + b * a.dk.sb + key * a.dk.ss + hk * a.dk.sh, dk, a.scale, a.D);
-        store_rows<DT, ND>(a.dv.p + b * a.dv.sb + key * a.dv.ss + hk * a.dv.sh, dv, 1.0f, a.D);
+        store_rows<DT, ND>(a.dk.p + b * a.dk.sb + key * a.dk.ss + hk * a.dk.sh, dk, a.scale, empty, a.D);
+        store_rows<DT, ND>(a.dv.p + b * a.dv.sb + key * a.dv.ss + hk * a.dv.sh, dv, 1.0f, empty, a.D);
     }
 }
 

@@ -541,9 +541,10 @@ __device__ __forceinline__ WorkItem work_item(uint32_t id, uint32_t heads, uint3
 }
 
 // Writes ND blocks of 32 x 32 results that are transposed rows: this lane's
-// row `row` gets elements 32 db + 8 (i / 4) + 4 h + i % 4, scaled by f.
+// row `row` gets elements 32 db + 8 (i / 4) + 4 h + i % 4, scaled by f.  A row
+// that nothing was added to is 0, whatever its unused products made of it.
 template <int DT, int ND>
-__device__ __forceinline__ void store_rows(char* row, const f32x16* acc, float f, int D) {
+__device__ __forceinline__ void store_rows(char* row, const f32x16* acc, float f, bool empty, int D) {
     const int h = lane_id() >> 5;
 #pragma unroll
     for (int db = 0; db < ND; ++db) {
@@ -551,16 +552,17 @@ __device__ __forceinline__ void store_rows(char* row, const f32x16* acc, float f
         for (int g = 0; g < 4; ++g) {
             const int e = 32 * db + 8 * g + 4 * h;
             if (e >= D) continue;
-            const float x0 = acc[db][4 * g] * f, x1 = acc[db][4 * g + 1] * f, x2 = acc[db][4 * g + 2] * f,
-                        x3 = acc[db][4 * g + 3] * f;
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = empty ? 0.0f : acc[db][4 * g + i] * f;
             if constexpr (DT == DT_BF16) {
                 bf16x2 u, v;
-                u[0] = (__bf16)x0, u[1] = (__bf16)x1, v[0] = (__bf16)x2, v[1] = (__bf16)x3;
+                u[0] = (__bf16)x[0], u[1] = (__bf16)x[1], v[0] = (__bf16)x[2], v[1] = (__bf16)x[3];
                 uint2 w;
                 w.x = __builtin_bit_cast(uint32_t, u), w.y = __builtin_bit_cast(uint32_t, v);
                 *reinterpret_cast<uint2*>(row + 2 * e) = w;
             } else {
-                *reinterpret_cast<float4*>(row + 4 * e) = make_float4(x0, x1, x2, x3);
+                *reinterpret_cast<float4*>(row + 4 * e) = make_float4(x[0], x[1], x[2], x[3]);
             }
         }
     }

@@ -377,3 +377,22 @@ def test_hidden_infinities_and_nans(dtype, Sq, Sk, D, window):
             keys = m[i0]
             bad = host(got["dv"])[0][keys][:, 0, D // 2]
             assert not np.isfinite(bad).any(), (i0, changes)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("Sq", [5, 70])
+def test_rows_past_the_lengths_are_zero_beside_nans(dtype, causal, Sq):
+    rng = np.random.default_rng(9)
+    B, Sk, H, Hkv, D, Lq, Lk = 1, 80, 4, 2, 64, Sq - 3, 45
+    d = {n: dev(values(rng, s, dtype), dtype) for n, s in (("q", (B, Sq, H, D)), ("k", (B, Sk, Hkv, D)),
+                                                           ("v", (B, Sk, Hkv, D)), ("do", (B, Sq, H, D)))}
+    for n, at in (("q", 1), ("k", 3), ("v", 4), ("do", 0)):
+        d[n][:, at] = float("nan")
+    kw = {"causal": causal, "q_len": lens([Lq]), "kv_len": lens([Lk])}
+    o, lse = pamm.attention(d["q"], d["k"], d["v"], **kw)
+    dq, dk, dv = pamm.attention_backward(d["do"], d["q"], d["k"], d["v"], o, lse, **kw)
+    if not causal or 1 + Lk - Lq >= 4:  # query 1 sees the keys that hold NaNs
+        assert torch.isnan(o[:, 1]).all()
+    assert (o[:, Lq:] == 0).all() and (dq[:, Lq:] == 0).all() and bool((lse[:, :, Lq:] == -float("inf")).all())
+    assert (dk[:, Lk:] == 0).all() and (dv[:, Lk:] == 0).all()
