@@ -9,9 +9,9 @@
 // what comes out needs one multiplication and an exponential to be P, and one
 // more multiplication to be dS.
 //
-// Two kernels, each with its sums in registers and in a fixed order: one owns
-// queries and runs over keys (dq, and delta on the way), one owns keys and
-// runs over the queries of every head that shares them (dk, dv).  Forming P
+// Two kinds of workgroup, each with its sums in registers and in a fixed order:
+// one owns queries and runs over keys (dq, and delta on the way), one owns keys
+// and runs over the queries of every head that shares them (dk, dv).  Forming P
 // and dS in both costs 7 products instead of 5, and buys sums without atomics:
 // the results are bitwise repeatable and no fp32 copy of dq is kept.
 #include <algorithm>
@@ -39,6 +39,11 @@ __device__ __forceinline__ float dot16(const uint4& x, const uint4& y) {
     return sum;
 }
 
+// delta = <do, o> with o rounded to bf16 is off by 2^-8 |do||o| at random, and
+// dS = P (<do, v> - delta) with it; a row that sees few keys feels it most.  It
+// is also sum_j P_ij <do_i, v_j>: where the first 32 keys of a workgroup are all
+// that a wave's rows see, that sum, taken before the loop, corrects delta.
+
 // dq.  Laid out as the forward pass: transposed scores, a lane owns a query.
 template <int DT, int ND>
 struct DqShared {
@@ -46,7 +51,7 @@ struct DqShared {
     char tile[2][2][BK * Tile<DT, ND>::PITCH];
 };
 
-template <int DT, int ND, bool SAFE>
+template <int DT, int ND, bool ONE, bool SAFE>
 __device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_tiles, DqShared<DT, ND>& shared) {
     using T = Tile<DT, ND>;
     constexpr int BK = DqShared<DT, ND>::BK;
@@ -76,7 +81,6 @@ __device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_
     for (int s = 0; s < T::NS; ++s) delta += dot16<DT>(qf[s], dof[s]);
     delta = half_sum(delta);
     const int64_t at = ((int64_t)b * a.H + head) * a.Sq + pos;
-    if (live && l < 32) a.delta[at] = delta;
     load_row_operand<DT, ND>(qf, a.q.p + b * a.q.sb + pos * a.q.ss + head * a.q.sh, seen, a.D);
     if (a.scale < 0.0f)
 #pragma unroll
@@ -87,9 +91,6 @@ __device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_
     float start = start_of(live ? a.lse[at] : 0.0f, c);
     asm volatile("" : "+v"(start));  // as for the operands
 
-    f32x16 acc[ND];
-#pragma unroll
-    for (int db = 0; db < ND; ++db) acc[db] = f32x16{};
     TileCopy<DT, ND, BK, 256> kc, vc;
     if (t0 < t1) {
         kc.fetch(kbase + t0 * BK * a.k.ss, (int)a.k.ss, Lk - t0 * BK, a.D, tid);
@@ -98,6 +99,26 @@ __device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_
         vc.put(lds[0][1], tid);
     }
     __syncthreads();
+    if (DT == DT_BF16 && wr.begin < wr.end && wr.begin >= t0 * BK && wr.end <= t0 * BK + BK) {
+        const int rb = row_base<DT, ND>();
+        f32x16 s = splat(start), dp = splat(-delta);
+#pragma unroll
+        for (int i = 0; i < T::NS; ++i) {
+            s = mma_step<DT>(row_operand<DT, ND>(lds[0][0], 0, rb, i), qf[i], s);
+            dp = mma_step<DT>(row_operand<DT, ND>(lds[0][1], 0, rb, i), dof[i], dp);
+        }
+        settle<DT>(s);
+        settle<DT>(dp);
+        float off = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (sees(t0 * BK, i, mine)) off += __builtin_amdgcn_exp2f(s[i] * c) * dp[i];
+        delta += half_sum(off);
+    }
+    if (!SAFE && !ONE && live && l < 32) a.delta[at] = delta;
+    f32x16 acc[ND];
+#pragma unroll
+    for (int db = 0; db < ND; ++db) acc[db] = f32x16{};
     int cur = 0;
     for (int t = t0; t < t1; ++t, cur ^= 1) {
         const bool more = t + 1 < t1;
@@ -148,7 +169,7 @@ __device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_
 template <int DT, int ND>
 __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kernel(AttnArgs a, int row_tiles) {
     __shared__ __attribute__((aligned(16))) DqShared<DT, ND> shared;
-    attention_dq<DT, ND, false>(a, blockIdx.x, row_tiles, shared);
+    attention_dq<DT, ND, false, false>(a, blockIdx.x, row_tiles, shared);
 }
 
 // dk and dv.  Scores as S = Q K^T: a lane owns a key.  Four waves of 32 keys
@@ -168,7 +189,7 @@ struct DkvShared {
     float rowstat[2][2][BQ];
 };
 
-template <int DT, int ND, bool SAFE>
+template <int DT, int ND, bool ONE, bool SAFE>
 __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key_tiles, DkvShared<DT, ND>& shared) {
     using T = Tile<DT, ND>;
     constexpr int BQ = DkvShared<DT, ND>::BQ, VR = T::NS - DkvShared<DT, ND>::VL;
@@ -231,21 +252,38 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
 #pragma unroll
     for (int db = 0; db < ND; ++db) dk[db] = dv[db] = f32x16{};
 
-    TileCopy<DT, ND, BQ, 256> qc, oc;
+    using Copy = TileCopy<DT, ND, BQ, 256>;
+    Copy qc, oc, rc;  // q, do and, for delta, o
     float stat = 0.0f;
     auto fetch = [&](int g, int t) {
         const int head = hk * a.G + g, q0 = t * BQ;
         qc.fetch(a.q.p + b * a.q.sb + head * a.q.sh + q0 * a.q.ss, (int)a.q.ss, Lq - q0, a.D, tid);
         oc.fetch(a.dout.p + b * a.dout.sb + head * a.dout.sh + q0 * a.dout.ss, (int)a.dout.ss, Lq - q0, a.D, tid);
+        if constexpr (ONE)
+            rc.fetch(a.o.p + b * a.o.sb + head * a.o.sh + q0 * a.o.ss, (int)a.o.ss, Lq - q0, a.D, tid);
         const int r = tid % BQ;
         const int64_t at = ((int64_t)b * a.H + head) * a.Sq + q0 + r;
         stat = 0.0f;
-        if (tid < 2 * BQ && q0 + r < Lq) stat = tid < BQ ? a.lse[at] : a.delta[at];
+        if (tid < (ONE ? BQ : 2 * BQ) && q0 + r < Lq) stat = tid < BQ ? a.lse[at] : a.delta[at];
     };
     auto put = [&](int buf) {
         qc.put(lds[buf][0], tid);
         oc.put(lds[buf][1], tid);
-        if (tid < 2 * BQ) rowstat[buf][tid / BQ][tid % BQ] = tid < BQ ? start_of(stat, c) : -stat;
+        if constexpr (ONE) {
+            // the threads that copy a row are neighbours
+            static_assert((T::CPR & (T::CPR - 1)) == 0);
+#pragma unroll
+            for (int i = 0; i < Copy::PER; ++i) {
+                float d = dot16<DT>(oc.r[i], rc.r[i]);
+#pragma unroll
+                for (int m = 1; m < T::CPR; m <<= 1) d += shfl_xor(d, m);
+                const int at = tid + i * 256;
+                if (at < Copy::N && at % T::CPR == 0) rowstat[buf][1][at / T::CPR] = -d;
+            }
+            if (tid < BQ) rowstat[buf][0][tid] = start_of(stat, c);
+        } else if (tid < 2 * BQ) {
+            rowstat[buf][tid / BQ][tid % BQ] = tid < BQ ? start_of(stat, c) : -stat;
+        }
     };
     int t = n0, g = 0;
     if (i0 < i1) {
@@ -347,16 +385,39 @@ template <int DT, int ND>
 __global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void attention_dkv_kernel(AttnArgs a,
                                                                                                   int key_tiles) {
     __shared__ __attribute__((aligned(16))) DkvShared<DT, ND> shared;
-    attention_dkv<DT, ND, false>(a, blockIdx.x, key_tiles, shared);
+    attention_dkv<DT, ND, false, false>(a, blockIdx.x, key_tiles, shared);
 }
 
-// The marked items of both kernels.
+template <int DT, int ND>
+struct BackwardShared {
+    static constexpr int BYTES = sizeof(DqShared<DT, ND>) > sizeof(DkvShared<DT, ND>) ? sizeof(DqShared<DT, ND>)
+                                                                                     : sizeof(DkvShared<DT, ND>);
+    char bytes[BYTES];
+    __device__ __forceinline__ DqShared<DT, ND>& dq() { return *reinterpret_cast<DqShared<DT, ND>*>(bytes); }
+    __device__ __forceinline__ DkvShared<DT, ND>& dkv() { return *reinterpret_cast<DkvShared<DT, ND>*>(bytes); }
+};
+
+// Both in one launch, the dk/dv items, which take longer, first.  They form delta
+// themselves (reading o too) instead of waiting for the dq items': the sums of
+// a row's products go over the neighbouring threads that copy it, for which
+// their number must be a power of two.
+template <int ND> constexpr bool kOneKernel = ND != 3;
+
+template <int DT, int ND>
+__global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void attention_backward_kernel(
+    AttnArgs a, int row_tiles, int key_tiles, int dkv_items) {
+    __shared__ __attribute__((aligned(16))) BackwardShared<DT, ND> shared;
+    if ((int)blockIdx.x < dkv_items)
+        attention_dkv<DT, ND, true, false>(a, blockIdx.x, key_tiles, shared.dkv());
+    else
+        attention_dq<DT, ND, true, false>(a, blockIdx.x - dkv_items, row_tiles, shared.dq());
+}
+
+// The marked items of both.
 template <int DT, int ND>
 __global__ __launch_bounds__(256, 1) void attention_backward_again_kernel(AttnArgs a, int row_tiles, int key_tiles,
                                                                           int items) {
-    constexpr int BYTES = sizeof(DqShared<DT, ND>) > sizeof(DkvShared<DT, ND>) ? sizeof(DqShared<DT, ND>)
-                                                                              : sizeof(DkvShared<DT, ND>);
-    __shared__ __attribute__((aligned(16))) char shared[BYTES];
+    __shared__ __attribute__((aligned(16))) BackwardShared<DT, ND> shared;
     each_marked(
         items,
         [&](int i) {
@@ -366,9 +427,9 @@ __global__ __launch_bounds__(256, 1) void attention_backward_again_kernel(AttnAr
         [&](int i) {
             i = __builtin_amdgcn_readfirstlane(i);
             if (i < a.dq_items)
-                attention_dq<DT, ND, true>(a, i, row_tiles, *reinterpret_cast<DqShared<DT, ND>*>(shared));
+                attention_dq<DT, ND, kOneKernel<ND>, true>(a, i, row_tiles, shared.dq());
             else
-                attention_dkv<DT, ND, true>(a, i - a.dq_items, key_tiles, *reinterpret_cast<DkvShared<DT, ND>*>(shared));
+                attention_dkv<DT, ND, kOneKernel<ND>, true>(a, i - a.dq_items, key_tiles, shared.dkv());
         });
 }
 
@@ -416,16 +477,40 @@ int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t
     return (int)std::max<int64_t>(1, std::min<int64_t>(n, 8));
 }
 
+// One launch or two?  One saves the wait between two kernels and fills the end
+// of the first with the second; two form delta once only.  With all items on
+// the device in two rounds of resident workgroups one launch is the faster
+// (bf16, causal: 1 x 512 tokens, 16 heads of 128, 43 us against 62; 4 x 1024, 16
+// of 128, 111 / 120; 8 x 1024, 12 of 64, 73 / 86; fp32: 4 x 128, 16 of 128, 51 / 82),
+// with more it loses (4 x 2048, 16 of 128: 340 / 295; 8 x 4096, 12 of 64: 843 / 777).
+// Without a causal mask workgroups end together, and rows above 64 gain in one
+// round only (4 x 1024, 16 of 128: 156 / 144; 4 x 512: 56 / 63).
+template <int DT, int ND>
+static bool one_backward_kernel(const AttnArgs& a, int64_t items) {
+    const int resident = DT != DT_BF16 ? 1 : ND <= 2 ? 3 : 2, rounds = ND <= 2 || a.causal ? 2 : 1;
+    return kOneKernel<ND> && items <= (int64_t)a.num_cus * resident * rounds;
+}
+
+
 template <int DT, int ND>
 static void launch_backward(const AttnArgs& a, hipStream_t st) {
     const int64_t tiles = ((int64_t)a.Sq * a.G + 127) / 128, key_tiles = ((int64_t)a.Sk + 127) / 128;
     const int64_t heads = (int64_t)a.B * a.Hkv;
     const int dq_items = (int)(heads * tiles), items = dq_items + (int)(heads * key_tiles * a.nsplit_kv);
-    if (tiles > 0)
-        hipLaunchKernelGGL((attention_dq_kernel<DT, ND>), dim3((unsigned)dq_items), dim3(256), 0, st, a, (int)tiles);
-    if (key_tiles > 0)
-        hipLaunchKernelGGL((attention_dkv_kernel<DT, ND>), dim3((unsigned)(items - dq_items)), dim3(256), 0, st, a,
-                           (int)key_tiles);
+    bool one = false;
+    if constexpr (kOneKernel<ND>) {
+        one = one_backward_kernel<DT, ND>(a, items);
+        if (one && items > 0)
+            hipLaunchKernelGGL((attention_backward_kernel<DT, ND>), dim3((unsigned)items), dim3(256), 0, st, a,
+                               (int)tiles, (int)key_tiles, items - dq_items);
+    }
+    if (!one) {
+        if (tiles > 0)
+            hipLaunchKernelGGL((attention_dq_kernel<DT, ND>), dim3((unsigned)dq_items), dim3(256), 0, st, a, (int)tiles);
+        if (key_tiles > 0)
+            hipLaunchKernelGGL((attention_dkv_kernel<DT, ND>), dim3((unsigned)(items - dq_items)), dim3(256), 0, st, a,
+                               (int)key_tiles);
+    }
     if (a.causal && items > 0)
         hipLaunchKernelGGL((attention_backward_again_kernel<DT, ND>), dim3((unsigned)std::min(items, a.num_cus)),
                            dim3(256), 0, st, a, (int)tiles, (int)key_tiles, items);
