@@ -374,49 +374,57 @@ __global__ __launch_bounds__(256, 1) void attention_few_again_kernel(AttnArgs a,
         [&](int id) { attention_few<DT, ND, true>(a, __builtin_amdgcn_readfirstlane(id), shared); });
 }
 
-// Joins the parts of one row: weights 2^(lse_part - lse).  One wave a row; lane
-// s holds part s's weight (there are at most 64 parts), then every lane adds up
-// two columns, eight parts' loads at a time.
+// Joins the parts of one row: weights 2^(lse_part - lse).  Half a wave a row:
+// lane s holds the weights of parts s and s + 32 (there are at most 64), then
+// every lane adds up four columns, eight parts' loads at a time.  Bound by
+// reading the parts: 3 of 32768 rows of 128, 59 MB in all, 12.2 us, 4.8 TB/s (a
+// wave a row with 4 bytes a lane: 17 us with 2 parts).
 template <int DT>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
-    const int64_t at = (int64_t)blockIdx.x * 4 + wave_id();
-    if (at >= (int64_t)a.B * a.H * a.Sq) return;
-    const int l = threadIdx.x & 63;
-    const float* po = a.part_o + at * a.nsplit * a.D;
-    const float lse = l < a.nsplit ? a.part_lse[at * a.nsplit + l] : -INFINITY;
-    float m = lse;
+    const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const bool live = at < (int64_t)a.B * a.H * a.Sq;
+    const int l = threadIdx.x & 31, n = live ? a.nsplit : 0;
+    const float* part = a.part_lse + at * a.nsplit;
+    const float lse0 = l < n ? part[l] : -INFINITY, lse1 = l + 32 < n ? part[l + 32] : -INFINITY;
+    float m = fmaxf(lse0, lse1);
 #pragma unroll
-    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, shfl_xor(m, x));
-    const float w = __builtin_amdgcn_exp2f(lse - (m == -INFINITY ? 0.0f : m));
-    float total = w;
+    for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, shfl_xor(m, x));
+    const float ref = m == -INFINITY ? 0.0f : m;
+    const float w0 = __builtin_amdgcn_exp2f(lse0 - ref), w1 = __builtin_amdgcn_exp2f(lse1 - ref);
+    float total = w0 + w1;
 #pragma unroll
-    for (int x = 1; x < 64; x <<= 1) total += shfl_xor(total, x);
+    for (int x = 1; x < 32; x <<= 1) total += shfl_xor(total, x);
     // parts that saw nothing hold zeros
-    const bool c0 = l < a.D, c1 = l + 64 < a.D;
-    float v0 = 0.0f, v1 = 0.0f;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o + at * a.nsplit * a.D) + l;
+    const bool mine = 4 * l < a.D;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int s = 0; s < a.nsplit; s += 8) {
-        float x0[8], x1[8];
+        float4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = mine && s + i < n ? po[(s + i) * (a.D / 4)] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            x0[i] = c0 && s + i < a.nsplit ? po[(s + i) * a.D + l] : 0.0f;
-            x1[i] = c1 && s + i < a.nsplit ? po[(s + i) * a.D + l + 64] : 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float u = __shfl(w, (s + i) & 63, 64);
-            v0 = fmaf(u, x0[i], v0);
-            v1 = fmaf(u, x1[i], v1);
+            const float u = __shfl(s < 32 ? w0 : w1, (s + i) & 31, 32);
+            sum.x = fmaf(u, x[i].x, sum.x), sum.y = fmaf(u, x[i].y, sum.y);
+            sum.z = fmaf(u, x[i].z, sum.z), sum.w = fmaf(u, x[i].w, sum.w);
         }
     }
+    if (!live) return;
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     const int64_t pos = at % a.Sq, bh = at / a.Sq;
     char* o = a.o.p + (bh / a.H) * a.o.sb + pos * a.o.ss + (bh % a.H) * a.o.sh;
-    if constexpr (DT == DT_BF16) {
-        if (c0) reinterpret_cast<__bf16*>(o)[l] = (__bf16)(v0 * inv);
-        if (c1) reinterpret_cast<__bf16*>(o)[l + 64] = (__bf16)(v1 * inv);
-    } else {
-        if (c0) reinterpret_cast<float*>(o)[l] = v0 * inv;
-        if (c1) reinterpret_cast<float*>(o)[l + 64] = v1 * inv;
+    if (mine) {
+        if constexpr (DT == DT_BF16) {
+            bf16x2 u, v;
+            u[0] = (__bf16)(sum.x * inv), u[1] = (__bf16)(sum.y * inv);
+            v[0] = (__bf16)(sum.z * inv), v[1] = (__bf16)(sum.w * inv);
+            *reinterpret_cast<uint2*>(o + 8 * l) =
+                make_uint2(__builtin_bit_cast(uint32_t, u), __builtin_bit_cast(uint32_t, v));
+        } else {
+            *reinterpret_cast<float4*>(o + 16 * l) =
+                make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+        }
     }
     if (l == 0) a.lse[at] = total == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(total)) * kLn2;
 }
@@ -426,12 +434,15 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 // even them out: 8 workgroups a unit (64 sequences of up to 8192, 8 heads of
 // 128: 229 us, against 245 with 4 and 272 with 2).  Equal lengths need no more
 // than fill the device (369 us with 2, 389 with 4, 394 with 8).  A part is at
-// least 256 keys, two blocks a wave; 512 for a tile of many rows.
+// least 256 keys, two blocks a wave; 512 for a tile of many rows, of which 3
+// workgroups a unit run at once (2 x 512 queries over 8192 keys, 32/8 heads of
+// 128: 166 us, 169 with 2, 177 with 4; 2048 of 2048, 16 heads of 128: 50, 53
+// and 58; against 4 x 128 over 4096: 64, 61 and 73).
 int attention_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, bool lengths, int num_cus) {
     const int64_t rows = Sq * G;
     const bool few = rows <= kFewRows;
     const int64_t tiles = few ? 1 : (rows + 127) / 128;
-    const int64_t blocks = B * Hkv * tiles, want = (few && lengths ? 8 : 2) * (int64_t)num_cus, least = few ? 256 : 512;
+    const int64_t blocks = B * Hkv * tiles, want = (!few ? 3 : lengths ? 8 : 2) * (int64_t)num_cus, least = few ? 256 : 512;
     if (blocks == 0 || blocks >= want) return 1;
     int64_t n = (want + blocks - 1) / blocks;
     n = std::min(n, (Sk + least - 1) / least);
@@ -453,7 +464,7 @@ static void launch_attention(const AttnArgs& a, hipStream_t st) {
         if (hides) hipLaunchKernelGGL((attention_again_kernel<DT, ND>), again, dim3(256), 0, st, a, (int)tiles, items);
     }
     if (a.nsplit > 1) {
-        const dim3 grid((unsigned)(((int64_t)a.B * a.H * a.Sq + 3) / 4));
+        const dim3 grid((unsigned)(((int64_t)a.B * a.H * a.Sq + 7) / 8));
         hipLaunchKernelGGL((attention_join_kernel<DT>), grid, dim3(256), 0, st, a);
     }
 }
