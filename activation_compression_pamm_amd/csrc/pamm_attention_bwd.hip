@@ -44,11 +44,17 @@ __device__ __forceinline__ float dot16(const uint4& x, const uint4& y) {
 // also sum_j P_ij <do_i, v_j>: where the first 32 keys of a workgroup are all that
 // a wave's rows see, that sum corrects delta (dk of 300 tokens, 8 heads of 64,
 // causal: relative error 0.0025 -> 0.0024, of 20 tokens 0.0028 -> 0.0024, where
-// the rounding of an exact result is 0.0017 and that of dS as much; dq of 1024 tokens: below
-// 0.0024 from 0.0025).  The dq side does it before its loop; inside, it cost a
-// tenth.
+// the rounding of an exact result is 0.0017 and that of dS as much).  The dq side
+// does it before its loop; inside, it cost a tenth.  With a window of up to 32
+// keys every row sees few, and the dq side goes over the keys twice (window 8: dq
+// and dk 0.0027 -> 0.0024).
+__device__ __host__ inline bool short_window(const AttnArgs& a) { return a.window > 0 && a.window <= 32; }
 
 // dq.  Laid out as the forward pass: transposed scores, a lane owns a query.
+// Tiles of 32 keys, not 64: three waves a SIMD at D = 64 (8 x 1024, 12 heads: 1.7 us
+// less) and fewer registers above.  Three products for each pair; bound as the
+// forward pass (matrix unit busy 41% of the cycles, vector instructions 34%).
+// 4 x 2048 tokens, 32 heads of 128: 280 us, 736 TFLOP/s; 8192, 32/8 of 64: 415 us, 993.
 template <int DT, int ND>
 struct DqShared {
     static constexpr int BK = 32;
@@ -103,27 +109,45 @@ __device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_
         vc.put(lds[0][1], tid);
     }
     __syncthreads();
-    if (DT == DT_BF16 && wr.begin < wr.end && wr.begin >= t0 * BK && wr.end <= t0 * BK + BK) {
-        const int rb = row_base<DT, ND>();
-        f32x16 s = splat(start), dp = splat(-delta);
-#pragma unroll
-        for (int i = 0; i < T::NS; ++i) {
-            s = mma_step<DT>(row_operand<DT, ND>(lds[0][0], 0, rb, i), qf[i], s);
-            dp = mma_step<DT>(row_operand<DT, ND>(lds[0][1], 0, rb, i), dof[i], dp);
-        }
-        settle<DT>(s);
-        settle<DT>(dp);
+    // delta corrected (see above): all tiles first where a window is short, then the first again
+    int cur = 0;
+    if constexpr (DT == DT_BF16) {
+        const bool whole = !ONE && t1 - t0 > 1 && short_window(a);
+        const int rb = row_base<DT, ND>(), tp = whole ? t1 : t0 + 1;
         float off = 0.0f;
+        for (int t = t0; t < tp; ++t) {
+            const int next = t + 1 < tp ? t + 1 : t0, key0 = t * BK;
+            if (whole) {
+                kc.fetch(kbase + next * BK * a.k.ss, (int)a.k.ss, Lk - next * BK, a.D, tid);
+                vc.fetch(vbase + next * BK * a.v.ss, (int)a.v.ss, Lk - next * BK, a.D, tid);
+            }
+            if (wr.begin < wr.end &&
+                (whole ? key0 < wr.end && key0 + BK > wr.begin : wr.begin >= key0 && wr.end <= key0 + BK)) {
+                f32x16 s = splat(start), dp = splat(-delta);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (sees(t0 * BK, i, mine)) off += __builtin_amdgcn_exp2f(s[i] * c) * dp[i];
+                for (int i = 0; i < T::NS; ++i) {
+                    s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], 0, rb, i), qf[i], s);
+                    dp = mma_step<DT>(row_operand<DT, ND>(lds[cur][1], 0, rb, i), dof[i], dp);
+                }
+                settle<DT>(s);
+                settle<DT>(dp);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (sees(key0, i, mine)) off += __builtin_amdgcn_exp2f(s[i] * c) * dp[i];
+            }
+            if (whole) {
+                cur ^= 1;
+                kc.put(lds[cur][0], tid);
+                vc.put(lds[cur][1], tid);
+                __syncthreads();
+            }
+        }
         delta += half_sum(off);
     }
     if (!SAFE && !ONE && live && l < 32) a.delta[at] = delta;
     f32x16 acc[ND];
 #pragma unroll
     for (int db = 0; db < ND; ++db) acc[db] = f32x16{};
-    int cur = 0;
     for (int t = t0; t < t1; ++t, cur ^= 1) {
         const bool more = t + 1 < t1;
         if (more) {
@@ -183,6 +207,9 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
 // 32-byte steps are kept in LDS (spilled, their reload waited for the next
 // tile's loads every time round).  Where there are few key tiles and many queries,
 // the queries of a tile are cut into parts whose sums a second kernel joins.
+// Four products for each pair; with two waves a SIMD waves wait 45% of their
+// cycles and the matrix unit is busy 36%.  4 x 2048 tokens, 32 heads of 128: 405 us,
+// 679 TFLOP/s; 8192, 32/8 of 64: 652 us, 843.
 template <int DT, int ND>
 struct DkvShared {
     static constexpr int BQ = 32;
@@ -363,7 +390,20 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
                 const int row = (l & 1) * 16 + (l & 2) * 4 + (l >> 2 & 1) * 2 + (l >> 3 & 1) + quad;
                 if (!(l & 16)) rowstat[cur][1][row] -= off;
             }
-            f32x16 s = probabilities();
+            f32x16 s = starts(0), dp = starts(1);
+#pragma unroll
+            for (int x = 0; x < T::NS; ++x)
+                s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], 0, rb, x),
+                                 row_operand<DT, ND>(ldk, wave * 32, rb, x), s);
+#pragma unroll
+            for (int x = 0; x < T::NS; ++x) {
+                const uint4 v = x < VR ? vf[x] : *reinterpret_cast<const uint4*>(vl + (x - VR) * 128 * 32);
+                dp = mma_step<DT>(row_operand<DT, ND>(lds[cur][1], 0, rb, x), v, dp);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(s[e] * c);
+            
+            settle<DT>(dp);
             // some pair of this block is masked?
             bool part = w0 + 32 > Lk || q0 + BQ > Lq;
             if (a.causal) {
@@ -379,7 +419,6 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
             Packed<DT> pk;
             pk.set(s);
             trans_product<DT, ND, false, SAFE>(lds[cur][1], 0, tb, pk, part, q0, positions(opaque(key)), dv);
-            const f32x16 dp = dout_v();
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[e] *= dp[e];
             if (part) {  // P is 0 there; keep what is not finite out as well
@@ -450,7 +489,8 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void at
         attention_dq<DT, ND, true, false>(a, blockIdx.x - dkv_items, row_tiles, shared.dq());
 }
 
-// The marked items of both.
+// The marked items of both.  With none marked, as ever but for a NaN or an infinity
+// that a mask hides, a launch and a look at the marks: 4 to 5 us.
 template <int DT, int ND>
 __global__ __launch_bounds__(256, 1) void attention_backward_again_kernel(AttnArgs a, int row_tiles, int key_tiles,
                                                                           int items) {
@@ -470,7 +510,8 @@ __global__ __launch_bounds__(256, 1) void attention_backward_again_kernel(AttnAr
         });
 }
 
-// Adds the parts of dk and dv in order, four elements a thread.
+// Adds the parts of dk and dv in order, four elements a thread.  Bound by reading
+// them: 8192 keys, 8 heads of 64, 4 parts, 143 MB with the result: 24 us, 5.9 TB/s.
 template <int DT>
 __global__ __launch_bounds__(256) void attention_dkv_join_kernel(AttnArgs a) {
     const int64_t quads = (int64_t)a.B * a.Hkv * a.Sk * (a.D / 4), i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -525,6 +566,8 @@ int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t
 template <int DT, int ND>
 static bool one_backward_kernel(const AttnArgs& a, int64_t items) {
     const int resident = DT != DT_BF16 ? 1 : ND <= 2 ? 3 : 2, rounds = ND <= 2 || a.causal ? 2 : 1;
+    // delta of a short window comes from the dq side
+    if (DT == DT_BF16 && a.causal && short_window(a)) return false;
     return kOneKernel<ND> && items <= (int64_t)a.num_cus * resident * rounds;
 }
 
