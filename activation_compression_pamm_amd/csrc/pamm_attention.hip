@@ -26,19 +26,23 @@ namespace pamm {
 // 2^kSlack: until then probabilities up to 2^kSlack are summed against the old
 // reference, which fp32 sums and bf16 products hold with the same relative
 // precision, and the ND x 16 multiplications of a rescale are skipped.
-constexpr float kSlack = 8.0f;
+constexpr float kSlack = 8.0f, kMost = 256.0f;  // kMost = 2^kSlack
 
 struct Running {
     float m, l;  // m in log2 units; l: this lane's keys only
 };
 
-// s (raw products; masked ones already -inf) becomes the probabilities.
-template <int ND>
-__device__ __forceinline__ void softmax_update(f32x16& s, float c, Running& st, f32x16* acc) {
+__device__ __forceinline__ float largest(const f32x16& s) {
     float top = s[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-    top = half_max(top) * c;
+    return half_max(top);
+}
+
+// s (raw products; masked ones already -inf) becomes the probabilities.
+template <int ND>
+__device__ __forceinline__ void softmax_update(f32x16& s, float c, Running& st, f32x16* acc) {
+    const float top = largest(s) * c;
     if (__any(top > st.m + kSlack)) {
         const float m = fmaxf(st.m, top);
         const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
@@ -57,6 +61,35 @@ __device__ __forceinline__ void softmax_update(f32x16& s, float c, Running& st, 
         sum += s[i];
     }
     st.l += sum;
+}
+
+// The same without looking for the maximum: the sum of the probabilities tells
+// whether some are above the slack.  A row that saw nothing yet has the reference
+// kUnseen, against which whatever it sees is infinite (or, for a score that low,
+// right).  For rows up to 64 in bf16, where the softmax of a block takes longer than
+// its products (8192 tokens, 32/8 heads of 64: 324 -> 311 us); with heads of 128 it
+// gains nothing (4 x 2048 tokens: 176 and 177 us).
+constexpr float kUnseen = -3.402823466e38f;
+
+__device__ __forceinline__ float probabilities(f32x16& s, float c, float ref) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -ref));
+        sum += s[i];
+    }
+    return sum;
+}
+
+template <int ND>
+__device__ __forceinline__ void raise_reference(const f32x16& s, float c, Running& st, f32x16* acc) {
+    const float m = fmaxf(st.m, largest(s) * c), f = __builtin_amdgcn_exp2f(st.m - m);
+    st.l *= f;
+#pragma unroll
+    for (int db = 0; db < ND; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[db][i] *= f;
+    st.m = m;
 }
 
 __device__ __forceinline__ void mask_block(f32x16& s, int key0, const KeyRange& r) {
@@ -79,7 +112,7 @@ __device__ __forceinline__ float score_factor(float scale) { return fmaxf(fabsf(
 // turns: at that size the matrix unit is busy 40% of the cycles, vector
 // instructions issue in 52%, and the clock falls below 2 GHz.  Without loads,
 // barriers or softmax it is 3%, 3% and 0% faster.  182 us, 755 TFLOP/s of the
-// pairs that the mask leaves; 8192 tokens, 32/8 heads of 64: 340 us, 810; 8 x
+// pairs that the mask leaves; 8192 tokens, 32/8 heads of 64: 311 us, 885; 8 x
 // 1024, 12 heads of 64: 30.5 us, 420, the end of a 768-workgroup launch.
 template <int DT, int ND>
 struct RowsShared {
@@ -91,6 +124,7 @@ template <int DT, int ND, bool SAFE>
 __device__ __forceinline__ void attention_rows(const AttnArgs& a, int id, int row_tiles, RowsShared<DT, ND>& shared) {
     using T = Tile<DT, ND>;
     constexpr int BK = RowsShared<DT, ND>::BK;
+    constexpr bool BY_SUM = DT == DT_BF16 && ND <= 2;
     auto& lds = shared.tile;
     const int tid = threadIdx.x, l = tid & 63, wave = wave_id();
 
@@ -130,7 +164,7 @@ __device__ __forceinline__ void attention_rows(const AttnArgs& a, int id, int ro
     f32x16 acc[ND];
 #pragma unroll
     for (int db = 0; db < ND; ++db) acc[db] = f32x16{};
-    Running st{-INFINITY, 0.0f};
+    Running st{BY_SUM ? kUnseen : -INFINITY, 0.0f};
 
     TileCopy<DT, ND, BK, 256> kc, vc;
     if (t0 < t1) {
@@ -152,14 +186,28 @@ __device__ __forceinline__ void attention_rows(const AttnArgs& a, int id, int ro
         for (int kb = 0; kb < BK / 32; ++kb) {
             const int key0 = t * BK + kb * 32;
             if (key0 >= wr.end || key0 + 32 <= wr.begin) continue;
-            f32x16 s{};
-#pragma unroll
-            for (int i = 0; i < T::NS; ++i)
-                s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], kb * 32, rb, i), qf[i], s);
-            settle<DT>(s);
             const bool part = key0 < wr.all_lo || key0 + 32 > wr.all_hi;
-            if (part) mask_block(s, key0, mine);
-            softmax_update<ND>(s, c, st, acc);
+            auto scores = [&] {
+                f32x16 s{};
+#pragma unroll
+                for (int i = 0; i < T::NS; ++i)
+                    s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], kb * 32, rb, i), qf[i], s);
+                settle<DT>(s);
+                if (part) mask_block(s, key0, mine);
+                return s;
+            };
+            f32x16 s = scores();
+            if constexpr (BY_SUM) {
+                float sum = probabilities(s, c, st.m);
+                if (__any(sum > kMost)) {  // the first block of a row, then rarely: form the scores again
+                    s = scores();
+                    raise_reference<ND>(s, c, st, acc);
+                    sum = probabilities(s, c, st.m);
+                }
+                st.l += sum;
+            } else {
+                softmax_update<ND>(s, c, st, acc);
+            }
             Packed<DT> p;
             p.set(s);
             trans_product<DT, ND, true, SAFE>(lds[cur][1], kb * 32, tb, p, part, key0, mine, acc);

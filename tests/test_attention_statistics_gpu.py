@@ -1,0 +1,80 @@
+"""GPU: attention's running softmax statistics where they move, and the
+precision of its gradients, against the 64-bit definition (tests/block_oracle.py)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import activation_compression_pamm_amd as pamm
+import block_oracle as bo
+from test_attention_gpu import close, dev, lens, say, values
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+
+def compare(q, k, v, do, dtype, **kw):
+    ref = bo.attention(q, k, v, do, dtype=dtype, **kw)
+    gk = dict(kw, q_len=lens(kw.get("q_len")), kv_len=lens(kw.get("kv_len")))
+    qd, kd, vd, dod = (dev(x, dtype) for x in (q, k, v, do))
+    o, lse = pamm.attention(qd, kd, vd, **gk)
+    close("o", o, ref["o"], ref["o_tol"])
+    close("lse", lse, ref["lse"], ref["lse_tol"])
+    for n, t in zip(("dq", "dk", "dv"), pamm.attention_backward(dod, qd, kd, vd, o, lse, **gk)):
+        close(n, t, ref[n], ref[n + "_tol"])
+
+
+# Factors of the keys along their sequence: the largest score of a block of 32
+# rises or falls by far more than 2^8 from block to block, stays, or leaps once.
+PATHS = {"rising": lambda n: np.linspace(0.1, 20.0, n), "falling": lambda n: np.linspace(20.0, 0.1, n),
+         "leap": lambda n: np.where(np.arange(n) == n // 2, 40.0, 1.0),
+         "late": lambda n: np.where(np.arange(n) == n - 1, 40.0, 0.01)}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("path", sorted(PATHS))
+@pytest.mark.parametrize("Sq,Sk,D,kw", [(70, 200, 64, {}), (150, 150, 64, {"causal": True}), (200, 200, 32, {"causal": True, "window": 37}),
+                                        (70, 200, 128, {"causal": True}), (1, 700, 64, {}), (40, 1500, 64, {})])
+def test_scores_that_rise_and_fall(dtype, path, Sq, Sk, D, kw):
+    say("path", dtype, path, Sq, Sk, D, kw)
+    rng = np.random.default_rng(3)
+    q, do = values(rng, (2, Sq, 2, D), dtype), values(rng, (2, Sq, 2, D), dtype)
+    k, v = values(rng, (2, Sk, 1, D), dtype), values(rng, (2, Sk, 1, D), dtype)
+    k = k * PATHS[path](Sk)[None, :, None, None]
+    compare(q, bo.to_bf16(k) if dtype == "bf16" else k.astype(np.float32).astype(np.float64), v, do, dtype, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_far_from_zero(dtype, sign, D):
+    """Every score near -1000 or 1000 of one sequence, near 0 of the other."""
+    say("far", dtype, sign, D)
+    rng = np.random.default_rng(4)
+    q, do = values(rng, (2, 90, 2, D), dtype), values(rng, (2, 90, 2, D), dtype)
+    k, v = values(rng, (2, 90, 2, D), dtype), values(rng, (2, 90, 2, D), dtype)
+    q[0, ..., 0], k[0, ..., 0] = 64.0, sign * 16.0 * math.sqrt(D)
+    k = bo.to_bf16(k) if dtype == "bf16" else k.astype(np.float32).astype(np.float64)
+    compare(q, k, v, do, dtype, causal=True)
+
+
+@pytest.mark.parametrize("S,H,Hkv,D,window", [(20, 8, 8, 64, 0), (300, 8, 8, 64, 0), (300, 8, 2, 128, 0), (300, 4, 4, 96, 0),
+                                              (500, 8, 8, 64, 8), (500, 8, 2, 128, 16), (33, 4, 4, 32, 12)])
+def test_precision_of_bf16_gradients(S, H, Hkv, D, window):
+    """Beside the rounding of the result, whose relative error an exact gradient
+    has too, dS (for dv: P) is rounded once, independently and as finely: sqrt(2)
+    times the exact gradient's error.  1.5 leaves the rest a quarter of one such
+    error's square, which the rounding of o in delta exceeds where rows see few
+    keys, if it is not corrected."""
+    say("precision", S, H, Hkv, D, window)
+    rng = np.random.default_rng(5)
+    q, do = values(rng, (2, S, H, D), "bf16"), values(rng, (2, S, H, D), "bf16")
+    k, v = values(rng, (2, S, Hkv, D), "bf16"), values(rng, (2, S, Hkv, D), "bf16")
+    ref = bo.attention(q, k, v, do, dtype="bf16", causal=True, window=window)
+    qd, kd, vd, dod = (dev(x, "bf16") for x in (q, k, v, do))
+    o, lse = pamm.attention(qd, kd, vd, causal=True, window=window)
+    for n, t in zip(("dq", "dk", "dv"), pamm.attention_backward(dod, qd, kd, vd, o, lse, causal=True, window=window)):
+        want = ref[n]
+        off = np.linalg.norm(t.double().cpu().numpy() - want)
+        exact = np.linalg.norm(bo.to_bf16(want) - want)
+        assert off <= 1.5 * exact, f"{n}: {off / exact:.3f} times the exact gradient's rounding"
