@@ -10,7 +10,9 @@ no probabilities; these are that attention and its neighbours.
 
 As in the rest of the package, PyTorch supplies device memory and the stream,
 every step runs in the library's HIP kernels, and there is no CPU fallback.
-All calls are asynchronous on the current stream (or ``stream``).
+All calls are asynchronous on the current stream.  With ``stream`` they run as
+under ``torch.cuda.stream(stream)``: what they allocate belongs to that stream,
+so that no memory of work pending on another is written.
 """
 from __future__ import annotations
 
@@ -104,10 +106,16 @@ def _ws(nbytes, device, workspace, where):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _stream_of(stream, index):
-    """The stream's handle; torch's current one on that GPU by default."""
-    if stream is not None:
-        return stream.cuda_stream
+def _under(stream, where, t, call, *args, **kw):
+    """call(*args) with ``stream``, which is on t's GPU, as the current one."""
+    if t.is_cuda and stream.device != t.device:
+        raise ValueError(f"{where}: stream is on {stream.device}, tensors are on {t.device}")
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
+
+
+def _stream_of(index):
+    """The handle of torch's current stream on that GPU."""
     if _raw_stream is not None:
         return _raw_stream(index)
     return torch.cuda.current_stream(index).cuda_stream
@@ -222,6 +230,9 @@ def attention(q, k, v, *, causal: bool = False, window: int = 0, scale=None, q_l
     Returns (o [B x Sq x H x D], lse [B x H x Sq] fp32); a query that sees no
     key has o = 0 and lse = -inf.  attention_backward takes both."""
     where = "attention"
+    if stream is not None:
+        return _under(stream, where, q, attention, q, k, v, causal=causal, window=window, scale=scale, q_len=q_len,
+                      kv_len=kv_len, o=o, lse=lse, workspace=workspace)
     if q.dim() != 4:
         _heads_tensor(where, "q", q)
     if o is None:
@@ -235,7 +246,7 @@ def attention(q, k, v, *, causal: bool = False, window: int = 0, scale=None, q_l
     _check_workspace(where, workspace)
     lib, index = _lib(), q.get_device()
     ws, nbytes = _ws(lib.pamm_attention_workspace_size(p), q.device, workspace, where)
-    _launch("pamm_attention", index, lib.pamm_attention, p, ws, nbytes, _stream_of(stream, index))
+    _launch("pamm_attention", index, lib.pamm_attention, p, ws, nbytes, _stream_of(index))
     return o, lse
 
 
@@ -250,6 +261,9 @@ def attention_backward(do, q, k, v, o, lse, *, causal: bool = False, window: int
     packed gradient); they are written whole, with zeros past the lengths.
     Bitwise deterministic."""
     where = "attention_backward"
+    if stream is not None:
+        return _under(stream, where, q, attention_backward, do, q, k, v, o, lse, causal=causal, window=window,
+                      scale=scale, q_len=q_len, kv_len=kv_len, dq=dq, dk=dk, dv=dv, workspace=workspace)
     doh = _heads_tensor(where, "do", do)
     if do.shape != q.shape or do.dtype != q.dtype:
         raise ValueError(f"{where}: do must be {q.dtype} of shape {tuple(q.shape)}, got {tuple(do.shape)} {do.dtype}")
@@ -275,7 +289,7 @@ def attention_backward(do, q, k, v, o, lse, *, causal: bool = False, window: int
     lib, index = _lib(), q.get_device()
     ws, nbytes = _ws(lib.pamm_attention_backward_workspace_size(p), q.device, workspace, where)
     _launch("pamm_attention_backward", index, lib.pamm_attention_backward, p, *packed, ws, nbytes,
-            _stream_of(stream, index))
+            _stream_of(index))
     return tuple(outs)
 
 
@@ -313,6 +327,8 @@ def _vector(where, name, t, d, dtype):
 
 
 def _norm_forward(where, x, weight, residual, eps, h, y, q, qscale, want_q, stream):
+    if stream is not None:
+        return _under(stream, where, x, _norm_forward, where, x, weight, residual, eps, h, y, q, qscale, want_q, None)
     if x.dim() != 2:
         raise ValueError(f"{where}: x must be a 2-D tensor with contiguous rows")
     n, d = x.shape
@@ -351,7 +367,7 @@ def _norm_forward(where, x, weight, residual, eps, h, y, q, qscale, want_q, stre
     rstd = torch.empty(n, dtype=torch.float32, device=device)
     index = x.get_device()
     _launch("pamm_add_rms_norm", index, _lib().pamm_add_rms_norm, x.data_ptr(), ldx, rp, ldr, weight.data_ptr(), n, d,
-            dt, eps, hp, ldh, yp, ldy, qp, ldq, sp, rstd.data_ptr(), _stream_of(stream, index))
+            dt, eps, hp, ldh, yp, ldy, qp, ldq, sp, rstd.data_ptr(), _stream_of(index))
     return (q, qscale, h_out, rstd) if want_q else (y, h_out, rstd)
 
 
@@ -381,6 +397,9 @@ def add_rms_norm_backward(dy, h, weight, rstd, *, dh=None, dx=None, dweight=None
     Returns (dx [n x d], the gradient of x and of residual alike,
     dweight [d] fp32).  dx may be dy or dh itself.  Bitwise deterministic."""
     where = "add_rms_norm_backward"
+    if stream is not None:
+        return _under(stream, where, h, add_rms_norm_backward, dy, h, weight, rstd, dh=dh, dx=dx, dweight=dweight,
+                      workspace=workspace)
     if h.dim() != 2:
         raise ValueError(f"{where}: h must be a 2-D tensor with contiguous rows")
     n, d = h.shape
@@ -403,7 +422,7 @@ def add_rms_norm_backward(dy, h, weight, rstd, *, dh=None, dx=None, dweight=None
     ws, nbytes = _ws(lib.pamm_add_rms_norm_backward_workspace_size(n, d, dt), h.device, workspace, where)
     _launch("pamm_add_rms_norm_backward", index, lib.pamm_add_rms_norm_backward, dy.data_ptr(), lddy, h.data_ptr(),
             ldh, weight.data_ptr(), rstd.data_ptr(), dh.data_ptr() if dh is not None else None, lddh, n, d, dt,
-            dx.data_ptr(), lddx, dweight.data_ptr(), ws, nbytes, _stream_of(stream, index))
+            dx.data_ptr(), lddx, dweight.data_ptr(), ws, nbytes, _stream_of(index))
     return dx, dweight
 
 
@@ -449,6 +468,8 @@ def clip_grad_norm(grads, max_norm=None, *, eps: float = 1e-6, out=None, workspa
     first = next((g for g in grads if g is not None), None)
     if first is None:
         raise ValueError(f"{where}: no gradient given")
+    if stream is not None:
+        return _under(stream, where, first, clip_grad_norm, grads, max_norm, eps=eps, out=out, workspace=workspace)
     index, device, codes, flat = first.get_device(), first.device, _CODES, []
     for i, (g, o) in enumerate(zip(grads, outs)):
         if g is None:
@@ -493,7 +514,7 @@ def clip_grad_norm(grads, max_norm=None, *, eps: float = 1e-6, out=None, workspa
     try:
         _launch("pamm_clip_grad_norm", index, lib.pamm_clip_grad_norm, arr, count,
                 math.inf if max_norm is None else float(max_norm), float(eps), norm.data_ptr(), ws, nbytes,
-                _stream_of(stream, index))
+                _stream_of(index))
     except PammError as e:
         if e.status == 10:  # PAMM_ERR_OVERLAP
             raise ValueError(f"{where}: two gradients share memory that is written") from e
