@@ -228,7 +228,8 @@ def attention(q, k, v, *, causal: bool = False, window: int = 0, scale=None, q_l
 
     One query per sequence (or few) splits the keys over the whole device.
     Returns (o [B x Sq x H x D], lse [B x H x Sq] fp32); a query that sees no
-    key has o = 0 and lse = -inf.  attention_backward takes both."""
+    key has o = 0 and lse = -inf.  attention_backward takes both.  o and lse,
+    where given, must not share memory with the inputs."""
     where = "attention"
     if stream is not None:
         return _under(stream, where, q, attention, q, k, v, causal=causal, window=window, scale=scale, q_len=q_len,
@@ -258,7 +259,8 @@ def attention_backward(do, q, k, v, o, lse, *, causal: bool = False, window: int
     The probabilities are recomputed from q, k and lse, so nothing of size
     Sq x Sk exists.  dk and dv are summed over the query heads that share
     them.  dq, dk and dv may be given (strided views, for instance of one
-    packed gradient); they are written whole, with zeros past the lengths.
+    packed gradient); they are written whole, with zeros past the lengths, and
+    must not share memory with each other or the inputs.
     Bitwise deterministic."""
     where = "attention_backward"
     if stream is not None:

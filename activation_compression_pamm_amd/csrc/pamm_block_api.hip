@@ -88,18 +88,23 @@ int attention_check(const pamm_attention_t* a) {
     return PAMM_OK;
 }
 
-pamm::HeadsArg heads_arg(const pamm_heads_t& t, int dtype) {
-    const int64_t e = elem_size(dtype);
-    return {reinterpret_cast<char*>(t.data), t.stride_b * e, t.stride_s * e, t.stride_h * e};
+// Strides in bytes.  That of a dimension with one entry may be anything (it is
+// not checked); kernels form addresses past the last row, which bounds turn
+// into zeros, so rows get a distance of their own length.
+pamm::HeadsArg heads_arg(const pamm_heads_t& t, const pamm_attention_t* a, bool query) {
+    const int64_t e = elem_size(a->dtype), seq = query ? a->seq_q : a->seq_k, heads = query ? a->heads : a->heads_kv;
+    return {reinterpret_cast<char*>(t.data), a->batch > 1 && seq > 0 ? t.stride_b * e : 0,
+            a->batch > 0 && seq > 1 ? t.stride_s * e : a->head_dim * e,
+            a->batch > 0 && seq > 0 && heads > 1 ? t.stride_h * e : 0};
 }
 
 pamm::AttnArgs attention_args(const pamm_attention_t* a) {
     pamm::AttnArgs r;
     memset(&r, 0, sizeof r);
-    r.q = heads_arg(a->q, a->dtype);
-    r.k = heads_arg(a->k, a->dtype);
-    r.v = heads_arg(a->v, a->dtype);
-    r.o = heads_arg(a->o, a->dtype);
+    r.q = heads_arg(a->q, a, true);
+    r.k = heads_arg(a->k, a, false);
+    r.v = heads_arg(a->v, a, false);
+    r.o = heads_arg(a->o, a, true);
     r.lse = a->lse;
     r.q_len = a->q_len;
     r.kv_len = a->kv_len;
@@ -161,7 +166,7 @@ bool rows_ok(int64_t n, int64_t ld, int64_t d) { return ld >= d && ld <= kMaxSpa
 // Sizes of the norm calls; their leading dimensions are checked with each matrix.
 int norm_sizes(int64_t n, int64_t d, int dtype) {
     if (!dtype_ok(dtype)) return PAMM_ERR_DTYPE;
-    if (n < 0 || n > kMaxSize || d < 1 || (d + per16(dtype) - 1) / per16(dtype) > pamm::kMaxNormVectors)
+    if (n < 0 || n > kMaxSize || d < 1 || d > pamm::kMaxNormVectors * per16(dtype))
         return PAMM_ERR_SHAPE;
     return PAMM_OK;
 }
@@ -216,10 +221,10 @@ int pamm_attention_backward(const pamm_attention_t* a, const pamm_heads_t* dout,
     if (int e = ws_check(ws, ws_bytes, need)) return e;
     if (a->batch == 0) return PAMM_OK;
     pamm::AttnArgs r = attention_args(a);
-    r.dout = heads_arg(*dout, a->dtype);
-    r.dq = heads_arg(*dq, a->dtype);
-    r.dk = heads_arg(*dk, a->dtype);
-    r.dv = heads_arg(*dv, a->dtype);
+    r.dout = heads_arg(*dout, a, true);
+    r.dq = heads_arg(*dq, a, true);
+    r.dk = heads_arg(*dk, a, false);
+    r.dv = heads_arg(*dv, a, false);
     const BackwardLayout L = backward_layout(a);
     char* at = reinterpret_cast<char*>(ws);
     r.delta = reinterpret_cast<float*>(at);
@@ -258,10 +263,10 @@ int pamm_add_rms_norm(const void* x, int64_t ldx, const void* r, int64_t ldr, co
     a.qscale = qscale;
     a.rstd = rstd;
     a.ldx = ldx * es;
-    a.ldr = ldr * es;
-    a.ldh = ldh * es;
-    a.ldy = ldy * es;
-    a.ldq = ldq;
+    a.ldr = r ? ldr * es : 0;  // without its matrix a leading dimension is not checked
+    a.ldh = r ? ldh * es : 0;
+    a.ldy = y ? ldy * es : 0;
+    a.ldq = q ? ldq : 0;
     a.n = n;
     a.d = (int)d;
     a.eps = eps;
@@ -296,10 +301,12 @@ int pamm_add_rms_norm_backward(const void* dy, int64_t lddy, const void* h, int6
     a.dx = reinterpret_cast<char*>(dx);
     a.dw = dw;
     a.part = reinterpret_cast<float*>(ws);
-    a.lddy = lddy * es;
-    a.ldh = ldh * es;
-    a.lddh = lddh * es;
-    a.lddx = lddx * es;
+    if (n > 0) {  // not checked otherwise, nor used
+        a.lddy = lddy * es;
+        a.ldh = ldh * es;
+        a.lddh = dh ? lddh * es : 0;
+        a.lddx = lddx * es;
+    }
     a.n = n;
     a.d = (int)d;
     a.num_cus = num_cus();

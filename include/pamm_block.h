@@ -82,7 +82,9 @@ size_t pamm_attention_workspace_size(const pamm_attention_t *a_host);
  * A query that sees no key (and every i >= q_len[b]) gets o = 0 and
  * lse = -infinity; so does one whose every score is -infinity.  bf16: products
  * of bf16 values summed in fp32, probabilities rounded to bf16 for the
- * product with V, o rounded once.  fp32: fp32 throughout.
+ * product with V, o rounded once.  fp32: fp32 throughout.  o and lse must not
+ * overlap each other or any input; the stride of a dimension with one entry is
+ * not looked at.
  *
  * Errors: PAMM_ERR_NULL, _DTYPE, _SHAPE (sizes < 0, heads not a multiple of
  * heads_kv, head_dim out of range, a stride that is negative or spans 2^40

@@ -78,3 +78,23 @@ def test_precision_of_bf16_gradients(S, H, Hkv, D, window):
         off = np.linalg.norm(t.double().cpu().numpy() - want)
         exact = np.linalg.norm(bo.to_bf16(want) - want)
         assert off <= 1.5 * exact, f"{n}: {off / exact:.3f} times the exact gradient's rounding"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Sq", [1, 40])
+@pytest.mark.parametrize("stride", [0, 64, 1 << 35])
+def test_stride_of_a_single_key(dtype, Sq, stride):
+    """A sequence of one key has no distance to the next: no tile's further rows
+    are that key again, whose infinity would meet their probability 0."""
+    say("single key", dtype, Sq, stride)
+    rng = np.random.default_rng(6)
+    q = dev(values(rng, (1, Sq, 2, 64), dtype), dtype)
+    flat = dev(values(rng, (2, 128), dtype), dtype)
+    flat[1, 5] = math.inf
+    k, v = (torch.as_strided(t, (1, 1, 2, 64), (stride, stride, 64, 1)) for t in flat)
+    o, lse = pamm.attention(q, k, v)
+    same, fin = v.expand(1, Sq, 2, 64).double(), torch.isfinite(v).expand(1, Sq, 2, 64)
+    assert torch.equal(torch.isfinite(o), fin) and torch.equal(o.double()[~fin], same[~fin])
+    assert ((o.double() - same)[fin].abs() <= same[fin].abs() * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -21)).all()
+    want = (q.double() * k.double()).sum(-1).transpose(1, 2) / 8.0
+    assert (lse.double() - want).abs().max() < 1e-4
