@@ -3,11 +3,21 @@ operators' C ABI, on the CPU: sizes and strides at their extremes, every kind
 of refusal, the workspace layouts and the clipping call's lists, with launchers
 that check their arguments in place of the kernels' (no GPU, no device code)."""
 import os
+import subprocess
 
 import pytest
 
 from conftest import ROOT
-from test_sanitizers_cpu import HIPCC, SAN_ENV, run
+
+HIPCC = "/opt/rocm/bin/hipcc"
+SAN_ENV = dict(os.environ, ASAN_OPTIONS="detect_leaks=0:abort_on_error=0",
+               UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1", HIP_VISIBLE_DEVICES="-1")
+
+
+def run(cmd, **kw):
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=600, **kw)
+    assert r.returncode == 0, f"{' '.join(cmd)}\n{r.stdout[-3000:]}\n{r.stderr[-3000:]}"
+    return r
 
 
 @pytest.mark.skipif(not os.path.exists(HIPCC), reason="needs the ROCm toolchain")
