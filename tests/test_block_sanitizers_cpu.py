@@ -20,7 +20,11 @@ def run(cmd, **kw):
     return r
 
 
-@pytest.mark.skipif(not os.path.exists(HIPCC), reason="needs the ROCm toolchain")
+DRIVER = os.path.join(ROOT, "tests", "sanitize", "block_driver.cpp")
+
+
+@pytest.mark.skipif(not (os.path.exists(HIPCC) and os.path.exists(DRIVER)),
+                    reason="needs the ROCm toolchain and the driver's source")
 def test_block_abi_host_side_under_asan_ubsan(tmp_path):
     csrc = os.path.join(ROOT, "activation_compression_pamm_amd", "csrc")
     san = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined", "-Xarch_host",
@@ -28,6 +32,6 @@ def test_block_abi_host_side_under_asan_ubsan(tmp_path):
     exe = str(tmp_path / "block_san")
     run([HIPCC, "--offload-arch=gfx950", "-O1", "-g", "-std=c++17", "-Xclang", "-target-feature", "-Xclang",
          "-packed-fp32-ops", *san, "-I", os.path.join(ROOT, "include"), "-I", csrc, "-x", "hip",
-         os.path.join(ROOT, "tests", "sanitize", "block_driver.cpp"), os.path.join(csrc, "pamm_block_api.hip"),
+         DRIVER, os.path.join(csrc, "pamm_block_api.hip"),
          "-o", exe])
     assert "block ABI sanitizer driver ok" in run([exe], env=SAN_ENV).stdout
