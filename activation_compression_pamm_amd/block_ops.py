@@ -56,7 +56,7 @@ class _Grad(ctypes.Structure):
 _HEADS = "Pqqq"
 _pack_attention = struct.Struct("@ii7qf4xPP" + 4 * _HEADS + "P").pack
 _pack_heads = struct.Struct("@" + _HEADS).pack
-_GRAD = "PP4qii"
+_pack_grad = struct.Struct("@PP4qii").pack
 
 _BLOCK_EXPORTS = {
     "pamm_attention_workspace_size": (_sz, [_vp]),
@@ -472,7 +472,7 @@ def clip_grad_norm(grads, max_norm=None, *, eps: float = 1e-6, out=None, workspa
         raise ValueError(f"{where}: no gradient given")
     if stream is not None:
         return _under(stream, where, first, clip_grad_norm, grads, max_norm, eps=eps, out=out, workspace=workspace)
-    index, device, codes, flat = first.get_device(), first.device, _CODES, []
+    index, device, codes, packed = first.get_device(), first.device, _CODES, []
     for i, (g, o) in enumerate(zip(grads, outs)):
         if g is None:
             continue
@@ -484,10 +484,10 @@ def clip_grad_norm(grads, max_norm=None, *, eps: float = 1e-6, out=None, workspa
         if o is g:
             if g.is_contiguous():
                 n, p = g.numel(), g.data_ptr()
-                flat += (p, p, 1, n, n, n, code, code)
+                packed.append(_pack_grad(p, p, 1, n, n, n, code, code))
             else:
                 rows, cols, ld = _grad_layout(where, f"gradient {i}", g)
-                flat += (g.data_ptr(), g.data_ptr(), rows, cols, ld, ld, code, code)
+                packed.append(_pack_grad(g.data_ptr(), g.data_ptr(), rows, cols, ld, ld, code, code))
             continue
         if o is None or o.shape != g.shape or o.get_device() != index:
             raise ValueError(f"{where}: output {i} must have shape {tuple(g.shape)} on {device}")
@@ -496,7 +496,7 @@ def clip_grad_norm(grads, max_norm=None, *, eps: float = 1e-6, out=None, workspa
             _code(where, o)
         if g.is_contiguous() and o.is_contiguous():
             n = g.numel()
-            flat += (g.data_ptr(), o.data_ptr(), 1, n, n, n, code, code_o)
+            packed.append(_pack_grad(g.data_ptr(), o.data_ptr(), 1, n, n, n, code, code_o))
             continue
         lay, lay_o = _grad_layout(where, f"gradient {i}", g), _grad_layout(where, f"output {i}", o)
         if (lay[0] == 1) != (lay_o[0] == 1) and g.dim() == 2 and (g.is_contiguous() or o.is_contiguous()):
@@ -504,9 +504,8 @@ def clip_grad_norm(grads, max_norm=None, *, eps: float = 1e-6, out=None, workspa
             lay, lay_o = ((t.shape[0], t.shape[1], t.stride(0)) for t in (g, o))
         elif lay[:2] != lay_o[:2] or (lay[0] == 1 and g.stride() != o.stride()):
             raise ValueError(f"{where}: output {i} must be laid out as its gradient")
-        flat += (g.data_ptr(), o.data_ptr(), lay[0], lay[1], lay[2], lay_o[2], code, code_o)
-    count = len(flat) // 8
-    arr = struct.pack("@" + _GRAD * count, *flat)
+        packed.append(_pack_grad(g.data_ptr(), o.data_ptr(), lay[0], lay[1], lay[2], lay_o[2], code, code_o))
+    count, arr = len(packed), b"".join(packed)
     if workspace is not None:
         _check_workspace(where, workspace)
         _on_gpu(where, gradients=first, workspace=workspace)
