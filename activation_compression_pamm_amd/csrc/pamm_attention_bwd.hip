@@ -292,13 +292,30 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
 
     using Copy = TileCopy<DT, ND, BQ, 256>;
     Copy qc, oc, rc;  // q, do and, for delta, o
+    // Where a row's vectors are no power of two, its sum's come again, LPR threads a row.
+    constexpr bool NEIGHBOURS = (T::CPR & (T::CPR - 1)) == 0;
+    constexpr int LPR = T::CPR <= 16 ? 16 : 32, RPP = 256 / LPR, PASSES = BQ / RPP;
+    uint4 xo[PASSES], xr[PASSES];
     float stat = 0.0f;
     auto fetch = [&](int g, int t) {
         const int head = hk * a.G + g, q0 = t * BQ;
         qc.fetch(a.q.p + b * a.q.sb + head * a.q.sh + q0 * a.q.ss, (int)a.q.ss, Lq - q0, a.D, tid);
         oc.fetch(a.dout.p + b * a.dout.sb + head * a.dout.sh + q0 * a.dout.ss, (int)a.dout.ss, Lq - q0, a.D, tid);
-        if constexpr (ONE)
+        if constexpr (ONE && NEIGHBOURS) {
             rc.fetch(a.o.p + b * a.o.sb + head * a.o.sh + q0 * a.o.ss, (int)a.o.ss, Lq - q0, a.D, tid);
+        } else if constexpr (ONE) {
+            const RowView o(a.o.p + b * a.o.sb + head * a.o.sh + q0 * a.o.ss, (int)a.o.ss, Lq - q0, BQ, a.D * T::ES);
+            const RowView d(a.dout.p + b * a.dout.sb + head * a.dout.sh + q0 * a.dout.ss, (int)a.dout.ss, Lq - q0, BQ,
+                            a.D * T::ES);
+            const int row = tid / LPR, x = tid % LPR;
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const int at = row + i * RPP;
+                const bool in = x * T::PE < a.D && q0 + at < Lq;
+                xr[i] = o.load(in ? at * (int)a.o.ss + x * 16 : kOutside);
+                xo[i] = d.load(in ? at * (int)a.dout.ss + x * 16 : kOutside);
+            }
+        }
         const int r = tid % BQ;
         const int64_t at = ((int64_t)b * a.H + head) * a.Sq + q0 + r;
         stat = 0.0f;
@@ -307,9 +324,17 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
     auto put = [&](int buf) {
         qc.put(lds[buf][0], tid);
         oc.put(lds[buf][1], tid);
-        if constexpr (ONE) {
+        if constexpr (ONE && !NEIGHBOURS) {
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                float d = dot16<DT>(xo[i], xr[i]);
+#pragma unroll
+                for (int m = 1; m < LPR; m <<= 1) d += shfl_xor(d, m);
+                if (tid % LPR == 0) rowstat[buf][1][tid / LPR + i * RPP] = -d;
+            }
+            if (tid < BQ) rowstat[buf][0][tid] = start_of(stat, c);
+        } else if constexpr (ONE) {
             // the threads that copy a row are neighbours
-            static_assert((T::CPR & (T::CPR - 1)) == 0);
 #pragma unroll
             for (int i = 0; i < Copy::PER; ++i) {
                 float d = dot16<DT>(oc.r[i], rc.r[i]);
@@ -474,11 +499,7 @@ struct BackwardShared {
 };
 
 // Both in one launch, the dk/dv items, which take longer, first.  They form delta
-// themselves (reading o too) instead of waiting for the dq items': the sums of
-// a row's products go over the neighbouring threads that copy it, for which
-// their number must be a power of two.
-template <int ND> constexpr bool kOneKernel = ND != 3;
-
+// themselves (reading o too) instead of waiting for the dq items'.
 template <int DT, int ND>
 __global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void attention_backward_kernel(
     AttnArgs a, int row_tiles, int key_tiles, int dkv_items) {
@@ -504,9 +525,9 @@ __global__ __launch_bounds__(256, 1) void attention_backward_again_kernel(AttnAr
         [&](int i) {
             i = __builtin_amdgcn_readfirstlane(i);
             if (i < a.dq_items)
-                attention_dq<DT, ND, kOneKernel<ND>, true>(a, i, row_tiles, shared.dq());
+                attention_dq<DT, ND, true, true>(a, i, row_tiles, shared.dq());
             else
-                attention_dkv<DT, ND, kOneKernel<ND>, true>(a, i - a.dq_items, key_tiles, shared.dkv());
+                attention_dkv<DT, ND, true, true>(a, i - a.dq_items, key_tiles, shared.dkv());
         });
 }
 
@@ -559,7 +580,7 @@ int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t
 // of the first with the second; two form delta once only.  With all items on
 // the device in two rounds of resident workgroups one launch is the faster
 // (bf16, causal: 1 x 512 tokens, 16 heads of 128, 43 us against 62; 4 x 1024, 16
-// of 128, 111 / 120; 8 x 1024, 12 of 64, 73 / 86; fp32: 4 x 128, 16 of 128, 51 / 82),
+// of 128, 111 / 120; 8 x 1024, 12 of 64, 73 / 86; 4 x 512, 8 of 80, 42 / 54; fp32: 4 x 128, 16 of 128, 51 / 82),
 // with more it loses (4 x 2048, 16 of 128: 340 / 295; 8 x 4096, 12 of 64: 843 / 777).
 // Without a causal mask workgroups end together, and rows above 64 gain in one
 // round only (4 x 1024, 16 of 128: 156 / 144; 4 x 512: 56 / 63).
@@ -568,7 +589,7 @@ static bool one_backward_kernel(const AttnArgs& a, int64_t items) {
     const int resident = DT != DT_BF16 ? 1 : ND <= 2 ? 3 : 2, rounds = ND <= 2 || a.causal ? 2 : 1;
     // delta of a short window comes from the dq side
     if (DT == DT_BF16 && a.causal && short_window(a)) return false;
-    return kOneKernel<ND> && items <= (int64_t)a.num_cus * resident * rounds;
+    return items <= (int64_t)a.num_cus * resident * rounds;
 }
 
 
@@ -577,13 +598,10 @@ static void launch_backward(const AttnArgs& a, hipStream_t st) {
     const int64_t tiles = ((int64_t)a.Sq * a.G + 127) / 128, key_tiles = ((int64_t)a.Sk + 127) / 128;
     const int64_t heads = (int64_t)a.B * a.Hkv;
     const int dq_items = (int)(heads * tiles), items = dq_items + (int)(heads * key_tiles * a.nsplit_kv);
-    bool one = false;
-    if constexpr (kOneKernel<ND>) {
-        one = one_backward_kernel<DT, ND>(a, items);
-        if (one && items > 0)
-            hipLaunchKernelGGL((attention_backward_kernel<DT, ND>), dim3((unsigned)items), dim3(256), 0, st, a,
-                               (int)tiles, (int)key_tiles, items - dq_items);
-    }
+    const bool one = one_backward_kernel<DT, ND>(a, items);
+    if (one && items > 0)
+        hipLaunchKernelGGL((attention_backward_kernel<DT, ND>), dim3((unsigned)items), dim3(256), 0, st, a, (int)tiles,
+                           (int)key_tiles, items - dq_items);
     if (!one) {
         if (tiles > 0)
             hipLaunchKernelGGL((attention_dq_kernel<DT, ND>), dim3((unsigned)dq_items), dim3(256), 0, st, a, (int)tiles);
