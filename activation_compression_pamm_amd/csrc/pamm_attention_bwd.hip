@@ -579,9 +579,10 @@ int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t
 // One launch or two?  One saves the wait between two kernels and fills the end
 // of the first with the second; two form delta once only.  With all items on
 // the device in two rounds of resident workgroups one launch is the faster
-// (bf16, causal: 1 x 512 tokens, 16 heads of 128, 43 us against 62; 4 x 1024, 16
-// of 128, 111 / 120; 8 x 1024, 12 of 64, 73 / 86; 4 x 512, 8 of 80, 42 / 54; fp32: 4 x 128, 16 of 128, 51 / 82),
-// with more it loses (4 x 2048, 16 of 128: 340 / 295; 8 x 4096, 12 of 64: 843 / 777).
+// (bf16, causal: 1 x 512 tokens, 16 heads of 128, 43 us against 62; 4 x 1024, 16 of
+// 128, 111 / 120; 8 x 1024, 12 of 64, 73 / 86; 4 x 512, 8 of 80, 42 / 54; fp32: 4 x
+// 128, 16 of 128, 51 / 82), with more it loses (4 x 2048, 16 of 128: 340 / 295; 8 x
+// 4096, 12 of 64: 843 / 777).
 // Without a causal mask workgroups end together, and rows above 64 gain in one
 // round only (4 x 1024, 16 of 128: 156 / 144; 4 x 512: 56 / 63).
 template <int DT, int ND>
@@ -591,7 +592,6 @@ static bool one_backward_kernel(const AttnArgs& a, int64_t items) {
     if (DT == DT_BF16 && a.causal && short_window(a)) return false;
     return items <= (int64_t)a.num_cus * resident * rounds;
 }
-
 
 template <int DT, int ND>
 static void launch_backward(const AttnArgs& a, hipStream_t st) {
