@@ -414,6 +414,9 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
                 const float off = p[0] + shfl_xor(p[0], 16);
                 const int row = (l & 1) * 16 + (l & 2) * 4 + (l >> 2 & 1) * 2 + (l >> 3 & 1) + quad;
                 if (!(l & 16)) rowstat[cur][1][row] -= off;
+                // half of the lanes write what all of the wave read next
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
             }
             f32x16 s = starts(0), dp = starts(1);
 #pragma unroll
@@ -427,7 +430,6 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(s[e] * c);
-            
             settle<DT>(dp);
             // some pair of this block is masked?
             bool part = w0 + 32 > Lk || q0 + BQ > Lq;

@@ -98,3 +98,27 @@ def test_stride_of_a_single_key(dtype, Sq, stride):
     assert ((o.double() - same)[fin].abs() <= same[fin].abs() * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -21)).all()
     want = (q.double() * k.double()).sum(-1).transpose(1, 2) / 8.0
     assert (lse.double() - want).abs().max() < 1e-4
+
+
+@pytest.mark.parametrize("H,Hkv,D", [(8, 8, 64), (16, 8, 128), (8, 8, 96), (16, 16, 32)])
+def test_every_lane_has_the_corrected_delta(H, Hkv, D):
+    """In one launch, delta's correction is formed by the lanes of the first 16
+    keys of a block and used by all.  Here the two keys behind those have all of
+    the weight, so that the rounding of o in delta shows: uncorrected it adds half
+    of an exact gradient's squared error or more to its own and that of dS (1.58
+    times its error), corrected the bound of test_precision_of_bf16_gradients holds."""
+    say("corrected delta", H, Hkv, D)
+    rng = np.random.default_rng(11)
+    B, Sq, Sk = 16, 40, 18
+    q, do = values(rng, (B, Sq, H, D), "bf16"), values(rng, (B, Sq, H, D), "bf16")
+    k, v = values(rng, (B, Sk, Hkv, D), "bf16"), values(rng, (B, Sk, Hkv, D), "bf16")
+    q[..., 0], k[:, :, :, 0] = 2.0, 0.0
+    k[:, :16, :, 0] = -32.0 * math.sqrt(D) // 1  # scores near -64
+    k = bo.to_bf16(k)
+    ref = bo.attention(q, k, v, do, dtype="bf16")
+    qd, kd, vd, dod = (dev(x, "bf16") for x in (q, k, v, do))
+    o, lse = pamm.attention(qd, kd, vd)
+    got = pamm.attention_backward(dod, qd, kd, vd, o, lse)[1].double().cpu().numpy()[:, 16:]
+    want = ref["dk"][:, 16:]
+    off, exact = np.linalg.norm(got - want), np.linalg.norm(bo.to_bf16(want) - want)
+    assert off <= 1.5 * exact, f"{off / exact:.3f} times the exact gradient's rounding"
