@@ -221,7 +221,7 @@ __device__ __forceinline__ void attention_rows(const AttnArgs& a, int id, int ro
 
 #pragma unroll
     for (int db = 0; db < ND; ++db) settle<DT>(acc[db]);
-    const bool marked = !SAFE && a.causal && !sums_finite<ND>(acc);
+    const bool marked = !SAFE && a.hides && !sums_finite<ND>(acc);
     if (!live) return;
     const float sum = half_sum(st.l);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -362,8 +362,7 @@ __device__ __forceinline__ void attention_few(const AttnArgs& a, int id, FewShar
 
 #pragma unroll
     for (int db = 0; db < ND; ++db) settle<DT>(acc[db]);
-    // one query has no key hidden between others
-    const bool marked = !SAFE && a.causal && a.Sq > 1 && !sums_finite<ND>(acc);
+    const bool marked = !SAFE && a.hides && !sums_finite<ND>(acc);
 
     // join the four waves: the common reference first, then the sums in order
     const float sum = marked ? NAN : half_sum(st.l);  // makes the joined lse NaN
@@ -514,14 +513,12 @@ static void launch_attention(const AttnArgs& a, hipStream_t st) {
     const int64_t rows = (int64_t)a.Sq * a.G, tiles = rows <= kFewRows ? 1 : (rows + 127) / 128;
     const int items = (int)((int64_t)a.B * a.Hkv * tiles * a.nsplit);
     const dim3 grid((unsigned)items), again((unsigned)std::min(items, a.num_cus));
-    // only a causal mask hides keys of one query between those of others
-    const bool hides = a.causal && a.Sq > 1;
     if (rows <= kFewRows) {
         hipLaunchKernelGGL((attention_few_kernel<DT, ND>), grid, dim3(256), 0, st, a);
-        if (hides) hipLaunchKernelGGL((attention_few_again_kernel<DT, ND>), again, dim3(256), 0, st, a, items);
+        if (a.hides) hipLaunchKernelGGL((attention_few_again_kernel<DT, ND>), again, dim3(256), 0, st, a, items);
     } else {
         hipLaunchKernelGGL((attention_kernel<DT, ND>), grid, dim3(256), 0, st, a, (int)tiles);
-        if (hides) hipLaunchKernelGGL((attention_again_kernel<DT, ND>), again, dim3(256), 0, st, a, (int)tiles, items);
+        if (a.hides) hipLaunchKernelGGL((attention_again_kernel<DT, ND>), again, dim3(256), 0, st, a, (int)tiles, items);
     }
     if (a.nsplit > 1) {
         const dim3 grid((unsigned)(((int64_t)a.B * a.H * a.Sq + 7) / 8));

@@ -187,7 +187,7 @@ __device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_
     }
 #pragma unroll
     for (int db = 0; db < ND; ++db) settle<DT>(acc[db]);
-    if (!SAFE && a.causal) {
+    if (!SAFE && a.hides) {
         const bool ok = sums_finite<ND>(acc);
         if (l == 0) a.marks[id * 4 + wave] = !ok;
     }
@@ -467,7 +467,7 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
         settle<DT>(dk[db]);
         settle<DT>(dv[db]);
     }
-    if (!SAFE && a.causal) {
+    if (!SAFE && a.hides) {
         const bool ok = sums_finite<ND>(dk) && sums_finite<ND>(dv);
         if (l == 0) a.marks[(a.dq_items + id) * 4 + wave] = !ok;
     }
@@ -611,7 +611,7 @@ static void launch_backward(const AttnArgs& a, hipStream_t st) {
             hipLaunchKernelGGL((attention_dkv_kernel<DT, ND>), dim3((unsigned)(items - dq_items)), dim3(256), 0, st, a,
                                (int)key_tiles);
     }
-    if (a.causal && items > 0)
+    if (a.hides && items > 0)
         hipLaunchKernelGGL((attention_backward_again_kernel<DT, ND>), dim3((unsigned)std::min(items, a.num_cus)),
                            dim3(256), 0, st, a, (int)tiles, (int)key_tiles, items);
     if (a.nsplit_kv > 1) {

@@ -117,6 +117,8 @@ pamm::AttnArgs attention_args(const pamm_attention_t* a) {
     r.D = (int)a->head_dim;
     r.causal = a->causal;
     r.window = a->window >= a->seq_k ? 0 : (int)a->window;  // a window as long as the keys hides none
+    // without a causal mask all queries see the same keys, and so does one query alone
+    r.hides = r.causal && r.Sq > 1;
     r.scale = a->scale;
     r.num_cus = num_cus();
     r.nsplit = r.nsplit_kv = 1;

@@ -24,6 +24,8 @@ struct AttnArgs {
     int B, Sq, Sk, H, Hkv, G, D;  // G = H / Hkv
     int causal;
     int window;             // 0: none
+    bool hides;             // the mask may hide a key between those of a block that are seen: waves mark
+                            // what they have to leave to the second kernel, and it is launched
     float scale;
     int nsplit;             // parts of the key axis (forward)
     float* part_o;          // [B x H x Sq x nsplit x D] when nsplit > 1

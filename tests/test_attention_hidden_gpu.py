@@ -1,0 +1,77 @@
+"""GPU: what a mask hides does not come through, and what it shows touches
+nothing else, for single queries (shared heads, split keys, windows) and in the
+second pass over marked work, against tests/block_oracle.py."""
+import numpy as np
+import pytest
+import torch
+
+import activation_compression_pamm_amd as pamm
+import block_oracle as bo
+from test_attention_gpu import close, dev, host, lens, say, values
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+
+def single(dtype, H, Hkv, Sk, D=64, B=2, **kw):
+    """One query a sequence: the inputs and the exact results of finite data."""
+    rng = np.random.default_rng(12)
+    x = {n: values(rng, s, dtype) for n, s in (("q", (B, 1, H, D)), ("k", (B, Sk, Hkv, D)), ("v", (B, Sk, Hkv, D)))}
+    return x, bo.attention(x["q"], x["k"], x["v"], dtype=dtype, **kw)
+
+
+def call(d, **kw):
+    return pamm.attention(d["q"], d["k"], d["v"], **dict(kw, kv_len=lens(kw.get("kv_len"))))
+
+
+def same(got, ref, pick=slice(None), columns=slice(None)):
+    """o of the heads `pick` in `columns` and lse of those heads."""
+    o, lse = got
+    close("o", host(o)[:, :, pick][..., columns], ref["o"][:, :, pick][..., columns],
+          ref["o_tol"][:, :, pick][..., columns])
+    close("lse", host(lse)[:, pick], ref["lse"][:, pick], ref["lse_tol"][:, pick])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,Hkv", [(4, 2), (32, 1), (40, 1), (80, 2)])
+@pytest.mark.parametrize("Sk", [300, 2000])
+def test_one_query_of_many_heads(dtype, H, Hkv, Sk):
+    """What is not finite in a head's query or in one column of V stays there."""
+    say("one query", dtype, H, Hkv, Sk)
+    kw = {"causal": True}
+    x, ref = single(dtype, H, Hkv, Sk, **kw)
+    d = {n: dev(t, dtype) for n, t in x.items()}
+    d["q"][:, 0, 3, 5] = float("nan")
+    got = call(d, **kw)
+    same(got, ref, np.arange(H) != 3)
+    assert torch.isnan(got[0][:, 0, 3]).all() and torch.isnan(got[1][:, 3]).all()
+    for value in (float("inf"), float("nan")):
+        d = {n: dev(t, dtype) for n, t in x.items()}
+        d["v"][:, Sk - 9, 0, 7] = value
+        got = call(d, **kw)
+        G = H // Hkv
+        same(got, ref, slice(None), np.arange(64) != 7)
+        same(got, ref, slice(G, None))
+        seen = host(got[0])[:, 0, :G, 7]
+        assert np.array_equal(seen, np.full(seen.shape, value), equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,Hkv", [(4, 2), (40, 1)])
+def test_gradients_of_one_query(dtype, H, Hkv):
+    """A NaN in one head's dout and an infinity in a key that the query sees."""
+    say("gradients of one query", dtype, H, Hkv)
+    B, Sk, D, G = 2, 150, 64, H // Hkv
+    x, _ = single(dtype, H, Hkv, Sk)
+    x["do"] = values(np.random.default_rng(13), (B, 1, H, D), dtype)
+    ref = bo.attention(x["q"], x["k"], x["v"], x["do"], causal=True, dtype=dtype)
+    d = {n: dev(t, dtype) for n, t in x.items()}
+    o, lse = call(d, causal=True)
+    d["do"][:, 0, 3, 5] = float("nan")
+    dq, dk, dv = pamm.attention_backward(d["do"], d["q"], d["k"], d["v"], o, lse, causal=True)
+    other = np.arange(H) != 3
+    close("dq", host(dq)[:, :, other], ref["dq"][:, :, other], ref["dq_tol"][:, :, other])
+    hit = 3 // G
+    for n, t in (("dk", dk), ("dv", dv)):
+        rest = np.arange(Hkv) != hit
+        close(n, host(t)[:, :, rest], ref[n][:, :, rest], ref[n + "_tol"][:, :, rest])
+    assert torch.isnan(dv[:, :, hit, 5]).all() and torch.isnan(dq[:, 0, 3]).all()
