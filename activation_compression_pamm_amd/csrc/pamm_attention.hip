@@ -276,7 +276,8 @@ __global__ __launch_bounds__(256, 1) void attention_again_kernel(AttnArgs a, int
 // waits for another wave until the end.  A lane reads its K operand straight
 // from memory (16 bytes of one key a step, the wave 32 keys), V goes through
 // the wave's own LDS tile; the next block's loads are issued as soon as the
-// registers of the current one are used.
+// registers of the current one are used.  Blocks are counted from the first key
+// that a row sees, so a query alone never meets a key outside its window.
 //
 // Bound by reading K and V: 64 sequences of 64 to 8192 keys, 8 heads of 128, 1.11
 // GB: 224 us with the join, 4.9 TB/s, where a large copy reaches 4.75.  130 keys
@@ -307,11 +308,8 @@ __device__ __forceinline__ void attention_few(const AttnArgs& a, int id, FewShar
     KeyRange mine = key_range(a, live ? pos : Lq, Lq, Lk);
     if (mine.hi < mine.lo) mine.hi = mine.lo;
     const RowsRange br = rows_range(a, 0, rows, rows, Lq, Lk);
-    const int n0 = br.begin / 32;
-    int n1 = (br.end + 31) / 32;
-    if (n1 < n0) n1 = n0;
-    const int per = (n1 - n0 + a.nsplit - 1) / a.nsplit;
-    const int p0 = n0 + split * per, p1 = p0 + per < n1 ? p0 + per : n1;
+    const int first = br.begin, n = br.end > first ? (br.end - first + 31) / 32 : 0;
+    const int per = (n + a.nsplit - 1) / a.nsplit, p0 = split * per, p1 = p0 + per < n ? p0 + per : n;
 
     const char* kbase = a.k.p + b * a.k.sb + hk * a.k.sh;
     const char* vbase = a.v.p + b * a.v.sb + hk * a.v.sh;
@@ -339,9 +337,9 @@ __device__ __forceinline__ void attention_few(const AttnArgs& a, int id, FewShar
         vc.fetch(vbase + key0 * a.v.ss, (int)a.v.ss, Lk - key0, a.D, l);
     };
     int t = p0 + wave;
-    if (t < p1) fetch(t * 32);
+    if (t < p1) fetch(first + t * 32);
     for (; t < p1; t += 4) {
-        const int key0 = t * 32;
+        const int key0 = first + t * 32;
         f32x16 s{};
 #pragma unroll
         for (int i = 0; i < T::NS; ++i) s = mma_step<DT>(kf[i], qf[i], s);

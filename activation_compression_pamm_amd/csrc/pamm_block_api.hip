@@ -117,8 +117,9 @@ pamm::AttnArgs attention_args(const pamm_attention_t* a) {
     r.D = (int)a->head_dim;
     r.causal = a->causal;
     r.window = a->window >= a->seq_k ? 0 : (int)a->window;  // a window as long as the keys hides none
-    // without a causal mask all queries see the same keys, and so does one query alone
-    r.hides = r.causal && r.Sq > 1;
+    // without a causal mask all queries see the same keys; one query alone sees the last ones, from
+    // somewhere inside a block if there is a window
+    r.hides = r.causal && (r.Sq > 1 || r.window > 0);
     r.scale = a->scale;
     r.num_cus = num_cus();
     r.nsplit = r.nsplit_kv = 1;
@@ -198,6 +199,8 @@ int pamm_attention(const pamm_attention_t* a, void* ws, size_t ws_bytes, void* s
     if (int e = ws_check(ws, ws_bytes, need)) return e;
     if (a->batch == 0 || a->seq_q == 0) return PAMM_OK;
     pamm::AttnArgs r = attention_args(a);
+    // the few-rows kernel's blocks start at the first key that its rows see
+    if (r.Sq == 1 && r.G <= pamm::kFewRows) r.hides = false;
     r.nsplit = splits_of(a);
     if (r.nsplit > 1) {
         const size_t rows = (size_t)(a->batch * a->heads * a->seq_q) * (size_t)r.nsplit;

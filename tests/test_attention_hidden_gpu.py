@@ -75,3 +75,44 @@ def test_gradients_of_one_query(dtype, H, Hkv):
         rest = np.arange(Hkv) != hit
         close(n, host(t)[:, :, rest], ref[n][:, :, rest], ref[n + "_tol"][:, :, rest])
     assert torch.isnan(dv[:, :, hit, 5]).all() and torch.isnan(dq[:, 0, 3]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (8, 2), (40, 1)])
+@pytest.mark.parametrize("Sk,window", [(200, 5), (300, 33), (300, 64), (2000, 37), (3000, 1500)])
+def test_one_query_with_a_window(dtype, H, Hkv, Sk, window):
+    """Expired keys, in the window's first block and before it, hold anything."""
+    say("window", dtype, H, Hkv, Sk, window)
+    n = [Sk, Sk - 50]
+    kw = {"causal": True, "window": window, "kv_len": n}
+    x, ref = single(dtype, H, Hkv, Sk, **kw)
+    for value in (float("nan"), float("inf"), float("-inf")):
+        for back in (1, 2, 40):  # so many keys before the window
+            d = {n: dev(t, dtype) for n, t in x.items()}
+            for b in range(2):
+                at = max(n[b] - window - back, 0)
+                d["v"][b, at, :, 7] = value
+                d["k"][b, at, :, 9] = value
+                d["v"][b, n[b]:], d["k"][b, n[b]:] = value, value
+            same(call(d, **kw), ref)
+    # beside that, what the window shows is taken up
+    d["v"][:, n[1] - 2, 0, 7] = float("inf")
+    got = call(d, **kw)
+    same(got, ref, slice(None), np.arange(64) != 7)
+    first = host(got[0])[1, 0, :H // Hkv, 7]
+    assert np.array_equal(first, np.full(first.shape, np.inf)) if window > 1 else np.isfinite(first).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_of_one_query_with_a_window(dtype):
+    say("gradients of one query with a window", dtype)
+    H, Hkv, Sk, kw = 8, 2, 150, {"causal": True, "window": 21}
+    x, _ = single(dtype, H, Hkv, Sk)
+    x["do"] = values(np.random.default_rng(14), (2, 1, H, 64), dtype)
+    ref = bo.attention(x["q"], x["k"], x["v"], x["do"], dtype=dtype, **kw)
+    d = {n: dev(t, dtype) for n, t in x.items()}
+    d["k"][:, Sk - 22, :, 3], d["v"][:, Sk - 23, :, 4] = float("nan"), float("inf")
+    o, lse = call(d, **kw)
+    for n, t in zip(("o", "lse", "dq", "dk", "dv"),
+                    (o, lse, *pamm.attention_backward(d["do"], d["q"], d["k"], d["v"], o, lse, **kw))):
+        close(n, t, ref[n], ref[n + "_tol"])
