@@ -28,6 +28,7 @@ __all__ = ["attention", "attention_backward", "attention_workspace_size", "atten
            "add_rms_norm", "add_rms_norm_fp8", "add_rms_norm_backward", "clip_grad_norm", "MAX_HEAD_DIM"]
 
 MAX_HEAD_DIM = 128
+_FLT_MAX = 3.4028234663852886e38
 
 _i32, _i64, _f32, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 
@@ -454,9 +455,10 @@ def clip_grad_norm(grads, max_norm=None, *, eps: float = 1e-6, out=None, workspa
     grads: a list of bf16 and fp32 tensors on one GPU, dense or 2-D with
     contiguous rows (such as the padded rows of a weight gradient); None
     entries are skipped.  out: as many tensors of the same shapes, bf16 or
-    fp32 (for instance fp32 copies for an optimizer).  max_norm None: the norm
-    alone.  Squares are summed in 64 bits; a norm under the limit leaves
-    gradients in place untouched.  Nothing waits for the GPU."""
+    fp32 (for instance fp32 copies for an optimizer).  max_norm None, or
+    infinity without out: the norm alone; out is always written whole.  Squares
+    are summed in 64 bits; a norm under the limit leaves gradients in place
+    untouched.  Nothing waits for the GPU."""
     where = "clip_grad_norm"
     if isinstance(grads, torch.Tensor):
         grads = [grads]
@@ -505,6 +507,10 @@ def clip_grad_norm(grads, max_norm=None, *, eps: float = 1e-6, out=None, workspa
         elif lay[:2] != lay_o[:2] or (lay[0] == 1 and g.stride() != o.stride()):
             raise ValueError(f"{where}: output {i} must be laid out as its gradient")
         packed.append(_pack_grad(g.data_ptr(), o.data_ptr(), lay[0], lay[1], lay[2], lay_o[2], code, code_o))
+    # the library takes infinity as the norm alone, and as fp32 any number past its range is that
+    limit = math.inf if max_norm is None else float(max_norm)
+    if max_norm is not None and (out is not None or limit != math.inf):
+        limit = min(limit, _FLT_MAX)
     count, arr = len(packed), b"".join(packed)
     if workspace is not None:
         _check_workspace(where, workspace)
@@ -514,8 +520,7 @@ def clip_grad_norm(grads, max_norm=None, *, eps: float = 1e-6, out=None, workspa
     ws, nbytes = _ws(lib.pamm_clip_grad_norm_workspace_size(arr, count), device, workspace, where)
     try:
         _launch("pamm_clip_grad_norm", index, lib.pamm_clip_grad_norm, arr, count,
-                math.inf if max_norm is None else float(max_norm), float(eps), norm.data_ptr(), ws, nbytes,
-                _stream_of(index))
+                limit, float(eps), norm.data_ptr(), ws, nbytes, _stream_of(index))
     except PammError as e:
         if e.status == 10:  # PAMM_ERR_OVERLAP
             raise ValueError(f"{where}: two gradients share memory that is written") from e
