@@ -179,7 +179,6 @@ class PammAttentionBlock(torch.nn.Module):
         self.qkv = PammLinear(dim, (heads + 2 * self.heads_kv) * self.head_dim, bias=False, ratio=ratio, eps=pamm_eps,
                               seed=seed, device=device, dtype=dtype)
         self.out = torch.nn.Linear(heads * self.head_dim, dim, bias=False, device=device, dtype=dtype)
-        self._qkv8 = None
 
     def _heads(self, qkv):
         return qkv.view(*qkv.shape[:2], self.heads + 2 * self.heads_kv, self.head_dim)
@@ -195,22 +194,22 @@ class PammAttentionBlock(torch.nn.Module):
                        dtype=self.qkv.weight.dtype)
 
     def quantize_qkv(self):
-        """Lay out the projection's weight in 8 bits with a scale per output
-        row, once, for step(eight_bits=True)."""
+        """The projection's weight as it is now in 8 bits, with a scale per
+        output row: for step(eight_bits=...), as long as the weight stays."""
         w = self.qkv.weight.detach().float()
         scale = w.abs().amax(1).clamp(min=2.0 ** -100) / 448.0
-        self._qkv8 = ((w / scale[:, None]).to(torch.float8_e4m3fn), scale[None, :])
+        return (w / scale[:, None]).to(torch.float8_e4m3fn), scale[None, :]
 
     @torch.no_grad()
-    def step(self, x, residual, cache: KVCache, *, eight_bits: bool = False):
+    def step(self, x, residual, cache: KVCache, *, eight_bits=False):
         """New tokens x [B x n x dim] over the cache: (out, h) as forward gives
         them for these tokens.  eight_bits: the norm's output and the
-        projection in 8 bits."""
+        projection in 8 bits, with the weight that quantize_qkv() gave; True
+        lays out the present weight in every call, so the block keeps none
+        that an update could leave behind."""
         d = x.shape[-1]
         if eight_bits:
-            if self._qkv8 is None:
-                self.quantize_qkv()
-            w8, w_scale = self._qkv8
+            w8, w_scale = eight_bits if isinstance(eight_bits, tuple) else self.quantize_qkv()
             y8, y_scale, h, _ = add_rms_norm_fp8(_aligned_rows(x.reshape(-1, d)), self.norm.weight,
                                                  _aligned_rows(residual.reshape(-1, d)) if residual is not None else None,
                                                  eps=self.norm.eps)
