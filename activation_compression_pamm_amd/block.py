@@ -26,6 +26,7 @@ import json
 import time
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .autograd import PammLinear, _aligned_rows
 from .block_ops import (add_rms_norm, add_rms_norm_backward, add_rms_norm_fp8, attention, attention_backward,
@@ -58,6 +59,7 @@ class AttentionFunction(torch.autograd.Function):
         return o, lse
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do, _):
         dq, dk, dv = attention_backward(_aligned_heads(do), *ctx.saved_tensors, **ctx.kw)
         return dq, dk, dv, None, None, None, None, None
@@ -81,6 +83,7 @@ class PackedAttentionFunction(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         qkv, o, lse = ctx.saved_tensors
         grad = torch.empty_like(qkv, memory_format=torch.contiguous_format)
@@ -107,6 +110,7 @@ class AddRMSNormFunction(torch.autograd.Function):
         return y.reshape(x.shape), h.reshape(x.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh=None):
         h, weight, rstd = ctx.saved_tensors
         d = h.shape[1]

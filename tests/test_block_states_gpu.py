@@ -51,3 +51,29 @@ def test_eight_bit_weights_kept_by_the_caller():
     block.qkv.weight.data.mul_(2)
     c, _ = block.step(x, None, block.cache(2, 16), eight_bits=kept)
     assert torch.equal(a, c)
+
+
+def layers():
+    from activation_compression_pamm_amd.block import AddRMSNorm, PackedAttentionFunction, differentiable_attention
+
+    g = torch.Generator(device="cuda").manual_seed(8)
+
+    def r(*shape):
+        return torch.randn(*shape, generator=g, device="cuda", requires_grad=True)
+
+    q, k, v, qkv, x = r(2, 20, 4, 32), r(2, 20, 2, 32), r(2, 20, 2, 32), r(2, 20, 8, 32), r(3, 5, 64)
+    norm = AddRMSNorm(64, device="cuda")
+    return {"attention": (q, differentiable_attention(q, k, v, causal=True)),
+            "packed": (qkv, PackedAttentionFunction.apply(qkv, 4, 2, True, 0, None, None)),
+            "norm": (x, norm(x)[0]), "residual": (x, norm(x, r(3, 5, 64))[0])}
+
+
+@pytest.mark.parametrize("name", ["attention", "packed", "norm", "residual"])
+def test_second_derivatives_are_refused(name):
+    """The backward passes have no gradient of their own; one that takes part in
+    a loss has to say so instead of counting as a constant."""
+    x, y = layers()[name]
+    (g,) = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    assert g.requires_grad
+    with pytest.raises(RuntimeError, match="once_differentiable|differentiating twice"):
+        (g.square().sum() + x.sum()).backward()
