@@ -512,9 +512,10 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void at
         attention_dq<DT, ND, true, false>(a, blockIdx.x - dkv_items, row_tiles, shared.dq());
 }
 
-// The marked items of both.  With none marked, as ever but for a NaN or an infinity
-// that a mask hides, a launch and a look at the marks: 4 to 5 us.
-template <int DT, int ND>
+// The marked items of both, with delta as the first pass formed it (ONE), so that
+// what nothing hidden reaches keeps its bits.  With none marked, as ever but for a
+// NaN or an infinity that a mask hides, a launch and a look at the marks: 4 to 5 us.
+template <int DT, int ND, bool ONE>
 __global__ __launch_bounds__(256, 1) void attention_backward_again_kernel(AttnArgs a, int row_tiles, int key_tiles,
                                                                           int items) {
     __shared__ __attribute__((aligned(16))) BackwardShared<DT, ND> shared;
@@ -527,9 +528,9 @@ __global__ __launch_bounds__(256, 1) void attention_backward_again_kernel(AttnAr
         [&](int i) {
             i = __builtin_amdgcn_readfirstlane(i);
             if (i < a.dq_items)
-                attention_dq<DT, ND, true, true>(a, i, row_tiles, shared.dq());
+                attention_dq<DT, ND, ONE, true>(a, i, row_tiles, shared.dq());
             else
-                attention_dkv<DT, ND, true, true>(a, i - a.dq_items, key_tiles, shared.dkv());
+                attention_dkv<DT, ND, ONE, true>(a, i - a.dq_items, key_tiles, shared.dkv());
         });
 }
 
@@ -611,9 +612,15 @@ static void launch_backward(const AttnArgs& a, hipStream_t st) {
             hipLaunchKernelGGL((attention_dkv_kernel<DT, ND>), dim3((unsigned)(items - dq_items)), dim3(256), 0, st, a,
                                (int)key_tiles);
     }
-    if (a.hides && items > 0)
-        hipLaunchKernelGGL((attention_backward_again_kernel<DT, ND>), dim3((unsigned)std::min(items, a.num_cus)),
-                           dim3(256), 0, st, a, (int)tiles, (int)key_tiles, items);
+    if (a.hides && items > 0) {
+        const dim3 grid((unsigned)std::min(items, a.num_cus));
+        if (one)
+            hipLaunchKernelGGL((attention_backward_again_kernel<DT, ND, true>), grid, dim3(256), 0, st, a, (int)tiles,
+                               (int)key_tiles, items);
+        else
+            hipLaunchKernelGGL((attention_backward_again_kernel<DT, ND, false>), grid, dim3(256), 0, st, a, (int)tiles,
+                               (int)key_tiles, items);
+    }
     if (a.nsplit_kv > 1) {
         const int64_t quads = heads * a.Sk * (a.D / 4);
         hipLaunchKernelGGL((attention_dkv_join_kernel<DT>), dim3((unsigned)((2 * quads + 255) / 256)), dim3(256), 0, st,

@@ -116,3 +116,36 @@ def test_gradients_of_one_query_with_a_window(dtype):
     for n, t in zip(("o", "lse", "dq", "dk", "dv"),
                     (o, lse, *pamm.attention_backward(d["do"], d["q"], d["k"], d["v"], o, lse, **kw))):
         close(n, t, ref[n], ref[n + "_tol"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,S,H,Hkv,D,window", [(1, 500, 4, 4, 64, 8), (1, 500, 4, 2, 128, 16), (2, 200, 4, 2, 64, 0),
+                                                (1, 300, 2, 2, 96, 50), (16, 1030, 4, 4, 32, 0)])
+def test_the_second_pass_computes_what_the_first_does(dtype, B, S, H, Hkv, D, window):
+    """With o and lse the same, gradients that nothing reaches of what is not
+    finite have the same bits as without it, whether dq and dk/dv run in one
+    launch or (short windows in bf16, many items) in two."""
+    say("second pass", dtype, B, S, H, Hkv, D, window)
+    rng = np.random.default_rng(15)
+    kw = {"causal": True, "window": window}
+    d = {n: dev(values(rng, s, dtype), dtype) for n, s in (("q", (B, S, H, D)), ("k", (B, S, Hkv, D)), ("v", (B, S, Hkv, D)),
+                                                           ("do", (B, S, H, D)))}
+    o, lse = pamm.attention(d["q"], d["k"], d["v"], **kw)
+
+    def gradients(**change):
+        c = {**d, **change}
+        return pamm.attention_backward(c["do"], c["q"], c["k"], c["v"], o, lse, **kw)
+
+    want = gradients()
+    m = torch.from_numpy(bo.visible(S, S, S, S, True, window)).cuda()
+    for name in ("k", "v", "q", "do"):
+        for at in (S // 2, S - 5):
+            t = d[name].clone()
+            t[0, at, 0, 3] = float("nan")
+            dq, dk, dv = gradients(**{name: t})
+            rows = ~m[:, at] if name in "kv" else torch.arange(S, device="cuda") != at
+            keys = ~(m[~rows].any(0))
+            assert torch.equal(dq[0][rows], want[0][0][rows]), (name, at)
+            assert torch.equal(dk[0][keys], want[1][0][keys]) and torch.equal(dv[0][keys], want[2][0][keys]), (name, at)
+            assert all(torch.equal(x[1:], y[1:]) for x, y in zip((dq, dk, dv), want))
+            assert not torch.isfinite(dk if name in ("q", "do") else dq).all()
