@@ -38,11 +38,12 @@ __all__ = ["AttentionFunction", "PackedAttentionFunction", "AddRMSNormFunction",
 
 def _aligned_heads(t):
     """t itself where its head rows are contiguous and start on 16 bytes, else
-    a contiguous copy (gradients arrive in any layout)."""
+    a contiguous copy of its own (gradients arrive in any layout, also as
+    contiguous views from anywhere in a buffer)."""
     size = t.element_size()
     if t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(s * size % 16 == 0 for s in t.stride()[:-1]):
         return t
-    return t.contiguous()
+    return t.clone(memory_format=torch.contiguous_format)
 
 
 class AttentionFunction(torch.autograd.Function):

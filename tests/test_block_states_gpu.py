@@ -77,3 +77,29 @@ def test_second_derivatives_are_refused(name):
     assert g.requires_grad
     with pytest.raises(RuntimeError, match="once_differentiable|differentiating twice"):
         (g.square().sum() + x.sum()).backward()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradients_at_any_address(dtype):
+    """A contiguous gradient whose rows start off 16 bytes, as a view of a flat buffer."""
+    from activation_compression_pamm_amd.block import AddRMSNorm, PackedAttentionFunction, differentiable_attention
+
+    torch.manual_seed(9)
+
+    def off(like):
+        flat = torch.randn(1 + like.numel(), device="cuda").to(dtype)
+        view = flat[1:].view(like.shape)
+        assert view.is_contiguous() and view.data_ptr() % 16
+        return view
+
+    def r(*shape):
+        return torch.randn(*shape, device="cuda").to(dtype).requires_grad_(True)
+
+    q, k, v, qkv, x = r(2, 33, 4, 32), r(2, 33, 2, 32), r(2, 33, 2, 32), r(2, 33, 8, 32), r(3, 5, 64)
+    norm = AddRMSNorm(64, device="cuda", dtype=dtype)
+    for y, inputs in ((differentiable_attention(q, k, v, causal=True), (q, k, v)),
+                      (PackedAttentionFunction.apply(qkv, 4, 2, True, 0, None, None), (qkv,)), (norm(x)[0], (x,))):
+        g = off(y)
+        a = torch.autograd.grad(y, inputs, g, retain_graph=True)
+        b = torch.autograd.grad(y, inputs, g.clone())
+        assert all(torch.equal(s, t) for s, t in zip(a, b))
