@@ -52,9 +52,9 @@ class AttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, causal, window, scale, q_len, kv_len):
-        kw = {"causal": causal, "window": window, "scale": scale, "q_len": q_len, "kv_len": kv_len}
-        o, lse = attention(q, k, v, **kw)
-        ctx.save_for_backward(q, k, v, o, lse)
+        kw = {"causal": causal, "window": window, "scale": scale}
+        o, lse = attention(q, k, v, q_len=q_len, kv_len=kv_len, **kw)
+        ctx.save_for_backward(q, k, v, o, lse, q_len, kv_len)
         ctx.kw = kw
         ctx.mark_non_differentiable(lse)
         return o, lse
@@ -62,7 +62,8 @@ class AttentionFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, do, _):
-        dq, dk, dv = attention_backward(_aligned_heads(do), *ctx.saved_tensors, **ctx.kw)
+        *saved, q_len, kv_len = ctx.saved_tensors
+        dq, dk, dv = attention_backward(_aligned_heads(do), *saved, q_len=q_len, kv_len=kv_len, **ctx.kw)
         return dq, dk, dv, None, None, None, None, None
 
 
@@ -77,19 +78,20 @@ class PackedAttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, qkv, heads, heads_kv, causal, window, scale, lengths):
-        kw = {"causal": causal, "window": window, "scale": scale, "q_len": lengths, "kv_len": lengths}
-        o, lse = attention(*qkv.split([heads, heads_kv, heads_kv], dim=2), **kw)
-        ctx.save_for_backward(qkv, o, lse)
+        kw = {"causal": causal, "window": window, "scale": scale}
+        o, lse = attention(*qkv.split([heads, heads_kv, heads_kv], dim=2), q_len=lengths, kv_len=lengths, **kw)
+        ctx.save_for_backward(qkv, o, lse, lengths)
         ctx.kw, ctx.sizes = kw, [heads, heads_kv, heads_kv]
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, do):
-        qkv, o, lse = ctx.saved_tensors
+        qkv, o, lse, lengths = ctx.saved_tensors
         grad = torch.empty_like(qkv, memory_format=torch.contiguous_format)
         dq, dk, dv = grad.split(ctx.sizes, dim=2)
-        attention_backward(_aligned_heads(do), *qkv.split(ctx.sizes, dim=2), o, lse, dq=dq, dk=dk, dv=dv, **ctx.kw)
+        attention_backward(_aligned_heads(do), *qkv.split(ctx.sizes, dim=2), o, lse, q_len=lengths, kv_len=lengths,
+                           dq=dq, dk=dk, dv=dv, **ctx.kw)
         return grad, None, None, None, None, None, None
 
 

@@ -103,3 +103,26 @@ def test_gradients_at_any_address(dtype):
         a = torch.autograd.grad(y, inputs, g, retain_graph=True)
         b = torch.autograd.grad(y, inputs, g.clone())
         assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_lengths_changed_before_the_backward_pass(packed):
+    """The backward pass needs the lengths of the forward pass: where they were
+    written over meanwhile it is refused, like any saved tensor's."""
+    from activation_compression_pamm_amd.block import PackedAttentionFunction, differentiable_attention
+
+    torch.manual_seed(10)
+    n = torch.tensor([33, 12], dtype=torch.int32, device="cuda")
+    qkv = torch.randn(2, 33, 8, 32, device="cuda", requires_grad=True)
+
+    def forward():
+        if packed:
+            return PackedAttentionFunction.apply(qkv, 4, 2, True, 0, None, n)
+        return differentiable_attention(*qkv.split([4, 2, 2], dim=2), causal=True, q_len=n, kv_len=n)
+
+    (want,) = torch.autograd.grad(forward().sum(), qkv)
+    assert not want[1, 12:].any() and want[1, :12].any()
+    y = forward()
+    n.sub_(5)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(y.sum(), qkv)
