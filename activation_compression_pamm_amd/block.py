@@ -156,11 +156,17 @@ class KVCache:
 
     def append(self, k, v):
         """k, v [B x n x Hkv x D] behind each sequence's tokens."""
+        batch, room, *head = self.k.shape
+        if k.dim() != 4 or k.shape != v.shape or k.shape[0] != batch or list(k.shape[2:]) != head:
+            raise ValueError(f"KVCache: k and v must be [{batch} x tokens x {head[0]} x {head[1]}], got "
+                             f"{tuple(k.shape)} and {tuple(v.shape)}")
+        if k.dtype != self.k.dtype or v.dtype != self.v.dtype:
+            raise TypeError(f"KVCache: k and v must be {self.k.dtype}, got {k.dtype} and {v.dtype}")
         n = k.shape[1]
-        if self.used + n > self.k.shape[1]:
-            raise ValueError(f"KVCache: {self.used} + {n} tokens do not fit {self.k.shape[1]}")
+        if self.used + n > room:
+            raise ValueError(f"KVCache: {self.used} + {n} tokens do not fit {room}")
         at = self.lengths[:, None].long() + torch.arange(n, device=k.device)
-        rows = torch.arange(k.shape[0], device=k.device)[:, None]
+        rows = torch.arange(batch, device=k.device)[:, None]
         self.k[rows, at] = k
         self.v[rows, at] = v
         self.lengths += n
