@@ -16,6 +16,9 @@ namespace {
 
 constexpr int64_t kMaxSize = 2147483647LL;
 constexpr int64_t kMaxSequence = ((int64_t)1 << 30) - 512;  // positions and their sums fit 32 bits
+// A grid holds less than 2^32 threads, a workgroup 256.  Cutting an axis into parts is left out
+// of the counts below: it is done up to 16 workgroups a unit, for which room is kept.
+constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 8192;
 constexpr int64_t kMaxSpan = (int64_t)1 << 40;  // elements; far beyond any device's memory
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -52,11 +55,18 @@ int attention_sizes(const pamm_attention_t* a) {
     const int64_t rows = mul(a->seq_q, a->heads / a->heads_kv);
     if (rows > kMaxSequence || mul(mul(a->batch, a->heads), a->seq_q) > kMaxSpan) return PAMM_ERR_SHAPE;
     const int64_t heads = mul(a->batch, a->heads_kv);
-    if (mul(heads, 64) > kMaxSize || mul(heads, (rows + 127) / 128) > kMaxSize / 64 ||
+    if (mul(heads, 64) > kMaxSize || mul(heads, (rows + 127) / 128) > kMaxGroups ||
         mul(heads, (a->seq_k + 127) / 128) > kMaxSize / 64 || mul(heads, a->seq_k) > 4 * kMaxSize ||
         mul(mul(a->batch, a->heads), a->seq_q) > 4 * kMaxSize)
         return PAMM_ERR_SHAPE;
     return PAMM_OK;
+}
+
+// The backward pass may run its items, tiles of queries and of keys, in one launch.
+int backward_sizes(const pamm_attention_t* a) {
+    if (int e = attention_sizes(a)) return e;
+    const int64_t heads = a->batch * a->heads_kv, rows = a->seq_q * (a->heads / a->heads_kv);
+    return heads * ((rows + 127) / 128) + heads * ((a->seq_k + 127) / 128) > kMaxGroups ? PAMM_ERR_SHAPE : PAMM_OK;
 }
 
 int heads_check(const pamm_heads_t& t, int64_t batch, int64_t seq, int64_t heads, int dtype) {
@@ -211,11 +221,12 @@ int pamm_attention(const pamm_attention_t* a, void* ws, size_t ws_bytes, void* s
 }
 
 size_t pamm_attention_backward_workspace_size(const pamm_attention_t* a) {
-    return attention_sizes(a) == PAMM_OK ? backward_layout(a).total : 0;
+    return backward_sizes(a) == PAMM_OK ? backward_layout(a).total : 0;
 }
 
 int pamm_attention_backward(const pamm_attention_t* a, const pamm_heads_t* dout, const pamm_heads_t* dq,
                             const pamm_heads_t* dk, const pamm_heads_t* dv, void* ws, size_t ws_bytes, void* stream) {
+    if (int e = backward_sizes(a)) return e;
     if (int e = attention_check(a)) return e;
     if (!dout || !dq || !dk || !dv) return PAMM_ERR_NULL;
     if (int e = heads_check(*dout, a->batch, a->seq_q, a->heads, a->dtype)) return e;
