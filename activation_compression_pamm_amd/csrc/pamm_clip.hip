@@ -176,8 +176,9 @@ __global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipArgs a) {
     for (int i = threadIdx.x; i < a.parts; i += kClipThreads) s += a.part[i];
     const float norm = (float)sqrt(block_sum(s));
     if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
-    float coef = a.max_norm / (norm + a.eps);
-    if (coef > 1.0f) coef = 1.0f;  // NaN stays
+    const float size = norm + a.eps;
+    float coef = size == 0.0f ? 1.0f : a.max_norm / size;  // all gradients are 0: not 0 / 0 of them
+    if (coef > 1.0f) coef = 1.0f;                          // NaN stays
     if (coef == 1.0f && a.in_place) return;
     for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
         const ClipTensor& t = a.t[clip_tensor(a, c)];

@@ -179,8 +179,8 @@ size_t pamm_clip_grad_norm_workspace_size(const pamm_grad_t *grads_host, int64_t
 
 /*
  * norm = sqrt(sum of squares of all elements of all gradients), summed in
- * 64 bits and rounded to fp32; coef = max_norm / (norm + eps), at most 1;
- * out = coef * data.  Where coef is 1, gradients scaled in place are not
+ * 64 bits and rounded to fp32; coef = max_norm / (norm + eps), at most 1 (and
+ * 1 if norm + eps is 0); out = coef * data.  Where coef is 1, gradients scaled in place are not
  * touched.  A NaN norm makes every output NaN; an infinite norm gives coef 0
  * (so infinities become NaN and finite values 0).
  *

@@ -46,3 +46,15 @@ def test_limits_that_are_none():
             pamm.clip_grad_norm(g, bad)
         with pytest.raises(pamm.PammError):
             pamm.clip_grad_norm(g, bad, out=[torch.empty_like(t) for t in g])
+
+
+def test_zero_gradients_under_a_limit_of_zero():
+    """coef is 0 / 0 without eps; what is scaled is 0 all the same."""
+    for eps in (0.0, 1e-6):
+        x, out = torch.zeros(1000, device="cuda"), torch.full((1000,), 7.0, device="cuda")
+        assert float(pamm.clip_grad_norm([x], 0.0, eps=eps, out=[out])) == 0.0
+        assert float(pamm.clip_grad_norm([x], 0.0, eps=eps)) == 0.0
+        assert not x.any() and not out.any()
+        y = torch.full((1000,), 1e-30, device="cuda")
+        pamm.clip_grad_norm([y], 0.0, eps=eps)
+        assert not y.any()
