@@ -5,9 +5,12 @@
 //   dv_j = sum_i P_ij do_i,  dk_j = scale sum_i dS_ij q_i,
 //   dq_i = scale sum_j dS_ij k_j
 //
-// The products that form s and <do, v> start from -lse / scale and -delta, so
-// what comes out needs one multiplication and an exponential to be P, and one
-// more multiplication to be dS.
+// The products that form s and <do, v> start from -lse / scale (bf16) and -delta,
+// so what comes out needs one multiplication and an exponential to be P, and one
+// more multiplication to be dS.  In fp32 s starts from 0 and lse is taken off in
+// the exponent: on top of lse / scale each of a score's D / 2 steps is rounded at
+// that size, which bf16's own rounding of P hides but fp32's does not (gradients of
+// 215 tokens, heads of 96: 1.2e-6 off, from 0 0.5e-6 to 0.6e-6).
 //
 // Two kinds of workgroup, each with its sums in registers and in a fixed order:
 // one owns queries and runs over keys (dq, and delta on the way), one owns keys
@@ -22,11 +25,20 @@ namespace pamm {
 
 __device__ __forceinline__ float score_factor(float scale) { return fmaxf(fabsf(scale) * kLog2e, 1e-36f); }
 
-// What a score starts from: -lse in units of the raw products, so that
-// 2^(c (start + <q, k>)) is the probability.  A row that saw nothing (lse =
-// -infinity) starts from what makes its probabilities 2^(-infinity) = 0.
+// What takes a row's lse off its scores: bf16 -lse in units of the raw products,
+// from which a score starts, so that 2^(c (start + <q, k>)) is the probability;
+// fp32 -lse in log2 units, 2^(c <q, k> + start).  A row that saw nothing (lse =
+// -infinity) has what makes its probabilities 2^(-infinity) = 0.
+template <int DT>
 __device__ __forceinline__ float start_of(float lse, float c) {
-    return lse == -INFINITY ? (c < 0.0f ? INFINITY : -INFINITY) : -lse * kLog2e / c;
+    if constexpr (DT == DT_BF16)
+        return lse == -INFINITY ? (c < 0.0f ? INFINITY : -INFINITY) : -lse * kLog2e / c;
+    else
+        return lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+}
+template <int DT>
+__device__ __forceinline__ float probability(float s, float c, float start) {
+    return __builtin_amdgcn_exp2f(DT == DT_BF16 ? s * c : fmaf(s, c, start));
 }
 
 template <int DT>
@@ -98,7 +110,7 @@ __device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_
     arrived(qf);
     arrived(dof);
     const float c = score_factor(a.scale);
-    float start = start_of(live ? a.lse[at] : 0.0f, c);
+    float start = start_of<DT>(live ? a.lse[at] : 0.0f, c);
     asm volatile("" : "+v"(start));  // as for the operands
 
     TileCopy<DT, ND, BK, 256> kc, vc;
@@ -123,7 +135,7 @@ __device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_
             }
             if (wr.begin < wr.end &&
                 (whole ? key0 < wr.end && key0 + BK > wr.begin : wr.begin >= key0 && wr.end <= key0 + BK)) {
-                f32x16 s = splat(start), dp = splat(-delta);
+                f32x16 s = splat(start), dp = splat(-delta);  // bf16
 #pragma unroll
                 for (int i = 0; i < T::NS; ++i) {
                     s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], 0, rb, i), qf[i], s);
@@ -159,7 +171,7 @@ __device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_
         for (int kb = 0; kb < BK / 32; ++kb) {
             const int key0 = t * BK + kb * 32;
             if (key0 >= wr.end || key0 + 32 <= wr.begin) continue;
-            f32x16 s = splat(start), dp = splat(-delta);
+            f32x16 s = splat(DT == DT_BF16 ? start : 0.0f), dp = splat(-delta);
 #pragma unroll
             for (int i = 0; i < T::NS; ++i) {
                 s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], kb * 32, rb, i), qf[i], s);
@@ -168,7 +180,7 @@ __device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_
             settle<DT>(s);
             settle<DT>(dp);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(s[i] * c) * dp[i];
+            for (int i = 0; i < 16; ++i) s[i] = probability<DT>(s[i], c, start) * dp[i];
             const bool part = key0 < wr.all_lo || key0 + 32 > wr.all_hi;
             if (part) {
 #pragma unroll
@@ -332,7 +344,7 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
                 for (int m = 1; m < LPR; m <<= 1) d += shfl_xor(d, m);
                 if (tid % LPR == 0) rowstat[buf][1][tid / LPR + i * RPP] = -d;
             }
-            if (tid < BQ) rowstat[buf][0][tid] = start_of(stat, c);
+            if (tid < BQ) rowstat[buf][0][tid] = start_of<DT>(stat, c);
         } else if constexpr (ONE) {
             // the threads that copy a row are neighbours
 #pragma unroll
@@ -343,9 +355,9 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
                 const int at = tid + i * 256;
                 if (at < Copy::N && at % T::CPR == 0) rowstat[buf][1][at / T::CPR] = -d;
             }
-            if (tid < BQ) rowstat[buf][0][tid] = start_of(stat, c);
+            if (tid < BQ) rowstat[buf][0][tid] = start_of<DT>(stat, c);
         } else if (tid < 2 * BQ) {
-            rowstat[buf][tid / BQ][tid % BQ] = tid < BQ ? start_of(stat, c) : -stat;
+            rowstat[buf][tid / BQ][tid % BQ] = tid < BQ ? start_of<DT>(stat, c) : -stat;
         }
     };
     int t = n0, g = 0;
@@ -418,7 +430,7 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 __builtin_amdgcn_wave_barrier();
             }
-            f32x16 s = starts(0), dp = starts(1);
+            f32x16 s = DT == DT_BF16 ? starts(0) : f32x16{}, dp = starts(1);
 #pragma unroll
             for (int x = 0; x < T::NS; ++x)
                 s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], 0, rb, x),
@@ -428,8 +440,14 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
                 const uint4 v = x < VR ? vf[x] : *reinterpret_cast<const uint4*>(vl + (x - VR) * 128 * 32);
                 dp = mma_step<DT>(row_operand<DT, ND>(lds[cur][1], 0, rb, x), v, dp);
             }
+            if constexpr (DT == DT_BF16) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(s[e] * c);
+                for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(s[e] * c);
+            } else {
+                const f32x16 lse2 = starts(0);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[e] = probability<DT>(s[e], c, lse2[e]);
+            }
             settle<DT>(dp);
             // some pair of this block is masked?
             bool part = w0 + 32 > Lk || q0 + BQ > Lq;
@@ -484,9 +502,13 @@ __device__ __forceinline__ void attention_dkv(const AttnArgs& a, int id, int key
     }
 }
 
+// Waves a SIMD: as many as registers and LDS can hold without spills (fp32 heads up
+// to 64: 1 x 512, 12 heads of 64, 93 us with two, 103 with one).
 template <int DT, int ND>
-__global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void attention_dkv_kernel(AttnArgs a,
-                                                                                                  int key_tiles) {
+constexpr int kDkvWaves = ND > 2 ? (DT == DT_BF16 ? 2 : 1) : DT == DT_BF16 ? 3 : 2;
+
+template <int DT, int ND>
+__global__ __launch_bounds__(256, kDkvWaves<DT, ND>) void attention_dkv_kernel(AttnArgs a, int key_tiles) {
     __shared__ __attribute__((aligned(16))) DkvShared<DT, ND> shared;
     attention_dkv<DT, ND, false, false>(a, blockIdx.x, key_tiles, shared);
 }
@@ -503,8 +525,8 @@ struct BackwardShared {
 // Both in one launch, the dk/dv items, which take longer, first.  They form delta
 // themselves (reading o too) instead of waiting for the dq items'.
 template <int DT, int ND>
-__global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 3 : 2) : 1) void attention_backward_kernel(
-    AttnArgs a, int row_tiles, int key_tiles, int dkv_items) {
+__global__ __launch_bounds__(256, kDkvWaves<DT, ND>) void attention_backward_kernel(AttnArgs a, int row_tiles,
+                                                                                  int key_tiles, int dkv_items) {
     __shared__ __attribute__((aligned(16))) BackwardShared<DT, ND> shared;
     if ((int)blockIdx.x < dkv_items)
         attention_dkv<DT, ND, true, false>(a, blockIdx.x, key_tiles, shared.dkv());

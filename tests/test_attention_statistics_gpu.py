@@ -122,3 +122,25 @@ def test_every_lane_has_the_corrected_delta(H, Hkv, D):
     want = ref["dk"][:, 16:]
     off, exact = np.linalg.norm(got - want), np.linalg.norm(bo.to_bf16(want) - want)
     assert off <= 1.5 * exact, f"{off / exact:.3f} times the exact gradient's rounding"
+
+
+@pytest.mark.parametrize("B,S,H,Hkv,D,kw", [(4, 215, 2, 2, 96, {}), (1, 31, 8, 4, 128, {"causal": True}), (2, 600, 2, 2, 64, {}),
+                                            (2, 333, 4, 2, 40, {"causal": True}), (1, 512, 2, 1, 128, {"scale": -0.02})])
+def test_precision_of_fp32_gradients(B, S, H, Hkv, D, kw):
+    """P = 2^x with x = log2(e) (s - lse): x, lse and its multiple are rounded at
+    their own size, |x| <= 16 and |lse| log2(e) <= 16 here, each to 2^-21 at most and
+    evenly: three of 2^-21 ln(2) / sqrt(3) add up, squared, to 3.3e-7; the scores'
+    products, |s| <= 8, and those of dout add less, and sums over keys at most as
+    much again: 1e-6 of the gradient.  Scores summed on top of lse / scale instead
+    are rounded at its size in each of their D / 2 steps."""
+    say("fp32 gradients", B, S, H, Hkv, D, kw)
+    rng = np.random.default_rng(16)
+    q, do = values(rng, (B, S, H, D), "f32"), values(rng, (B, S, H, D), "f32")
+    k, v = values(rng, (B, S, Hkv, D), "f32"), values(rng, (B, S, Hkv, D), "f32")
+    ref = bo.attention(q, k, v, do, **kw)
+    qd, kd, vd, dod = (dev(x, "f32") for x in (q, k, v, do))
+    o, lse = pamm.attention(qd, kd, vd, **kw)
+    for n, t in zip(("dq", "dk", "dv"), pamm.attention_backward(dod, qd, kd, vd, o, lse, **kw)):
+        off = np.linalg.norm(t.double().cpu().numpy() - ref[n]) / np.linalg.norm(ref[n])
+        say(n, off)
+        assert off <= 1e-6, f"{n}: {off:.3g}"
