@@ -508,7 +508,7 @@ template <int DT, int ND>
 constexpr int kDkvWaves = ND > 2 ? (DT == DT_BF16 ? 2 : 1) : DT == DT_BF16 ? 3 : 2;
 
 template <int DT, int ND>
-__global__ __launch_bounds__(256, kDkvWaves<DT, ND>) void attention_dkv_kernel(AttnArgs a, int key_tiles) {
+__global__ __launch_bounds__(256, (kDkvWaves<DT, ND>)) void attention_dkv_kernel(AttnArgs a, int key_tiles) {
     __shared__ __attribute__((aligned(16))) DkvShared<DT, ND> shared;
     attention_dkv<DT, ND, false, false>(a, blockIdx.x, key_tiles, shared);
 }
@@ -525,7 +525,7 @@ struct BackwardShared {
 // Both in one launch, the dk/dv items, which take longer, first.  They form delta
 // themselves (reading o too) instead of waiting for the dq items'.
 template <int DT, int ND>
-__global__ __launch_bounds__(256, kDkvWaves<DT, ND>) void attention_backward_kernel(AttnArgs a, int row_tiles,
+__global__ __launch_bounds__(256, (kDkvWaves<DT, ND>)) void attention_backward_kernel(AttnArgs a, int row_tiles,
                                                                                   int key_tiles, int dkv_items) {
     __shared__ __attribute__((aligned(16))) BackwardShared<DT, ND> shared;
     if ((int)blockIdx.x < dkv_items)
