@@ -389,7 +389,8 @@ def add_rms_norm_fp8(x, weight, residual=None, *, eps: float = 1e-6, h=None, q=N
     qscale [n] fp32, h, rstd) with y ~ q * qscale[:, None].
 
     qscale is each row's largest |y| / 448 (at least 2^-126), the row-wise
-    form an 8-bit matrix product takes; y is rounded once, from fp32."""
+    form an 8-bit matrix product takes; y / qscale is rounded once, to nearest
+    even, for bf16 exactly as in the definition."""
     return _norm_forward("add_rms_norm_fp8", x, weight, residual, eps, h, None, q, qscale, True, stream)
 
 

@@ -83,7 +83,8 @@ __device__ __forceinline__ float row_reduce(float v, float (*buf)[16], int& slot
 
 template <int TPR> constexpr int kNormThreads = TPR < 256 ? 256 : TPR;
 
-template <int DT, int TPR, int VPT>
+// Q: the 8-bit output is asked for.
+template <int DT, int TPR, int VPT, bool Q>
 __global__ __launch_bounds__(kNormThreads<TPR>) void add_rms_norm_kernel(NormArgs a) {
     constexpr int P = Elem<DT>::per16, RPB = kNormThreads<TPR> / TPR;
     __shared__ float buf[2][16];
@@ -129,6 +130,25 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void add_rms_norm_kernel(NormArg
         ss = row_reduce<TPR, false>(ss, buf, slot);
         const float rstd = 1.0f / sqrtf(ss / (float)d + a.eps);
         if (a.rstd && tid == 0) a.rstd[row] = rstd;
+        if (a.y) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                float g[P];
+                unpack16<DT>(w[i], g);
+#pragma unroll
+                for (int e = 0; e < P; ++e) g[e] *= v[i][e] * rstd;
+                if ((tid + i * TPR) * P < d)
+                    store16_tail<DT>(a.y + row * a.ldy, (tid + i * TPR) * P, d, pack16<DT>(g));
+            }
+        }
+        if constexpr (!Q) continue;
+        // y / scale = 448 p / max|p| for p = h w 2^k, with rstd = 2^k t, 1 <= t < 2: t
+        // cancels, and for bf16 p is exact, so that elements half way between two
+        // 8-bit values (1 of 3000, whose quotient fp32 holds) are rounded to even as
+        // they should be and not by the errors of rstd, scale and 1 / scale.
+        const uint32_t bits = __float_as_uint(rstd);
+        const float t = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+        const float power = isfinite(rstd) ? __uint_as_float(bits & 0x7f800000u) : NAN;
         float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -136,17 +156,17 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void add_rms_norm_kernel(NormArg
             unpack16<DT>(w[i], g);
 #pragma unroll
             for (int e = 0; e < P; ++e) {
-                v[i][e] = v[i][e] * rstd * g[e];
+                v[i][e] = v[i][e] * power * g[e];
                 top = fmaxf(top, fabsf(v[i][e]));
             }
-            if (a.y && (tid + i * TPR) * P < d)
-                store16_tail<DT>(a.y + row * a.ldy, (tid + i * TPR) * P, d, pack16<DT>(v[i]));
         }
-        if (!a.q) continue;
         top = row_reduce<TPR, true>(top, buf, slot);
-        // at least the smallest normal number, so that its inverse is finite
-        const float scale = fmaxf(top / 448.0f, 1.17549435e-38f), inv = 1.0f / scale;
-        if (tid == 0) a.qscale[row] = scale;
+        // the scale is at least the smallest normal number, so that inverses are finite
+        constexpr float kLeast = 1.17549435e-38f;
+        if (tid == 0) a.qscale[row] = fmaxf(top * t / 448.0f, kLeast);
+        // 448 p / most = (7/8 p) / (most / 512): a quotient and its correction by the remainder
+        const float most = fmaxf(top, 448.0f * kLeast / t), inv = 512.0f / most;
+        const float part = isinf(most) ? 0.0f : most * (1.0f / 512.0f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int col = (tid + i * TPR) * P;
@@ -157,7 +177,8 @@ __global__ __launch_bounds__(kNormThreads<TPR>) void add_rms_norm_kernel(NormArg
                 float u[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    u[j] = v[i][e + j] * inv;  // NaN stays NaN below
+                    const float n = v[i][e + j] * 0.875f, q = n * inv;
+                    u[j] = fmaf(fmaf(-q, part, n), inv, q);  // NaN stays NaN below
                     u[j] = u[j] > 448.0f ? 448.0f : u[j] < -448.0f ? -448.0f : u[j];
                 }
                 if (e & 2)
@@ -332,10 +353,11 @@ hipError_t run_add_rms_norm(const NormArgs& a, int dtype, hipStream_t st) {
     const dim3 grid((unsigned)norm_blocks(a.n, s, false, a.num_cus));
 #define PAMM_RUN(T, V)                                                                                           \
     if (s.tpr == T && s.vpt == V) {                                                                              \
-        if (dtype == DT_BF16)                                                                                    \
-            hipLaunchKernelGGL((add_rms_norm_kernel<DT_BF16, T, V>), grid, dim3(kNormThreads<T>), 0, st, a);     \
-        else                                                                                                     \
-            hipLaunchKernelGGL((add_rms_norm_kernel<DT_F32, T, V>), grid, dim3(kNormThreads<T>), 0, st, a);      \
+        auto* kernel = dtype == DT_BF16 ? (a.q ? add_rms_norm_kernel<DT_BF16, T, V, true>                        \
+                                               : add_rms_norm_kernel<DT_BF16, T, V, false>)                      \
+                                        : (a.q ? add_rms_norm_kernel<DT_F32, T, V, true>                         \
+                                               : add_rms_norm_kernel<DT_F32, T, V, false>);                      \
+        hipLaunchKernelGGL(kernel, grid, dim3(kNormThreads<T>), 0, st, a);                                       \
     }
     PAMM_NORM_CASES(PAMM_RUN)
 #undef PAMM_RUN

@@ -133,7 +133,8 @@ int pamm_attention_backward(const pamm_attention_t *a_host, const pamm_heads_t *
  *   q     [n x d] 8-bit floats (4 exponent and 3 fraction bits, largest 448,
  *         no infinities), leading dimension ldq in bytes        (written; may be NULL)
  *   qscale [n] fp32: max_l |y_il| / 448, at least 2^-126        (written iff q is)
- *         q_il = y_il (1 / qscale_i), rounded to nearest even from the fp32 y
+ *         q_il = y_il / qscale_i as 448 h_il w_l / max_l |h_il w_l|, in which rstd
+ *         cancels, rounded to nearest even: exactly that for bf16, whose products fp32 holds
  *   rstd  [n] fp32                                              (written; may be NULL)
  *
  * x, r, h, y 16-byte aligned with leading dimensions multiples of 16 bytes;
