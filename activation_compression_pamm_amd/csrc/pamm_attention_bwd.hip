@@ -59,8 +59,14 @@ __device__ __forceinline__ float dot16(const uint4& x, const uint4& y) {
 // the rounding of an exact result is 0.0017 and that of dS as much).  The dq side
 // does it before its loop; inside, it cost a tenth.  With a window of up to 32
 // keys every row sees few, and the dq side goes over the keys twice (window 8: dq
-// and dk 0.0027 -> 0.0024).
+// and dk 0.0027 -> 0.0024).  So it does without a causal mask where all keys are two
+// or three tiles (35 keys, 16/4 heads of 32: 1.52 -> 1.45 times the error of an exact
+// result's rounding; 8 x 64 tokens, 12 heads of 64, 17.6 -> 20.2 us for the second
+// launch); from 80 keys on the error is below 1.5 times anyway, and causal rows
+// start with the first 32 keys, where it counts most.
 __device__ __host__ inline bool short_window(const AttnArgs& a) { return a.window > 0 && a.window <= 32; }
+constexpr int kFewKeys = 96;
+inline bool few_keys(const AttnArgs& a) { return !a.causal && a.Sk > 32 && a.Sk <= kFewKeys; }
 
 // dq.  Laid out as the forward pass: transposed scores, a lane owns a query.
 // Tiles of 32 keys, not 64: three waves a SIMD at D = 64 (8 x 1024, 12 heads: 1.7 us
@@ -124,7 +130,7 @@ __device__ __forceinline__ void attention_dq(const AttnArgs& a, int id, int row_
     // delta corrected (see above): all tiles first where a window is short, then the first again
     int cur = 0;
     if constexpr (DT == DT_BF16) {
-        const bool whole = !ONE && t1 - t0 > 1 && short_window(a);
+        const bool whole = !ONE && t1 - t0 > 1 && (short_window(a) || (!a.causal && t1 - t0 <= kFewKeys / BK));
         const int rb = row_base<DT, ND>(), tp = whole ? t1 : t0 + 1;
         float off = 0.0f;
         for (int t = t0; t < tp; ++t) {
@@ -613,8 +619,8 @@ int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t
 template <int DT, int ND>
 static bool one_backward_kernel(const AttnArgs& a, int64_t items) {
     const int resident = DT != DT_BF16 ? 1 : ND <= 2 ? 3 : 2, rounds = ND <= 2 || a.causal ? 2 : 1;
-    // delta of a short window comes from the dq side
-    if (DT == DT_BF16 && a.causal && short_window(a)) return false;
+    // delta of a short window or of few keys comes from the dq side
+    if (DT == DT_BF16 && (short_window(a) || few_keys(a))) return false;
     return items <= (int64_t)a.num_cus * resident * rounds;
 }
 

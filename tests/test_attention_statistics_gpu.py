@@ -144,3 +144,21 @@ def test_precision_of_fp32_gradients(B, S, H, Hkv, D, kw):
         off = np.linalg.norm(t.double().cpu().numpy() - ref[n]) / np.linalg.norm(ref[n])
         say(n, off)
         assert off <= 1e-6, f"{n}: {off:.3g}"
+
+
+@pytest.mark.parametrize("S", [33, 35, 48, 64, 65, 70, 96])
+@pytest.mark.parametrize("H,Hkv,D", [(16, 4, 32), (8, 2, 96), (4, 1, 128), (8, 8, 64)])
+def test_precision_of_bf16_gradients_of_few_keys(S, H, Hkv, D):
+    """The bound of test_precision_of_bf16_gradients where every query sees the
+    same few keys, more than one tile of them."""
+    say("few keys", S, H, Hkv, D)
+    rng = np.random.default_rng(S)
+    q, do = values(rng, (4, S, H, D), "bf16"), values(rng, (4, S, H, D), "bf16")
+    k, v = values(rng, (4, S, Hkv, D), "bf16"), values(rng, (4, S, Hkv, D), "bf16")
+    ref = bo.attention(q, k, v, do, dtype="bf16")
+    qd, kd, vd, dod = (dev(x, "bf16") for x in (q, k, v, do))
+    o, lse = pamm.attention(qd, kd, vd)
+    for n, t in zip(("dq", "dk", "dv"), pamm.attention_backward(dod, qd, kd, vd, o, lse)):
+        want = ref[n]
+        off, exact = np.linalg.norm(t.double().cpu().numpy() - want), np.linalg.norm(bo.to_bf16(want) - want)
+        assert off <= 1.5 * exact, f"{n}: {off / exact:.3f} times the exact gradient's rounding"
