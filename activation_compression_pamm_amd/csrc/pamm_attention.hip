@@ -67,8 +67,8 @@ __device__ __forceinline__ void softmax_update(f32x16& s, float c, Running& st, 
 // whether some are above the slack.  A row that saw nothing yet has the reference
 // kUnseen, against which whatever it sees is infinite (or, for a score that low,
 // right).  For rows up to 64 in bf16, where the softmax of a block takes longer than
-// its products (8192 tokens, 32/8 heads of 64: 324 -> 311 us); with heads of 128 it
-// gains nothing (4 x 2048 tokens: 176 and 177 us).
+// its products (8192 tokens, 32/8 heads of 64: 4% less time); with heads of 128 it
+// gains nothing (4 x 2048 tokens).
 constexpr float kUnseen = -3.402823466e38f;
 
 __device__ __forceinline__ float probabilities(f32x16& s, float c, float ref) {
@@ -105,15 +105,16 @@ __device__ __forceinline__ float score_factor(float scale) { return fmaxf(fabsf(
 
 // Four waves of 32 rows share tiles of 64 keys (32 in fp32 and for rows above 64,
 // where 64 leave two waves a SIMD instead of three: 4 x 2048 tokens, 32 heads of
-// 128, 192 us against 182), which two LDS buffers hold: while one is used, the
-// next tile travels through registers into the other.
+// 128, 5% more time), which two LDS buffers hold: while one is used, the next tile
+// travels through registers into the other.
 //
-// Bound by the matrix and the vector unit together, which one wave uses by
-// turns: at that size the matrix unit is busy 40% of the cycles, vector
-// instructions issue in 52%, and the clock falls below 2 GHz.  Without loads,
-// barriers or softmax it is 3%, 3% and 0% faster.  182 us, 755 TFLOP/s of the
-// pairs that the mask leaves; 8192 tokens, 32/8 heads of 64: 311 us, 885; 8 x
-// 1024, 12 heads of 64: 30.5 us, 420, the end of a 768-workgroup launch.
+// No single unit bounds it: at that size the matrix unit is busy 41% of the
+// cycles, vector instructions issue in 52%, waves wait 29% of theirs, and the clock
+// falls below 2 GHz; without loads, barriers or softmax it is 3%, 3% and 0% faster.
+// A wave has one chain of products, exponentials and products, and each operand
+// read from LDS feeds one product.  174 us, 788 TFLOP/s of the pairs that the mask
+// leaves; 8192 tokens, 32/8 heads of 64: 322 us, 854; 8 x 1024, 12 heads of 64: 30
+// us, 428, whose 768 workgroups, all resident at once, end at very different times.
 template <int DT, int ND>
 struct RowsShared {
     static constexpr int BK = DT == DT_BF16 && ND <= 2 ? 64 : 32;
@@ -280,8 +281,8 @@ __global__ __launch_bounds__(256, 1) void attention_again_kernel(AttnArgs a, int
 // that a row sees, so a query alone never meets a key outside its window.
 //
 // Bound by reading K and V: 64 sequences of 64 to 8192 keys, 8 heads of 128, 1.11
-// GB: 224 us with the join, 4.9 TB/s, where a large copy reaches 4.75.  130 keys
-// of 12 heads: 6 us, one block's latency and the launch.
+// GB: 224 us, 4.95 TB/s (a large copy reaches 4.75), and 5 us for the join.  130
+// keys of 12 heads: 6 us, one block's latency and the launch.
 template <int DT, int ND>
 struct FewShared {
     static constexpr int OP = ND * 32 + 4;  // floats between rows of the merged result

@@ -71,8 +71,8 @@ inline bool few_keys(const AttnArgs& a) { return !a.causal && a.Sk > 32 && a.Sk 
 // dq.  Laid out as the forward pass: transposed scores, a lane owns a query.
 // Tiles of 32 keys, not 64: three waves a SIMD at D = 64 (8 x 1024, 12 heads: 1.7 us
 // less) and fewer registers above.  Three products for each pair; bound as the
-// forward pass (matrix unit busy 41% of the cycles, vector instructions 34%).
-// 4 x 2048 tokens, 32 heads of 128: 280 us, 736 TFLOP/s; 8192, 32/8 of 64: 415 us, 993.
+// forward pass (matrix unit busy 41% of the cycles, vector instructions 35%, waits 35%).
+// 4 x 2048 tokens, 32 heads of 128: 248 us, 832 TFLOP/s; 8192, 32/8 of 64: 406 us, 1015.
 template <int DT, int ND>
 struct DqShared {
     static constexpr int BK = 32;
@@ -225,9 +225,9 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 2 : 1) void attention_dq_kerne
 // 32-byte steps are kept in LDS (spilled, their reload waited for the next
 // tile's loads every time round).  Where there are few key tiles and many queries,
 // the queries of a tile are cut into parts whose sums a second kernel joins.
-// Four products for each pair; with two waves a SIMD waves wait 45% of their
-// cycles and the matrix unit is busy 36%.  4 x 2048 tokens, 32 heads of 128: 405 us,
-// 679 TFLOP/s; 8192, 32/8 of 64: 652 us, 843.
+// Four products for each pair; with two waves a SIMD waves wait 42% of their
+// cycles and the matrix unit is busy 38%.  4 x 2048 tokens, 32 heads of 128: 339 us,
+// 812 TFLOP/s; 8192, 32/8 of 64: 611 us, 900.
 template <int DT, int ND>
 struct DkvShared {
     static constexpr int BQ = 32;
@@ -595,8 +595,8 @@ __global__ __launch_bounds__(256) void attention_dkv_join_kernel(AttnArgs a) {
 // share few keys: the workgroups of a causal mask are then few and uneven.  A
 // part costs a write and a read of fp32 sums, 16 bytes an element of its keys,
 // against 8 Sq G operations, so with 4096 rows or more a part it is lost in
-// the rest (8192 tokens, 32/8 heads of 64: dk/dv 1298 us whole, 808 + 25 us in
-// 4 parts).  Or the device is not full: then parts run side by side, and the
+// the rest (8192 tokens, 32/8 heads of 64: the backward pass takes 1404 us whole,
+// 1033 in 4 parts; 4096: 658 and 305).  Or the device is not full: then parts run side by side, and the
 // joining launch is paid for by a tile of 32 rows in fp32 (4 us) or 8 such
 // tiles in bf16.
 int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int dtype, int num_cus) {
@@ -610,12 +610,12 @@ int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t
 // One launch or two?  One saves the wait between two kernels and fills the end
 // of the first with the second; two form delta once only.  With all items on
 // the device in two rounds of resident workgroups one launch is the faster
-// (bf16, causal: 1 x 512 tokens, 16 heads of 128, 43 us against 62; 4 x 1024, 16 of
-// 128, 111 / 120; 8 x 1024, 12 of 64, 73 / 86; 4 x 512, 8 of 80, 42 / 54; fp32: 4 x
-// 128, 16 of 128, 51 / 82), with more it loses (4 x 2048, 16 of 128: 340 / 295; 8 x
-// 4096, 12 of 64: 843 / 777).
+// (bf16, causal: 1 x 512 tokens, 16 heads of 128, 44 us against 61; 4 x 1024, 16 of
+// 128, 112 / 121; 8 x 1024, 12 of 64, 73 / 83; 4 x 512, 8 of 80, 41 / 53; fp32: 4 x
+// 128, 16 of 128, 57 / 88), with more it loses (4 x 2048, 16 of 128: 335 / 297; 8 x
+// 4096, 12 of 64: 888 / 809).
 // Without a causal mask workgroups end together, and rows above 64 gain in one
-// round only (4 x 1024, 16 of 128: 156 / 144; 4 x 512: 56 / 63).
+// round only (4 x 1024, 16 of 128: 158 / 144; 4 x 512: 55 / 62).
 template <int DT, int ND>
 static bool one_backward_kernel(const AttnArgs& a, int64_t items) {
     const int resident = DT != DT_BF16 ? 1 : ND <= 2 ? 3 : 2, rounds = ND <= 2 || a.causal ? 2 : 1;

@@ -432,9 +432,9 @@ __device__ __forceinline__ bool sees(int key0, int i, const KeyRange& r) {
 // looked through, and one that holds something not finite is multiplied without
 // it, after which the results that do see such an element take it up (its
 // infinity if SIGNED, where b is not negative, else NaN).  In one kernel the two
-// share registers: forward of 4 x 2048 tokens, 32 heads of 128, 172 us became
-// 196 us (a function of its own) or 221 us (inline); the second kernel's look
-// at the marks takes 4 us.
+// share registers: the forward pass of 4 x 2048 tokens, 32 heads of 128, took 14%
+// more time (a function of its own) or 28% (inline); the second kernel's look
+// at the marks takes 4 to 5 us.
 template <int DT, int ND, bool SIGNED, bool SAFE>
 __device__ __forceinline__ void trans_product(const char* tile, int r0, int base, const Packed<DT>& b, bool part,
                                               int row0, const KeyRange& r, f32x16* acc) {

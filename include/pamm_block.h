@@ -141,7 +141,8 @@ int pamm_attention_backward(const pamm_attention_t *a_host, const pamm_heads_t *
  * w 16-byte aligned; q 8-byte aligned with ldq a multiple of 8.  A row holds
  * at most PAMM_MAX_NORM_BYTES (32768 bf16 or 16384 fp32 elements).  What is
  * not finite in a row changes that row alone: a NaN makes all of it NaN, an
- * infinity makes its own place NaN and the others 0.
+ * infinity makes its own place NaN and the others 0.  A row whose sum of
+ * squares passes fp32's range has rstd = 0.
  *
  * Errors: PAMM_ERR_NULL (x, w; h with r; qscale with q; neither y nor q),
  * _DTYPE, _SHAPE, _VALUE (eps negative, infinite or NaN), _ALIGN.
