@@ -24,6 +24,9 @@ __all__ = [
     # the operators around the projection (block_ops.py)
     "attention", "attention_backward", "attention_workspace_size", "attention_backward_workspace_size",
     "add_rms_norm", "add_rms_norm_fp8", "add_rms_norm_backward", "clip_grad_norm", "MAX_HEAD_DIM",
+    # positions and norms of queries and keys (position_ops.py)
+    "rotary", "rotary_frequencies", "qk_norm_rotary", "qk_norm_rotary_backward",
+    "qk_norm_rotary_backward_workspace_size",
 ]
 
 F32 = 0
@@ -386,11 +389,13 @@ def decompress(C, f, alpha, *, out=None, stream=None):
 
 
 def __getattr__(name):
-    # block_ops is built on the helpers above and on torch, which the package
-    # itself does not load; it is imported on first use
+    # these modules are built on the helpers above and on torch, which the
+    # package itself does not load; they are imported on first use
     if name in __all__:
-        from . import block_ops
-        value = getattr(block_ops, name)
-        globals()[name] = value
-        return value
+        from . import block_ops, position_ops
+        for module in (block_ops, position_ops):
+            if name in module.__all__:
+                value = getattr(module, name)
+                globals()[name] = value
+                return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

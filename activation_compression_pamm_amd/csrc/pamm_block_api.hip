@@ -10,35 +10,12 @@
 #include <vector>
 
 #include "pamm_block.h"
+#include "pamm_block_checks.hpp"
 #include "pamm_block_kernels.hpp"
 
+using namespace pamm_checks;
+
 namespace {
-
-constexpr int64_t kMaxSize = 2147483647LL;
-constexpr int64_t kMaxSequence = ((int64_t)1 << 30) - 512;  // positions and their sums fit 32 bits
-// A grid holds less than 2^32 threads, a workgroup 256.  Cutting an axis into parts is left out
-// of the counts below: it is done up to 16 workgroups a unit, for which room is kept.
-constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 8192;
-constexpr int64_t kMaxSpan = (int64_t)1 << 40;  // elements; far beyond any device's memory
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-int elem_size(int dtype) { return dtype == PAMM_BF16 ? 2 : 4; }
-int per16(int dtype) { return 16 / elem_size(dtype); }
-bool dtype_ok(int dtype) { return dtype == PAMM_F32 || dtype == PAMM_BF16; }
-size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
-
-int num_cus() {
-    int dev = 0, cus = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return 256;
-    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) return 256;
-    return cus;
-}
-
-// a * b, or a number beyond every limit if that overflows (a, b >= 0)
-int64_t mul(int64_t a, int64_t b) {
-    int64_t r;
-    return __builtin_mul_overflow(a, b, &r) ? INT64_MAX : r;
-}
 
 // Sizes and scalars of an attention problem, without its pointers.
 int attention_sizes(const pamm_attention_t* a) {
@@ -69,30 +46,13 @@ int backward_sizes(const pamm_attention_t* a) {
     return heads * ((rows + 127) / 128) + heads * ((a->seq_k + 127) / 128) > kMaxGroups ? PAMM_ERR_SHAPE : PAMM_OK;
 }
 
-int heads_check(const pamm_heads_t& t, int64_t batch, int64_t seq, int64_t heads, int dtype) {
-    if (batch == 0 || seq == 0) return PAMM_OK;
-    const int64_t s[3] = {t.stride_b, t.stride_s, t.stride_h}, n[3] = {batch, seq, heads};
-    int64_t span = PAMM_MAX_HEAD_DIM;
-    for (int i = 0; i < 3; ++i) {
-        if (s[i] < 0) return PAMM_ERR_SHAPE;
-        if (n[i] > 1) span = std::max<int64_t>(span, mul(n[i] - 1, s[i]));
-        if (span > kMaxSpan) return PAMM_ERR_SHAPE;
-    }
-    if (!t.data) return PAMM_ERR_NULL;
-    if (!aligned(t.data, 16)) return PAMM_ERR_ALIGN;
-    for (int i = 0; i < 3; ++i)
-        if (n[i] > 1 && s[i] % per16(dtype) != 0) return PAMM_ERR_ALIGN;
-    if (seq > 1 && mul(t.stride_s, 64 * elem_size(dtype)) >= (int64_t)1 << 31) return PAMM_ERR_UNSUPPORTED;
-    return PAMM_OK;
-}
-
 int attention_check(const pamm_attention_t* a) {
     if (int e = attention_sizes(a)) return e;
     const int64_t B = a->batch, H = a->heads;
-    if (int e = heads_check(a->q, B, a->seq_q, H, a->dtype)) return e;
-    if (int e = heads_check(a->k, B, a->seq_k, a->heads_kv, a->dtype)) return e;
-    if (int e = heads_check(a->v, B, a->seq_k, a->heads_kv, a->dtype)) return e;
-    if (int e = heads_check(a->o, B, a->seq_q, H, a->dtype)) return e;
+    if (int e = heads_check(a->q, B, a->seq_q, H, elem_size(a->dtype))) return e;
+    if (int e = heads_check(a->k, B, a->seq_k, a->heads_kv, elem_size(a->dtype))) return e;
+    if (int e = heads_check(a->v, B, a->seq_k, a->heads_kv, elem_size(a->dtype))) return e;
+    if (int e = heads_check(a->o, B, a->seq_q, H, elem_size(a->dtype))) return e;
     if (B > 0 && a->seq_q > 0 && !a->lse) return PAMM_ERR_NULL;
     if (!aligned(a->lse, 4) || !aligned(a->q_len, 4) || !aligned(a->kv_len, 4)) return PAMM_ERR_ALIGN;
     return PAMM_OK;
@@ -166,14 +126,6 @@ BackwardLayout backward_layout(const pamm_attention_t* a) {
     return L;
 }
 
-int ws_check(const void* ws, size_t ws_bytes, size_t need) {
-    if (need == 0) return PAMM_OK;
-    if (!ws || ws_bytes < need) return PAMM_ERR_WORKSPACE;
-    return aligned(ws, 256) ? PAMM_OK : PAMM_ERR_ALIGN;
-}
-
-int status(hipError_t e) { return e == hipSuccess ? PAMM_OK : PAMM_ERR_HIP; }
-
 bool rows_ok(int64_t n, int64_t ld, int64_t d) { return ld >= d && ld <= kMaxSpan && n - 1 <= (kMaxSpan - d) / ld; }
 
 // Sizes of the norm calls; their leading dimensions are checked with each matrix.
@@ -229,10 +181,10 @@ int pamm_attention_backward(const pamm_attention_t* a, const pamm_heads_t* dout,
     if (int e = backward_sizes(a)) return e;
     if (int e = attention_check(a)) return e;
     if (!dout || !dq || !dk || !dv) return PAMM_ERR_NULL;
-    if (int e = heads_check(*dout, a->batch, a->seq_q, a->heads, a->dtype)) return e;
-    if (int e = heads_check(*dq, a->batch, a->seq_q, a->heads, a->dtype)) return e;
-    if (int e = heads_check(*dk, a->batch, a->seq_k, a->heads_kv, a->dtype)) return e;
-    if (int e = heads_check(*dv, a->batch, a->seq_k, a->heads_kv, a->dtype)) return e;
+    if (int e = heads_check(*dout, a->batch, a->seq_q, a->heads, elem_size(a->dtype))) return e;
+    if (int e = heads_check(*dq, a->batch, a->seq_q, a->heads, elem_size(a->dtype))) return e;
+    if (int e = heads_check(*dk, a->batch, a->seq_k, a->heads_kv, elem_size(a->dtype))) return e;
+    if (int e = heads_check(*dv, a->batch, a->seq_k, a->heads_kv, elem_size(a->dtype))) return e;
     const size_t need = pamm_attention_backward_workspace_size(a);
     if (int e = ws_check(ws, ws_bytes, need)) return e;
     if (a->batch == 0) return PAMM_OK;

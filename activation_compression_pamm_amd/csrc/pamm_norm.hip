@@ -13,24 +13,6 @@
 
 namespace pamm {
 
-template <int DT>
-__device__ __forceinline__ uint4 pack16(const float* v) {
-    uint32_t w[4];
-    if constexpr (DT == DT_BF16) {
-        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            b2 p;
-            p[0] = (__bf16)v[2 * i], p[1] = (__bf16)v[2 * i + 1];
-            w[i] = __builtin_bit_cast(uint32_t, p);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[i]);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Store the 16-byte group of element `col` of a row that holds d elements.
 // Results are written past the caches: what reads them comes a whole matrix
 // later (32768 x 4096 bf16 with the 8-bit output: 6% more time without this hint).
