@@ -27,6 +27,8 @@ __all__ = [
     # positions and norms of queries and keys (position_ops.py)
     "rotary", "rotary_frequencies", "qk_norm_rotary", "qk_norm_rotary_backward",
     "qk_norm_rotary_backward_workspace_size",
+    # a cache in 8 bits and attention over it (cache_ops.py)
+    "CacheFP8", "cache_append_fp8", "attention_fp8", "attention_fp8_workspace_size",
 ]
 
 F32 = 0
@@ -392,8 +394,8 @@ def __getattr__(name):
     # these modules are built on the helpers above and on torch, which the
     # package itself does not load; they are imported on first use
     if name in __all__:
-        from . import block_ops, position_ops
-        for module in (block_ops, position_ops):
+        from . import block_ops, cache_ops, position_ops
+        for module in (block_ops, position_ops, cache_ops):
             if name in module.__all__:
                 value = getattr(module, name)
                 globals()[name] = value

@@ -16,90 +16,9 @@
 // row r is position r / G of head r % G.
 #include <algorithm>
 
-#include "pamm_attention_device.hpp"
+#include "pamm_attention_forward.hpp"
 
 namespace pamm {
-
-// Running statistics of one row, and its update by 32 keys.
-//
-// The reference m follows the maximum only when it is exceeded by more than
-// 2^kSlack: until then probabilities up to 2^kSlack are summed against the old
-// reference, which fp32 sums and bf16 products hold with the same relative
-// precision, and the ND x 16 multiplications of a rescale are skipped.
-constexpr float kSlack = 8.0f, kMost = 256.0f;  // kMost = 2^kSlack
-
-struct Running {
-    float m, l;  // m in log2 units; l: this lane's keys only
-};
-
-__device__ __forceinline__ float largest(const f32x16& s) {
-    float top = s[0];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-    return half_max(top);
-}
-
-// s (raw products; masked ones already -inf) becomes the probabilities.
-template <int ND>
-__device__ __forceinline__ void softmax_update(f32x16& s, float c, Running& st, f32x16* acc) {
-    const float top = largest(s) * c;
-    if (__any(top > st.m + kSlack)) {
-        const float m = fmaxf(st.m, top);
-        const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
-        st.l *= f;
-#pragma unroll
-        for (int db = 0; db < ND; ++db)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[db][i] *= f;
-        st.m = m;
-    }
-    const float ref = st.m == -INFINITY ? 0.0f : st.m;
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -ref));
-        sum += s[i];
-    }
-    st.l += sum;
-}
-
-// The same without looking for the maximum: the sum of the probabilities tells
-// whether some are above the slack.  A row that saw nothing yet has the reference
-// kUnseen, against which whatever it sees is infinite (or, for a score that low,
-// right).  For rows up to 64 in bf16, where the softmax of a block takes longer than
-// its products (8192 tokens, 32/8 heads of 64: 4% less time); with heads of 128 it
-// gains nothing (4 x 2048 tokens).
-constexpr float kUnseen = -3.402823466e38f;
-
-__device__ __forceinline__ float probabilities(f32x16& s, float c, float ref) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -ref));
-        sum += s[i];
-    }
-    return sum;
-}
-
-template <int ND>
-__device__ __forceinline__ void raise_reference(const f32x16& s, float c, Running& st, f32x16* acc) {
-    const float m = fmaxf(st.m, largest(s) * c), f = __builtin_amdgcn_exp2f(st.m - m);
-    st.l *= f;
-#pragma unroll
-    for (int db = 0; db < ND; ++db)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[db][i] *= f;
-    st.m = m;
-}
-
-__device__ __forceinline__ void mask_block(f32x16& s, int key0, const KeyRange& r) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (!sees(key0, i, r)) s[i] = -INFINITY;
-}
-
-// Scores' factor in log2 units; its sign is folded into the query operand.
-__device__ __forceinline__ float score_factor(float scale) { return fmaxf(fabsf(scale) * kLog2e, 1e-36f); }
 
 // ---------------------------------------------------------------- many rows
 
@@ -244,16 +163,6 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 3 : 1) void attention_kernel(A
     attention_rows<DT, ND, false>(a, blockIdx.x, row_tiles, shared);
 }
 
-// The mark of a wave is the lse of its first row: NaN.  (One that is NaN by
-// itself is computed twice, with the same result.)
-__device__ __forceinline__ bool is_marked(const AttnArgs& a, const WorkItem& w, int row, int split) {
-    if (row >= a.Sq * a.G) return false;
-    const int b = w.head / a.Hkv, head = w.head % a.Hkv * a.G + row % a.G, pos = row / a.G;
-    const int64_t at = ((int64_t)b * a.H + head) * a.Sq + pos;
-    const float v = a.nsplit > 1 ? a.part_lse[at * a.nsplit + split] : a.lse[at];
-    return v != v;
-}
-
 template <int DT, int ND>
 __global__ __launch_bounds__(256, 1) void attention_again_kernel(AttnArgs a, int row_tiles, int items) {
     __shared__ __attribute__((aligned(16))) RowsShared<DT, ND> shared;
@@ -283,22 +192,12 @@ __global__ __launch_bounds__(256, 1) void attention_again_kernel(AttnArgs a, int
 // Bound by reading K and V: 64 sequences of 64 to 8192 keys, 8 heads of 128, 1.11
 // GB: 224 us, 4.95 TB/s (a large copy reaches 4.75), and 5 us for the join.  130
 // keys of 12 heads: 6 us, one block's latency and the launch.
-template <int DT, int ND>
-struct FewShared {
-    static constexpr int OP = ND * 32 + 4;  // floats between rows of the merged result
-    static constexpr int VT = 32 * Tile<DT, ND>::PITCH;
-    static constexpr int SH = 4 * VT > 32 * OP * 4 ? 4 * VT : 32 * OP * 4;
-    char lds[SH];
-    float stat[4][2][32];
-};
-
 template <int DT, int ND, bool SAFE>
 __device__ __forceinline__ void attention_few(const AttnArgs& a, int id, FewShared<DT, ND>& shared) {
     using T = Tile<DT, ND>;
-    constexpr int OP = FewShared<DT, ND>::OP, VT = FewShared<DT, ND>::VT;
+    constexpr int VT = FewShared<DT, ND>::VT;
     char* lds = shared.lds;
-    auto& stat = shared.stat;
-    const int tid = threadIdx.x, l = tid & 63, wave = wave_id();
+    const int l = threadIdx.x & 63, wave = wave_id();
 
     const WorkItem w = work_item(id, a.B * a.Hkv, a.nsplit, false);
     const int split = w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;
@@ -363,55 +262,7 @@ __device__ __forceinline__ void attention_few(const AttnArgs& a, int id, FewShar
     for (int db = 0; db < ND; ++db) settle<DT>(acc[db]);
     const bool marked = !SAFE && a.hides && !sums_finite<ND>(acc);
 
-    // join the four waves: the common reference first, then the sums in order
-    const float sum = marked ? NAN : half_sum(st.l);  // makes the joined lse NaN
-    if (l < 32) {
-        stat[wave][0][l] = sum == 0.0f ? -INFINITY : st.m;
-        stat[wave][1][l] = sum;
-    }
-    __syncthreads();
-    float m = -INFINITY, total = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) m = fmaxf(m, stat[w][0][row]);
-    const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) total += stat[w][1][row] * __builtin_amdgcn_exp2f(stat[w][0][row] - ref);
-    const float f = sum == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(st.m - ref) / total;
-    float* merged = reinterpret_cast<float*>(lds);
-    for (int w = 0; w < 4; ++w) {
-        if (w == wave && live) {
-#pragma unroll
-            for (int db = 0; db < ND; ++db)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float* to = merged + row * OP + 32 * db + 8 * (i >> 2) + 4 * (l >> 5) + (i & 3);
-                    const float x = sum == 0.0f ? 0.0f : acc[db][i] * f;
-                    *to = w == 0 ? x : *to + x;
-                }
-        }
-        __syncthreads();
-    }
-    const float lse2 = total == 0.0f ? -INFINITY : m + __builtin_amdgcn_logf(total);
-    const int64_t at = ((int64_t)b * a.H + head) * a.Sq + pos;
-    if (tid < 32 && live) {
-        if (a.nsplit > 1)
-            a.part_lse[at * a.nsplit + split] = lse2;
-        else
-            a.lse[at] = lse2 * kLn2;
-    }
-    for (int e = tid; e < rows * a.D; e += 256) {
-        const int r = e / a.D, x = e % a.D, p = r / a.G, h = hk * a.G + r % a.G;
-        const float v = merged[r * OP + x];
-        if (a.nsplit > 1) {
-            a.part_o[((((int64_t)b * a.H + h) * a.Sq + p) * a.nsplit + split) * a.D + x] = v;
-        } else {
-            char* o = a.o.p + b * a.o.sb + p * a.o.ss + h * a.o.sh;
-            if constexpr (DT == DT_BF16)
-                reinterpret_cast<__bf16*>(o)[x] = (__bf16)v;
-            else
-                reinterpret_cast<float*>(o)[x] = v;
-        }
-    }
+    join_waves<DT, ND>(a, shared, acc, st, marked, b, hk, split);
 }
 
 template <int DT, int ND>
@@ -487,6 +338,12 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     if (l == 0) a.lse[at] = total == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
+void launch_attention_join(const AttnArgs& a, int dtype, hipStream_t st) {
+    const dim3 grid((unsigned)(((int64_t)a.B * a.H * a.Sq + 7) / 8));
+    auto* kernel = dtype == DT_BF16 ? attention_join_kernel<DT_BF16> : attention_join_kernel<DT_F32>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, a);
+}
+
 // Single tokens are bound by reading K and V once.  Where the keys' lengths are
 // given they differ, unknown to the host, so the parts are made small enough to
 // even them out: 8 workgroups a unit (64 sequences of up to 8192, 8 heads of
@@ -519,10 +376,7 @@ static void launch_attention(const AttnArgs& a, hipStream_t st) {
         hipLaunchKernelGGL((attention_kernel<DT, ND>), grid, dim3(256), 0, st, a, (int)tiles);
         if (a.hides) hipLaunchKernelGGL((attention_again_kernel<DT, ND>), again, dim3(256), 0, st, a, (int)tiles, items);
     }
-    if (a.nsplit > 1) {
-        const dim3 grid((unsigned)(((int64_t)a.B * a.H * a.Sq + 7) / 8));
-        hipLaunchKernelGGL((attention_join_kernel<DT>), grid, dim3(256), 0, st, a);
-    }
+    if (a.nsplit > 1) launch_attention_join(a, DT, st);
 }
 
 hipError_t run_attention(const AttnArgs& a, int dtype, hipStream_t st) {

@@ -17,28 +17,6 @@ using namespace pamm_checks;
 
 namespace {
 
-// Sizes and scalars of an attention problem, without its pointers.
-int attention_sizes(const pamm_attention_t* a) {
-    if (!a) return PAMM_ERR_NULL;
-    if (!dtype_ok(a->dtype)) return PAMM_ERR_DTYPE;
-    if (a->batch < 0 || a->batch > kMaxSize || a->seq_q < 0 || a->seq_q > kMaxSequence || a->seq_k < 0 ||
-        a->seq_k > kMaxSequence || a->heads < 1 || a->heads > kMaxSize || a->heads_kv < 1 || a->heads_kv > a->heads ||
-        a->heads % a->heads_kv != 0 || a->head_dim < 1 || a->head_dim > PAMM_MAX_HEAD_DIM)
-        return PAMM_ERR_SHAPE;
-    if (a->head_dim % per16(a->dtype) != 0) return PAMM_ERR_ALIGN;
-    if ((a->causal != 0 && a->causal != 1) || !isfinite(a->scale) || a->window < 0 || (a->window > 0 && !a->causal))
-        return PAMM_ERR_VALUE;
-    // rows of one key/value head, elements of lse, workgroups of either kernel
-    const int64_t rows = mul(a->seq_q, a->heads / a->heads_kv);
-    if (rows > kMaxSequence || mul(mul(a->batch, a->heads), a->seq_q) > kMaxSpan) return PAMM_ERR_SHAPE;
-    const int64_t heads = mul(a->batch, a->heads_kv);
-    if (mul(heads, 64) > kMaxSize || mul(heads, (rows + 127) / 128) > kMaxGroups ||
-        mul(heads, (a->seq_k + 127) / 128) > kMaxSize / 64 || mul(heads, a->seq_k) > 4 * kMaxSize ||
-        mul(mul(a->batch, a->heads), a->seq_q) > 4 * kMaxSize)
-        return PAMM_ERR_SHAPE;
-    return PAMM_OK;
-}
-
 // The backward pass may run its items, tiles of queries and of keys, in one launch.
 int backward_sizes(const pamm_attention_t* a) {
     if (int e = attention_sizes(a)) return e;
@@ -56,44 +34,6 @@ int attention_check(const pamm_attention_t* a) {
     if (B > 0 && a->seq_q > 0 && !a->lse) return PAMM_ERR_NULL;
     if (!aligned(a->lse, 4) || !aligned(a->q_len, 4) || !aligned(a->kv_len, 4)) return PAMM_ERR_ALIGN;
     return PAMM_OK;
-}
-
-// Strides in bytes.  That of a dimension with one entry may be anything (it is
-// not checked); kernels form addresses past the last row, which bounds turn
-// into zeros, so rows get a distance of their own length.
-pamm::HeadsArg heads_arg(const pamm_heads_t& t, const pamm_attention_t* a, bool query) {
-    const int64_t e = elem_size(a->dtype), seq = query ? a->seq_q : a->seq_k, heads = query ? a->heads : a->heads_kv;
-    return {reinterpret_cast<char*>(t.data), a->batch > 1 && seq > 0 ? t.stride_b * e : 0,
-            a->batch > 0 && seq > 1 ? t.stride_s * e : a->head_dim * e,
-            a->batch > 0 && seq > 0 && heads > 1 ? t.stride_h * e : 0};
-}
-
-pamm::AttnArgs attention_args(const pamm_attention_t* a) {
-    pamm::AttnArgs r;
-    memset(&r, 0, sizeof r);
-    r.q = heads_arg(a->q, a, true);
-    r.k = heads_arg(a->k, a, false);
-    r.v = heads_arg(a->v, a, false);
-    r.o = heads_arg(a->o, a, true);
-    r.lse = a->lse;
-    r.q_len = a->q_len;
-    r.kv_len = a->kv_len;
-    r.B = (int)a->batch;
-    r.Sq = (int)a->seq_q;
-    r.Sk = (int)a->seq_k;
-    r.H = (int)a->heads;
-    r.Hkv = (int)a->heads_kv;
-    r.G = (int)(a->heads / a->heads_kv);
-    r.D = (int)a->head_dim;
-    r.causal = a->causal;
-    r.window = a->window >= a->seq_k ? 0 : (int)a->window;  // a window as long as the keys hides none
-    // without a causal mask all queries see the same keys; one query alone sees the last ones, from
-    // somewhere inside a block if there is a window
-    r.hides = r.causal && (r.Sq > 1 || r.window > 0);
-    r.scale = a->scale;
-    r.num_cus = num_cus();
-    r.nsplit = r.nsplit_kv = 1;
-    return r;
 }
 
 int splits_of(const pamm_attention_t* a) {

@@ -48,6 +48,8 @@ int attention_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, 
 // Parts into which the dk/dv pass cuts the queries of a key tile.
 int attention_dkv_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, int dtype, int num_cus);
 hipError_t run_attention(const AttnArgs& a, int dtype, hipStream_t st);
+// Joins the parts of the key axis (nsplit > 1).
+void launch_attention_join(const AttnArgs& a, int dtype, hipStream_t st);
 hipError_t run_attention_backward(const AttnArgs& a, int dtype, hipStream_t st);
 
 // Longest row of the RMS norm in 16-byte vectors: 1024 threads hold it in
