@@ -10,11 +10,14 @@ the backward pass:
     o = softmax(q k^T) v                 keeps qkv, o, one number a row
     out = o W_o^T                        keeps o
 
-and the gradients of all layers are clipped by their global norm.  For
-serving, `PammAttentionBlock.step` takes new tokens (one or a chunk) over a
-cache of keys and values, optionally with the norm's output in 8 bits.
+and the gradients of all layers are clipped by their global norm.  Queries and
+keys may be normed for each head and rotated by their positions on the way;
+that is done again in the backward pass from the kept qkv, so it keeps nothing.
+For serving, `PammAttentionBlock.step` takes new tokens (one or a chunk) over a
+cache of keys and values, optionally held in 8 bits, and optionally with the
+norm's output in 8 bits.
 
-    python -m activation_compression_pamm_amd.block [--steps 10] [--json]
+    python -m activation_compression_pamm_amd.block [--steps 10] [--rotary] [--qk-norm] [--cache8] [--json]
 
 trains one block for a few steps on synthetic clustered tokens, then decodes
 with it and compares with the whole forward pass.
@@ -31,9 +34,11 @@ from torch.autograd.function import once_differentiable
 from .autograd import PammLinear, _aligned_rows
 from .block_ops import (add_rms_norm, add_rms_norm_backward, add_rms_norm_fp8, attention, attention_backward,
                         clip_grad_norm)
+from .cache_ops import CacheFP8, attention_fp8, cache_append_fp8
+from .position_ops import qk_norm_rotary, qk_norm_rotary_backward, rotary, rotary_frequencies
 
-__all__ = ["AttentionFunction", "PackedAttentionFunction", "AddRMSNormFunction", "AddRMSNorm", "KVCache",
-           "PammAttentionBlock", "differentiable_attention"]
+__all__ = ["AttentionFunction", "PackedAttentionFunction", "PositionedAttentionFunction", "AddRMSNormFunction",
+           "AddRMSNorm", "KVCache", "KVCache8", "PammAttentionBlock", "differentiable_attention"]
 
 
 def _aligned_heads(t):
@@ -93,6 +98,56 @@ class PackedAttentionFunction(torch.autograd.Function):
         attention_backward(_aligned_heads(do), *qkv.split(ctx.sizes, dim=2), o, lse, q_len=lengths, kv_len=lengths,
                            dq=dq, dk=dk, dv=dv, **ctx.kw)
         return grad, None, None, None, None, None, None
+
+
+class PositionedAttentionFunction(torch.autograd.Function):
+    """PackedAttentionFunction with queries and keys normed for each head and
+    rotated by their positions.  Only qkv, o and lse are kept: what goes into
+    the products is formed again in the backward pass."""
+
+    @staticmethod
+    def _turned(qkv, q_weight, k_weight, inv_freq, sizes, kw, eps):
+        """Queries and keys as the products take them, side by side."""
+        H, K, _ = sizes
+        if q_weight is None:  # one call for both
+            return rotary(qkv[:, :, :H + K], inv_freq, **kw).split([H, K], dim=2)
+        both = torch.empty((*qkv.shape[:2], H + K, qkv.shape[3]), dtype=qkv.dtype, device=qkv.device)
+        q, k, _ = qkv.split(sizes, dim=2)
+        qo, ko = both.split([H, K], dim=2)
+        return qk_norm_rotary(q, k, q_weight, k_weight, inv_freq, eps=eps, q_out=qo, k_out=ko, **kw)
+
+    @staticmethod
+    def forward(ctx, qkv, q_weight, k_weight, inv_freq, positions, heads, heads_kv, causal, window, scale, lengths,
+                interleaved, magnitude, eps):
+        ctx.sizes, ctx.eps = [heads, heads_kv, heads_kv], eps
+        ctx.kw = {"causal": causal, "window": window, "scale": scale}
+        ctx.turn = {"interleaved": interleaved, "magnitude": magnitude}
+        q, k = PositionedAttentionFunction._turned(qkv, q_weight, k_weight, inv_freq, ctx.sizes,
+                                                   dict(ctx.turn, positions=positions), eps)
+        o, lse = attention(q, k, qkv[:, :, heads + heads_kv:], q_len=lengths, kv_len=lengths, **ctx.kw)
+        ctx.save_for_backward(qkv, q_weight, k_weight, inv_freq, positions, o, lse, lengths)
+        return o
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do):
+        qkv, q_weight, k_weight, inv_freq, positions, o, lse, lengths = ctx.saved_tensors
+        turn = dict(ctx.turn, positions=positions)
+        q, k = PositionedAttentionFunction._turned(qkv, q_weight, k_weight, inv_freq, ctx.sizes, turn, ctx.eps)
+        grad = torch.empty_like(qkv, memory_format=torch.contiguous_format)
+        dq, dk, dv = grad.split(ctx.sizes, dim=2)
+        attention_backward(_aligned_heads(do), q, k, qkv[:, :, ctx.sizes[0] + ctx.sizes[1]:], o, lse, q_len=lengths,
+                           kv_len=lengths, dq=dq, dk=dk, dv=dv, **ctx.kw)
+        dwq = dwk = None
+        if q_weight is not None:
+            q, k, _ = qkv.split(ctx.sizes, dim=2)
+            _, _, dwq, dwk = qk_norm_rotary_backward(dq, dk, q, k, q_weight, k_weight, inv_freq, eps=ctx.eps, dq_out=dq,
+                                                     dk_out=dk, **turn)
+            dwq, dwk = dwq.to(q_weight.dtype), dwk.to(k_weight.dtype)
+        else:
+            both = grad[:, :, :ctx.sizes[0] + ctx.sizes[1]]
+            rotary(both, inv_freq, inverse=True, out=both, **turn)
+        return (grad, dwq, dwk, *([None] * 11))
 
 
 class AddRMSNormFunction(torch.autograd.Function):
@@ -172,18 +227,55 @@ class KVCache:
         self.lengths += n
         self.used += n
 
+    def attend(self, q, window=0):
+        """Causal attention of the newest tokens' queries [B x n x H x D]."""
+        return attention(q, self.k[:, :self.used], self.v[:, :self.used], causal=True, window=window,
+                         kv_len=self.lengths)[0]
+
+
+class KVCache8:
+    """KVCache in 8 bits, with a scale for each block of tokens and head: half
+    of bf16's memory, and of what a new token's attention has to read.  Tokens
+    of the last, partial block stay in dtype until it is whole."""
+
+    def __init__(self, batch, room, heads_kv, head_dim, *, block=64, device="cuda", dtype=torch.bfloat16):
+        self.tensors = CacheFP8.empty(batch, room, heads_kv, head_dim, block=block, device=device, dtype=dtype)
+        self.lengths = torch.zeros(batch, device=device, dtype=torch.int32)
+        self.used = 0  # the longest sequence, known on the host
+
+    def append(self, k, v):
+        """k, v [B x n x Hkv x D] behind each sequence's tokens."""
+        room = self.tensors.k.shape[1]
+        if k.dim() == 4 and self.used + k.shape[1] > room:
+            raise ValueError(f"KVCache8: {self.used} + {k.shape[1]} tokens do not fit {room}")
+        cache_append_fp8(self.tensors, k, v, self.lengths)
+        self.used += k.shape[1]
+
+    def attend(self, q, window=0):
+        """Causal attention of the newest tokens' queries [B x n x H x D]."""
+        c = self.tensors
+        return attention_fp8(q, c._replace(k=c.k[:, :self.used], v=c.v[:, :self.used]), self.lengths, causal=True,
+                             window=window)[0]
+
 
 class PammAttentionBlock(torch.nn.Module):
     """Residual addition, norm, PammLinear for queries, keys and values, causal
     attention, output projection.
 
-    forward(x, residual=None, lengths=None): x [B x S x dim] -> (out, h), to be
-    given to the next block as x and residual; lengths [B] int32 are the valid
-    tokens of each sequence."""
+    forward(x, residual=None, lengths=None, positions=None): x [B x S x dim] ->
+    (out, h), to be given to the next block as x and residual; lengths [B] int32
+    are the valid tokens of each sequence, positions [B x S] or [S] int64 or
+    int32 those of the rotation (0, 1, ... by default).
+
+    rotary: how many elements of each query and key head are rotated by their
+    position (True: all), with rotary_base, rotary_interleaved and
+    rotary_scaling (arguments of rotary_frequencies: scaling, factor, ...).
+    qk_norm: queries and keys are normed for each head before that."""
 
     def __init__(self, dim: int, heads: int, heads_kv: int | None = None, *, head_dim: int | None = None,
                  window: int = 0, ratio: int = 512, pamm_eps: float = 0.0, norm_eps: float = 1e-6, seed: int = 0,
-                 device=None, dtype=None):
+                 rotary: int | bool = 0, rotary_base: float = 10000.0, rotary_interleaved: bool = False,
+                 rotary_scaling: dict | None = None, qk_norm: bool = False, device=None, dtype=None):
         super().__init__()
         self.heads, self.heads_kv = heads, heads_kv if heads_kv is not None else heads
         self.head_dim = head_dim if head_dim is not None else dim // heads
@@ -192,19 +284,48 @@ class PammAttentionBlock(torch.nn.Module):
         self.qkv = PammLinear(dim, (heads + 2 * self.heads_kv) * self.head_dim, bias=False, ratio=ratio, eps=pamm_eps,
                               seed=seed, device=device, dtype=dtype)
         self.out = torch.nn.Linear(heads * self.head_dim, dim, bias=False, device=device, dtype=dtype)
+        self.q_norm = self.k_norm = None
+        if qk_norm:
+            self.q_norm, self.k_norm = (torch.nn.Parameter(torch.ones(self.head_dim, device=device, dtype=dtype))
+                                        for _ in range(2))
+        self.interleaved = bool(rotary_interleaved)
+        self.rotary_dim = self.head_dim if rotary is True else int(rotary)
+        if not 0 <= self.rotary_dim <= self.head_dim:
+            raise ValueError(f"PammAttentionBlock: rotary must be at most the head dimension {self.head_dim}, got {rotary}")
+        # 64 bits, whatever the module is cast to: no buffer
+        self._inv_freq, self.magnitude = None, 1.0
+        if self.rotary_dim:
+            self._inv_freq, self.magnitude = rotary_frequencies(self.rotary_dim, rotary_base, device="cpu",
+                                                                **(rotary_scaling or {}))
 
     def _heads(self, qkv):
         return qkv.view(*qkv.shape[:2], self.heads + 2 * self.heads_kv, self.head_dim)
 
-    def forward(self, x, residual=None, lengths=None):
+    def _frequencies(self, device):
+        if self._inv_freq is not None and self._inv_freq.device != device:
+            self._inv_freq = self._inv_freq.to(device)
+        return self._inv_freq
+
+    def forward(self, x, residual=None, lengths=None, positions=None):
         y, h = self.norm(x, residual)
-        o = PackedAttentionFunction.apply(self._heads(self.qkv(y)), self.heads, self.heads_kv, True, self.window, None,
-                                          lengths)
+        qkv = self._heads(self.qkv(y))
+        if self.rotary_dim or self.q_norm is not None:
+            o = PositionedAttentionFunction.apply(qkv, self.q_norm, self.k_norm, self._frequencies(x.device), positions,
+                                                  self.heads, self.heads_kv, True, self.window, None, lengths,
+                                                  self.interleaved, self.magnitude, self.norm.eps)
+        else:
+            if positions is not None:
+                raise ValueError("PammAttentionBlock: positions are given, but the block has no rotary positions")
+            o = PackedAttentionFunction.apply(qkv, self.heads, self.heads_kv, True, self.window, None, lengths)
         return self.out(o.reshape(*x.shape[:2], -1)), h
 
-    def cache(self, batch: int, room: int) -> KVCache:
-        return KVCache(batch, room, self.heads_kv, self.head_dim, device=self.qkv.weight.device,
-                       dtype=self.qkv.weight.dtype)
+    def cache(self, batch: int, room: int, *, eight_bits: bool = False, block: int = 64):
+        """An empty cache for step(): keys and values in the block's type, or
+        with eight_bits in 8 bits, `block` tokens to a scale."""
+        kw = {"device": self.qkv.weight.device, "dtype": self.qkv.weight.dtype}
+        if eight_bits:
+            return KVCache8(batch, room, self.heads_kv, self.head_dim, block=block, **kw)
+        return KVCache(batch, room, self.heads_kv, self.head_dim, **kw)
 
     def quantize_qkv(self):
         """The projection's weight as it is now in 8 bits, with a scale per
@@ -214,9 +335,9 @@ class PammAttentionBlock(torch.nn.Module):
         return (w / scale[:, None]).to(torch.float8_e4m3fn), scale[None, :]
 
     @torch.no_grad()
-    def step(self, x, residual, cache: KVCache, *, eight_bits=False):
+    def step(self, x, residual, cache: KVCache | KVCache8, *, eight_bits=False):
         """New tokens x [B x n x dim] over the cache: (out, h) as forward gives
-        them for these tokens.  eight_bits: the norm's output and the
+        them for these tokens, whose positions follow those in the cache.  eight_bits: the norm's output and the
         projection in 8 bits, with the weight that quantize_qkv() gave; True
         lays out the present weight in every call, so the block keeps none
         that an update could leave behind."""
@@ -231,22 +352,30 @@ class PammAttentionBlock(torch.nn.Module):
         else:
             y, h = self.norm(x, residual)
             qkv = torch.nn.functional.linear(y, self.qkv.weight)
-        q, k, v = self._heads(qkv).split([self.heads, self.heads_kv, self.heads_kv], dim=2)
+        qkv = self._heads(qkv)
+        q, k, v = qkv.split([self.heads, self.heads_kv, self.heads_kv], dim=2)
+        if self.rotary_dim or self.q_norm is not None:  # in place: the projection's output is this call's own
+            kw = {"offset": cache.lengths, "interleaved": self.interleaved, "magnitude": self.magnitude}
+            freq = self._frequencies(x.device)
+            if self.q_norm is not None:
+                qk_norm_rotary(q, k, self.q_norm, self.k_norm, freq, eps=self.norm.eps, q_out=q, k_out=k, **kw)
+            else:
+                both = qkv[:, :, :self.heads + self.heads_kv]
+                rotary(both, freq, out=both, **kw)
         cache.append(k, v)
-        o, _ = attention(q, cache.k[:, :cache.used], cache.v[:, :cache.used], causal=True, window=self.window,
-                         kv_len=cache.lengths)
+        o = cache.attend(q, self.window)
         return self.out(o.reshape(*x.shape[:2], -1)), h
 
 
 def run(steps: int = 10, batch: int = 4, seq: int = 1024, dim: int = 768, heads: int = 12, ratio: int = 64,
-        decode: int = 32) -> dict:
+        decode: int = 32, rotary: bool = False, qk_norm: bool = False, cache8: bool = False) -> dict:
     import numpy as np
 
     from . import synth
 
     torch.manual_seed(0)
     dev, dt = "cuda", torch.bfloat16
-    block = PammAttentionBlock(dim, heads, ratio=ratio, seed=3, device=dev, dtype=dt)
+    block = PammAttentionBlock(dim, heads, ratio=ratio, seed=3, rotary=rotary, qk_norm=qk_norm, device=dev, dtype=dt)
     X = synth.clustered_activations(batch * seq, dim, 64, seed=5, dtype="bf16")
     X = torch.from_numpy(X.view(np.int16)).view(dt).to(dev).reshape(batch, seq, dim)
     target = torch.roll(X, 1, dims=1)  # each position is to give the token before it
@@ -269,7 +398,7 @@ def run(steps: int = 10, batch: int = 4, seq: int = 1024, dim: int = 768, heads:
     block.eval()
     with torch.no_grad():
         whole, _ = block(X)
-    cache = block.cache(batch, seq)
+    cache = block.cache(batch, seq, eight_bits=cache8)
     start = seq - decode
     part, _ = block.step(X[:, :start], None, cache)
     got = [part]
@@ -289,9 +418,12 @@ def run(steps: int = 10, batch: int = 4, seq: int = 1024, dim: int = 768, heads:
 def main():
     ap = argparse.ArgumentParser(description="Train and decode with one PAMM attention block.")
     ap.add_argument("--steps", type=int, default=10)
+    ap.add_argument("--rotary", action="store_true", help="rotary positions")
+    ap.add_argument("--qk-norm", action="store_true", help="norms of queries and keys for each head")
+    ap.add_argument("--cache8", action="store_true", help="decode over a cache in 8 bits")
     ap.add_argument("--json", action="store_true")
     a = ap.parse_args()
-    res = run(a.steps)
+    res = run(a.steps, rotary=a.rotary, qk_norm=a.qk_norm, cache8=a.cache8)
     if a.json:
         print(json.dumps(res))
     else:
