@@ -202,9 +202,16 @@ def attention_backward_workspace_size(q, k, *, causal=False) -> int:
     return int(_lib().pamm_attention_backward_workspace_size(p))
 
 
+def _apart(stride, n, row):
+    """Whether a tensor's entries have addresses of their own, by its outer
+    strides and sizes: heads first, or tokens first (other orders: False)."""
+    (b, s, h), (S, H) = stride[:3], n
+    return (s >= row and h >= S * s and b >= H * h) or (h >= row and s >= H * h and b >= S * s)
+
+
 def _not_overlapping(where, name, t):
     """A written tensor must give every element an address of its own."""
-    if t.is_contiguous():
+    if t.is_contiguous() or (t.dim() == 4 and t.stride(3) == 1 and _apart(t.stride(), t.shape[1:3], t.shape[3])):
         return
     need = 1
     for stride, size in sorted((t.stride(i), t.shape[i]) for i in range(t.dim()) if t.shape[i] > 1):

@@ -16,7 +16,7 @@ from typing import NamedTuple
 import torch
 
 from . import _check_workspace, _on_gpu, load_library
-from .block_ops import (MAX_HEAD_DIM, _HEADS, _code, _heads_tensor, _launch, _lengths, _not_overlapping, _pack_attention,
+from .block_ops import (MAX_HEAD_DIM, _HEADS, _apart, _code, _heads_tensor, _launch, _lengths, _not_overlapping, _pack_attention,
                         _pack_heads, _stream_of, _under, _ws)
 
 __all__ = ["CacheFP8", "cache_append_fp8", "attention_fp8", "attention_fp8_workspace_size"]
@@ -78,40 +78,60 @@ class CacheFP8(NamedTuple):
                    heads(block, dtype), heads(block, dtype))
 
 
+_F8, _F32 = torch.float8_e4m3fn, torch.float32
+
+
 def _cache(where, c, written):
     """The checked cache as a packed pamm_cache8_t."""
     k, v, ks, vs, kt, vt = c
-    kh, vh = _heads_tensor(where, "cache.k", k), _heads_tensor(where, "cache.v", v)
-    kth, vth = _heads_tensor(where, "cache.k_tail", kt), _heads_tensor(where, "cache.v_tail", vt)
-    B, room, H, D = k.shape
-    block = kt.shape[1]
-    if k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
+    shape, tail, dtype = k.shape, kt.shape, kt.dtype
+    kst, vst, kts, vts = k.stride(), v.stride(), kt.stride(), vt.stride()
+    if len(shape) != 4 or len(tail) != 4 or len(vst) != 4 or len(vts) != 4 or not kst[3] == vst[3] == kts[3] == vts[3] == 1:
+        for name, t in (("k", k), ("v", v), ("k_tail", kt), ("v_tail", vt)):
+            _heads_tensor(where, f"cache.{name}", t)
+    B, room, H, D = shape
+    block = tail[1]
+    if k.dtype != _F8 or v.dtype != _F8:
         raise TypeError(f"{where}: the cache's k and v must be float8_e4m3fn, got {k.dtype} and {v.dtype}")
-    if v.shape != k.shape:
+    if v.shape != shape:
         raise ValueError(f"{where}: the cache's k and v must share a shape, got {tuple(k.shape)} and {tuple(v.shape)}")
     if block not in (32, 64, 128):
         raise ValueError(f"{where}: the cache's tails must hold a block of 32, 64 or 128 tokens, got {block}")
-    if kt.shape != (B, block, H, D) or vt.shape != kt.shape:
+    if tail != (B, block, H, D) or vt.shape != tail:
         raise ValueError(f"{where}: the cache's tails must have shape {(B, block, H, D)}, got {tuple(kt.shape)} and "
                          f"{tuple(vt.shape)}")
-    if vt.dtype != kt.dtype:
+    if vt.dtype != dtype:
         raise TypeError(f"{where}: the cache's tails must share a dtype, got {kt.dtype} and {vt.dtype}")
-    need = (B, room // block, H)
-    for name, s in (("k_scale", ks), ("v_scale", vs)):
-        if s.dtype != torch.float32:
-            raise TypeError(f"{where}: the cache's {name} must be float32, got {s.dtype}")
-        # more blocks than the rows in view: of a cache whose k and v are sliced
-        if s.dim() != 3 or (s.shape[0], s.shape[2]) != (B, H) or s.shape[1] < need[1]:
-            raise ValueError(f"{where}: the cache's {name} must have shape {need}, got {tuple(s.shape)}")
-    if written:
+    if ks.dtype != _F32 or vs.dtype != _F32:
+        raise TypeError(f"{where}: the cache's k_scale and v_scale must be float32, got {ks.dtype} and {vs.dtype}")
+    blocks, kss, vss = room // block, ks.shape, vs.shape
+    # more blocks than the rows in view: of a cache whose k and v are sliced
+    for name, n in (("k_scale", kss), ("v_scale", vss)):
+        if len(n) != 3 or n[0] != B or n[2] != H or n[1] < blocks:
+            raise ValueError(f"{where}: the cache's {name} must have shape {(B, blocks, H)}, got {tuple(n)}")
+    kst3, vst3 = ks.stride(), vs.stride()
+    if written and not (_apart(kst, (room, H), D) and _apart(vst, (room, H), D) and _apart(kts, (block, H), D)
+                        and _apart(vts, (block, H), D) and _apart(kst3, (kss[1], H), 1) and _apart(vst3, (vss[1], H), 1)):
         for name, t in zip(c._fields, c):
             _not_overlapping(where, f"cache.{name}", t)
-    return _pack_cache(_code(where, kt), B, room, H, D, block, *kh, *vh, ks.data_ptr(), *ks.stride(), vs.data_ptr(),
-                       *vs.stride(), *kth, *vth)
+    return _pack_cache(_code(where, kt), B, room, H, D, block, k.data_ptr(), *kst[:3], v.data_ptr(), *vst[:3],
+                       ks.data_ptr(), *kst3, vs.data_ptr(), *vst3, kt.data_ptr(), *kts[:3], vt.data_ptr(), *vts[:3])
 
 
-def _named(c):
-    return {f"cache_{n}": t for n, t in zip(c._fields, c)}
+def _one_gpu(where, cache, **tensors):
+    """The GPU that all tensors are on."""
+    index = cache[0].get_device()
+    if index >= 0:
+        for t in cache:
+            if t.get_device() != index:
+                break
+        else:
+            for t in tensors.values():
+                if t is not None and t.get_device() != index:
+                    break
+            else:
+                return index
+    _on_gpu(where, **tensors, **{f"cache_{n}": t for n, t in zip(cache._fields, cache)})  # says which
 
 
 def cache_append_fp8(cache: CacheFP8, k, v, lengths, *, new_len=None, advance: bool = True, stream=None):
@@ -139,14 +159,13 @@ def cache_append_fp8(cache: CacheFP8, k, v, lengths, *, new_len=None, advance: b
     if lengths is None:
         raise ValueError(f"{where}: lengths are needed")
     at, new = _lengths(where, "lengths", lengths, B), _lengths(where, "new_len", new_len, B)
-    _on_gpu(where, k=k, v=v, lengths=lengths, new_len=new_len, **_named(cache))
-    index = k.get_device()
+    index = _one_gpu(where, cache, k=k, v=v, lengths=lengths, new_len=new_len)
     _launch("pamm_cache8_append", index, _lib().pamm_cache8_append, c, _pack_heads(*kh), _pack_heads(*vh), k.shape[1],
             new, at, int(bool(advance)), _stream_of(index))
 
 
 def _attention(where, q, cache, kv_len, causal, window, scale, q_len, o, lse, **others):
-    """The checked arguments as a packed pamm_attention_t and pamm_cache8_t."""
+    """The GPU, and the checked arguments as a packed pamm_attention_t and pamm_cache8_t."""
     qh = _heads_tensor(where, "q", q)
     oh = _heads_tensor(where, "o", o) if o is not None else (0, 0, 0, 0)
     c = _cache(where, cache, False)
@@ -164,16 +183,16 @@ def _attention(where, q, cache, kv_len, causal, window, scale, q_len, o, lse, **
     if lse is not None and (lse.shape != (B, H, Sq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
         raise ValueError(f"{where}: lse must be contiguous float32 of shape {(B, H, Sq)}")
     lengths = _lengths(where, "q_len", q_len, B), _lengths(where, "kv_len", kv_len, B)
-    _on_gpu(where, q=q, kv_len=kv_len, q_len=q_len, o=o, lse=lse, **_named(cache), **others)
+    index = _one_gpu(where, cache, q=q, kv_len=kv_len, q_len=q_len, o=o, lse=lse, **others)
     none = (0, 0, 0, 0)
-    return _pack_attention(_code(where, q), 1 if causal else 0, B, Sq, room, H, Hkv, D, int(window or 0),
+    return index, _pack_attention(_code(where, q), 1 if causal else 0, B, Sq, room, H, Hkv, D, int(window or 0),
                            1.0 / math.sqrt(max(D, 1)) if scale is None else float(scale), *lengths, *qh, *none, *none,
                            *oh, lse.data_ptr() if lse is not None else 0), c
 
 
 def attention_fp8_workspace_size(q, cache: CacheFP8, kv_len=None) -> int:
     """Bytes of workspace ``attention_fp8`` needs for tensors of these shapes."""
-    a, c = _attention("attention_fp8_workspace_size", q, cache, kv_len, False, 0, None, None, None, None)
+    _, a, c = _attention("attention_fp8_workspace_size", q, cache, kv_len, False, 0, None, None, None, None)
     return int(_lib().pamm_cache8_attention_workspace_size(a, c))
 
 
@@ -201,9 +220,9 @@ def attention_fp8(q, cache: CacheFP8, kv_len, *, causal: bool = False, window: i
         _not_overlapping(where, "o", o)
     if lse is None:
         lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=q.device)
-    a, c = _attention(where, q, cache, kv_len, causal, window, scale, q_len, o, lse, workspace=workspace)
+    index, a, c = _attention(where, q, cache, kv_len, causal, window, scale, q_len, o, lse, workspace=workspace)
     _check_workspace(where, workspace)
-    lib, index = _lib(), q.get_device()
+    lib = _lib()
     ws, nbytes = _ws(lib.pamm_cache8_attention_workspace_size(a, c), q.device, workspace, where)
     _launch("pamm_cache8_attention", index, lib.pamm_cache8_attention, a, c, ws, nbytes, _stream_of(index))
     return o, lse

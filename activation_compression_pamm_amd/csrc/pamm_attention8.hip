@@ -15,9 +15,9 @@
 
 namespace pamm {
 
-// 16 8-bit floats as 16 / per16 vectors of the type; exact.
+// 16 8-bit floats as 16 / per16 vectors of the type, bf16 times a power of two; exact.
 template <int DT>
-__device__ __forceinline__ void widen16(const uint4& r, uint4* out) {
+__device__ __forceinline__ void widen16(const uint4& r, uint4* out, float power = 1.0f) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     if constexpr (DT == DT_BF16) {
 #pragma unroll
@@ -25,8 +25,8 @@ __device__ __forceinline__ void widen16(const uint4& r, uint4* out) {
             uint32_t u[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                u[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * i + j], 1.0f, false));
-                u[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * i + j], 1.0f, true));
+                u[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * i + j], power, false));
+                u[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * i + j], power, true));
             }
             out[i] = make_uint4(u[0], u[1], u[2], u[3]);
         }
@@ -49,17 +49,46 @@ struct Wide {
     static constexpr int GROUPS = 2 * ND;
     static constexpr int N = 32 * GROUPS;   // groups of a tile
     // Writes group c of row r to a tile.
-    __device__ static __forceinline__ void put(char* tile, int r, int c, const uint4& raw) {
+    __device__ static __forceinline__ void put(char* tile, int r, int c, const uint4& raw, float power = 1.0f) {
         uint4 v[PER];
-        widen16<DT>(raw, v);
+        widen16<DT>(raw, v, power);
 #pragma unroll
         for (int i = 0; i < PER; ++i) *reinterpret_cast<uint4*>(tile + T::offset(r, PER * c + i)) = v[i];
     }
 };
 
-__device__ __forceinline__ float scale_of(const ScalesArg& s, int b, int block, int h) {
-    return s.p[b * s.sb + block * s.ss + h * s.sh];
-}
+// The scales of 64 tiles to come, one a lane, from which each tile's are read
+// into scalar registers.  Loaded tile by tile, a scale on its way is copied to
+// where the current one was at the loop's end, and that copy waits for all loads
+// (64 queries over ragged 8192 keys, 32/8 heads of 128: 135 us instead of TODO).
+struct TileScales {
+    float v;
+    __device__ __forceinline__ void load(const ScalesArg& s, int b, int h, int block, bool ok) {
+        v = ok ? s.p[b * s.sb + h * s.sh + (int64_t)block * s.ss] : 1.0f;  // the tail's
+    }
+    // waits for them here and not, with all loads since, where they are used
+    __device__ __forceinline__ void arrived() { asm volatile("" : "+v"(v)); }
+    __device__ __forceinline__ float at(int i) const {
+        return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), i));
+    }
+};
+
+// The values' scales of 64 tiles as many rows take them: 2^exponent times `power`, a power of two
+// that the values take on their way into LDS, exactly; the exponent, within 48 of 0, is added to
+// the probabilities' (one addition a tile instead of 16 multiplications), and `inverse` turns
+// their sum back into one of plain probabilities.
+struct TileExponents {
+    TileScales exponent, inverse, power;
+    __device__ __forceinline__ void load(const ScalesArg& s, int b, int h, int block, bool ok) {
+        exponent.load(s, b, h, block, ok);
+    }
+    __device__ __forceinline__ void arrived() {
+        const float v = exponent.v, near = v < 0x1p-40f ? v * 0x1p86f : v > 0x1p40f ? v * 0x1p-80f : v;
+        power.v = v < 0x1p-40f ? 0x1p-86f : v > 0x1p40f ? 0x1p80f : 1.0f;
+        exponent.v = __builtin_amdgcn_logf(near);
+        inverse.v = __builtin_amdgcn_rcpf(near);
+    }
+};
 
 // The start of the tail.
 __device__ __forceinline__ int whole_blocks(const Cache8Args& c, int Lk) { return Lk >> c.block_log << c.block_log; }
@@ -68,6 +97,31 @@ __device__ __forceinline__ int whole_blocks(const Cache8Args& c, int Lk) { retur
 
 // As attention_rows: four waves of 32 rows share tiles of 32 keys in two LDS
 // buffers, the next tile under way in registers.
+//
+// The softmax of a tile and its probabilities times the values' scale, in the
+// exponent, from which the sum is turned back; otherwise as softmax_update.
+template <int ND>
+__device__ __forceinline__ void softmax_update8(f32x16& s, float f, float exponent, float inverse, Running& st, f32x16* acc) {
+    const float top = largest(s) * f;
+    if (__any(top > st.m + kSlack)) {
+        const float m = fmaxf(st.m, top), g = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
+        st.l *= g;
+#pragma unroll
+        for (int db = 0; db < ND; ++db)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[db][i] *= g;
+        st.m = m;
+    }
+    const float from = exponent - (st.m == -INFINITY ? 0.0f : st.m);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], f, from));
+        sum += s[i];
+    }
+    st.l = fmaf(sum, inverse, st.l);
+}
+
 template <int DT, int ND>
 struct Rows8Shared {
     char tile[2][2][32 * Tile<DT, ND>::PITCH];
@@ -116,54 +170,68 @@ __device__ __forceinline__ void attention8_rows(const AttnArgs& a, const Cache8A
     for (int db = 0; db < ND; ++db) acc[db] = f32x16{};
     Running st{-INFINITY, 0.0f};
 
-    // a tile on its way: 8 bits in the first vector of each copy, or the tail's rows
     const char* kbase = a.k.p + b * a.k.sb + hk * a.k.sh;
     const char* vbase = a.v.p + b * a.v.sb + hk * a.v.sh;
-    const char* ktail = c8.kt.p + b * c8.kt.sb + hk * c8.kt.sh;
-    const char* vtail = c8.vt.p + b * c8.vt.sb + hk * c8.vt.sh;
-    TileCopy<DT, ND, 32, 256> kc, vc;
-    float ks = 1.0f, vs = 1.0f, next_ks = 1.0f, next_vs = 1.0f;
+    uint4 kr, vr;
+    TileScales ks, vs;     // fp32
+    TileExponents ve;      // bf16
+    int base = t0;         // the tile of the first lane's scales
     const int group_row = tid / W::GROUPS, group = tid % W::GROUPS;
     const bool takes = (W::N >= 256 || tid < W::N) && group * 16 < a.D;
+    const int kat = takes ? group_row * (int)a.k.ss + group * 16 : kOutside;
+    const int vat = takes ? group_row * (int)a.v.ss + group * 16 : kOutside;
     auto fetch = [&](int t) {
-        const int key0 = t * 32;
-        if (key0 < whole) {
-            kc.r[0] = RowView(kbase + key0 * a.k.ss, (int)a.k.ss, 32, 32, a.D)
-                          .load(takes ? group_row * (int)a.k.ss + group * 16 : kOutside);
-            vc.r[0] = RowView(vbase + key0 * a.v.ss, (int)a.v.ss, 32, 32, a.D)
-                          .load(takes ? group_row * (int)a.v.ss + group * 16 : kOutside);
-            next_ks = scale_of(c8.ks, b, key0 >> c8.block_log, hk);
-            next_vs = scale_of(c8.vs, b, key0 >> c8.block_log, hk);
-        } else {
-            const int at = key0 - whole;
-            kc.fetch(ktail + at * c8.kt.ss, (int)c8.kt.ss, Lk - key0, a.D, tid);
-            vc.fetch(vtail + at * c8.vt.ss, (int)c8.vt.ss, Lk - key0, a.D, tid);
-            next_ks = next_vs = 1.0f;
-        }
+        const int key0 = t * 32, some = t < t1 && key0 < whole ? 32 : 0;
+        kr = RowView(kbase + key0 * a.k.ss, (int)a.k.ss, some, 32, a.D).load(kat);
+        vr = RowView(vbase + key0 * a.v.ss, (int)a.v.ss, some, 32, a.D).load(vat);
     };
     auto put = [&](int t, int to) {
-        if (t * 32 < whole) {
+        const int key0 = t * 32;
+        if (key0 < whole) {
             if (W::N >= 256 || tid < W::N) {
-                W::put(lds[to][0], group_row, group, kc.r[0]);
-                W::put(lds[to][1], group_row, group, vc.r[0]);
+                W::put(lds[to][0], group_row, group, kr);
+                W::put(lds[to][1], group_row, group, vr, DT == DT_BF16 ? ve.power.at(t - base) : 1.0f);
             }
-        } else {
-            kc.put(lds[to][0], tid);
-            vc.put(lds[to][1], tid);
+        } else {  // four tiles at most, which are waited for
+            const int at = key0 - whole;
+            TileCopy<DT, ND, 32, 256> copy;
+            copy.fetch(c8.kt.p + b * c8.kt.sb + hk * c8.kt.sh + at * c8.kt.ss, (int)c8.kt.ss, Lk - key0, a.D, tid);
+            copy.put(lds[to][0], tid);
+            copy.fetch(c8.vt.p + b * c8.vt.sb + hk * c8.vt.sh + at * c8.vt.ss, (int)c8.vt.ss, Lk - key0, a.D, tid);
+            copy.put(lds[to][1], tid);
         }
-        ks = next_ks, vs = next_vs;
     };
-    if (t0 < t1) {
-        fetch(t0);
-        put(t0, 0);
-    }
+    auto scales = [&](int t) {
+        const int at = (t + l) * 32;
+        ks.load(c8.ks, b, hk, at >> c8.block_log, at < whole);
+        if constexpr (DT == DT_BF16)
+            ve.load(c8.vs, b, hk, at >> c8.block_log, at < whole);
+        else
+            vs.load(c8.vs, b, hk, at >> c8.block_log, at < whole);
+        base = t;
+    };
+    auto scales_arrived = [&] {
+        ks.arrived();
+        if constexpr (DT == DT_BF16)
+            ve.arrived();
+        else
+            vs.arrived();
+    };
+    scales(t0);
+    fetch(t0);
+    scales_arrived();
+    if (t0 < t1) put(t0, 0);
     __syncthreads();
     int cur = 0;
     for (int t = t0; t < t1; ++t, cur ^= 1) {
         const bool more = t + 1 < t1;
-        if (more) fetch(t + 1);
+        fetch(t + 1);
         const int rb = opaque(row_base<DT, ND>()), tb = opaque(trans_base<DT, ND>());
         const int key0 = t * 32;
+        if (t + 1 - base > 63) {  // this tile's are used, and the next one's
+            scales(t);
+            scales_arrived();
+        }
         if (key0 < wr.end && key0 + 32 > wr.begin) {
             const bool part = key0 < wr.all_lo || key0 + 32 > wr.all_hi;
             f32x16 s{};
@@ -171,9 +239,15 @@ __device__ __forceinline__ void attention8_rows(const AttnArgs& a, const Cache8A
             for (int i = 0; i < T::NS; ++i) s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], 0, rb, i), qf[i], s);
             settle<DT>(s);
             if (part) mask_block(s, key0, mine);
-            softmax_update<ND>(s, c * ks, st, acc);
+            const float f = c * ks.at(t - base);
+            if constexpr (DT == DT_BF16) {
+                softmax_update8<ND>(s, f, ve.exponent.at(t - base), ve.inverse.at(t - base), st, acc);
+            } else {  // whose precision the exponent's rounding would reach
+                softmax_update<ND>(s, f, st, acc);
+                const float vscale = vs.at(t - base);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] *= vs;
+                for (int i = 0; i < 16; ++i) s[i] *= vscale;
+            }
             Packed<DT> p;
             p.set(s);
             trans_product<DT, ND, true, SAFE>(lds[cur][1], 0, tb, p, part, key0, mine, acc);
@@ -286,26 +360,39 @@ __device__ __forceinline__ void attention8_few(const AttnArgs& a, const Cache8Ar
     };
 
     uint4 kr[ND], vr[ND];
-    float ks = 0.0f, vs = 0.0f;
-    auto fetch = [&](int key0) {
-        const RowView kv(kbase + key0 * a.k.ss, (int)a.k.ss, 32, 32, a.D), vv(vbase + key0 * a.v.ss, (int)a.v.ss, 32, 32, a.D);
+    TileScales ks, vs;
+    auto fetch = [&](int t) {
+        const int key0 = first + t * 32, some = t < p8 ? 32 : 0;
+        const RowView kv(kbase + key0 * a.k.ss, (int)a.k.ss, some, 32, a.D);
+        const RowView vv(vbase + key0 * a.v.ss, (int)a.v.ss, some, 32, a.D);
 #pragma unroll
         for (int j = 0; j < ND; ++j) {
             const int g = 2 * j + half;
-            kr[j] = kv.load(g * 16 < a.D ? row * (int)a.k.ss + g * 16 : kOutside);
+            kr[j] = kv.load_once(g * 16 < a.D ? row * (int)a.k.ss + g * 16 : kOutside);
         }
 #pragma unroll
         for (int j = 0; j < ND; ++j) {
             const int at = l + 64 * j, r = at / W::GROUPS, g = at % W::GROUPS;
-            vr[j] = vv.load(g * 16 < a.D && key0 + r >= br.begin ? r * (int)a.v.ss + g * 16 : kOutside);
+            vr[j] = vv.load_once(g * 16 < a.D && key0 + r >= br.begin ? r * (int)a.v.ss + g * 16 : kOutside);
         }
-        ks = scale_of(c8.ks, b, key0 >> c8.block_log, hk);
-        vs = scale_of(c8.vs, b, key0 >> c8.block_log, hk);
+    };
+    // those of this wave's next 64 tiles
+    auto scales = [&](int t) {
+        const int mine = t + 4 * l, block = (first + mine * 32) >> c8.block_log;
+        ks.load(c8.ks, b, hk, block, mine < p8);
+        vs.load(c8.vs, b, hk, block, mine < p8);
     };
     int t = p0 + wave;
-    if (t < p8) fetch(first + t * 32);
-    for (; t < p8; t += 4) {
+    scales(t);
+    fetch(t);
+    ks.arrived(), vs.arrived();
+    for (int nth = 0; t < p8; t += 4, ++nth) {
         const int key0 = first + t * 32;
+        if (nth == 64) {
+            scales(t);
+            ks.arrived(), vs.arrived();
+            nth = 0;
+        }
         f32x16 s{};
 #pragma unroll
         for (int j = 0; j < ND; ++j) {
@@ -323,9 +410,8 @@ __device__ __forceinline__ void attention8_few(const AttnArgs& a, const Cache8Ar
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        const float k_now = ks, v_now = vs;
-        if (t + 4 < p8) fetch(key0 + 128);
-        consume(s, key0, k_now, v_now);
+        fetch(t + 4);
+        consume(s, key0, ks.at(nth), vs.at(nth));
     }
     for (; t < p1; t += 4) {  // the tail: at most one tile a wave
         const int key0 = first + t * 32, at = key0 - whole;
@@ -378,8 +464,392 @@ __global__ __launch_bounds__(256, 1) void attention8_few_again_kernel(AttnArgs a
         [&](int id) { attention8_few<DT, ND, true>(a, c, __builtin_amdgcn_readfirstlane(id), shared); });
 }
 
+// ------------------------------------------------------------ at most 16 rows
+
+// Single tokens whose key/value heads are shared by up to 16 query heads: 16 x 16
+// products, which take half the registers, exponentials and matrix cycles of the
+// 32 x 32 ones, so four waves a SIMD have loads under way instead of two.
+//
+// A lane holds row (A) or column (B) l % 16 of a product and the 16-byte vector
+// of quarter l / 16 of each step; result element i is D[4 (l / 16) + i][l % 16].
+template <int DT>
+__device__ __forceinline__ f32x4 mma16_step(const uint4& a, const uint4& b, f32x4 c) {
+    if constexpr (DT == DT_BF16) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+    } else {
+        const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[j], y[j], c, 0, 0, 0);
+        return c;
+    }
+}
+
+// 8 8-bit floats as an operand of products over keys.
+typedef float Eight __attribute__((ext_vector_type(8)));
+template <int DT>
+__device__ __forceinline__ auto widen8(uint32_t a, uint32_t b) {
+    if constexpr (DT == DT_BF16) {
+        const uint4 v = make_uint4(
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true)));
+        return __builtin_bit_cast(bf16x8, v);
+    } else {
+        Eight x;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(i ? b : a, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(i ? b : a, true);
+            x[4 * i] = lo[0], x[4 * i + 1] = lo[1], x[4 * i + 2] = hi[0], x[4 * i + 3] = hi[1];
+        }
+        return x;
+    }
+}
+
+// As settle(): results are waited for before any branch (7 wait states after the
+// bf16 product, 11 after the fp32 one).
+__device__ __forceinline__ void settle16(f32x4& d) { asm volatile("s_nop 11" : "+v"(d)); }
+
+// v of the four lanes that hold a column, in each.
+template <typename F>
+__device__ __forceinline__ float quarters(float v, F&& f) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return f(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+
+// A tile of 32 keys or values as it lies in memory, rows PITCH bytes apart: group
+// g of row r at slot g ^ key(r).  Sixteen rows read at one group (keys), and the
+// eight rows of a transposing read (values), fall into different banks as far as
+// their bytes fill a line of 256.
+template <int ND>
+struct Raw {
+    static constexpr int GROUPS = ND == 1 ? 2 : ND == 2 ? 4 : 8, PITCH = 16 * GROUPS, SIZE = 32 * PITCH;
+    static constexpr int LOADS = GROUPS / 2;  // 16 bytes a lane
+    __device__ static __forceinline__ int offset(int r, int g) {
+        return r * PITCH + ((g ^ (r / (256 / PITCH) % GROUPS)) << 4);
+    }
+};
+
+template <int DT, int ND>
+struct OneShared {
+    static constexpr int OP = ND * 32 + 4;  // floats between rows of a wave's result
+    static constexpr int most(int a, int b) { return a > b ? a : b; }
+    // of each wave: keys and values in 8 bits, a tile of the tail's values, the result
+    static constexpr int SLOT = most(most(2 * Raw<ND>::SIZE, 32 * Tile<DT, ND>::PITCH), 16 * OP * 4);
+    char lds[4 * SLOT];
+    float stat[4][2][16];
+};
+
+template <int DT, int ND>
+__device__ __forceinline__ void attention8_one(const AttnArgs& a, const Cache8Args& c8, int id, OneShared<DT, ND>& shared) {
+    using T = Tile<DT, ND>;
+    using W = Wide<DT, ND>;
+    using R = Raw<ND>;
+    constexpr int NJ = (ND + 1) / 2, NB = 2 * ND;  // groups of a key's row in a lane, blocks of 16 elements
+    const int tid = threadIdx.x, l = tid & 63, wave = wave_id(), quarter = l >> 4;
+
+    const WorkItem w = work_item(id, a.B * a.Hkv, a.nsplit, false);
+    const int split = w.item, b = w.head / a.Hkv, hk = w.head % a.Hkv;
+    const int Lq = valid_length(a.q_len, b, a.Sq), Lk = valid_length(a.kv_len, b, a.Sk), whole = whole_blocks(c8, Lk);
+    const int rows = a.Sq * a.G;
+    const int row = l & 15, pos = row / a.G, head = hk * a.G + row % a.G;
+    const bool live = row < rows;
+    KeyRange mine = key_range(a, live ? pos : Lq, Lq, Lk);
+    if (mine.hi < mine.lo) mine.hi = mine.lo;
+    const RowsRange br = rows_range(a, 0, rows, rows, Lq, Lk);
+    const int first = br.begin & ~31, n = br.end > br.begin ? (br.end - first + 31) / 32 : 0;
+    const int per = (n + a.nsplit - 1) / a.nsplit, p0 = split * per, p1 = p0 + per < n ? p0 + per : n;
+    const int eight = whole > first ? (whole - first) / 32 : 0;  // tiles in 8 bits
+    const int p8 = p1 < eight ? p1 : eight;
+
+    const char* kbase = a.k.p + b * a.k.sb + hk * a.k.sh;
+    const char* vbase = a.v.p + b * a.v.sb + hk * a.v.sh;
+    // element of vector i of a row's operand
+    auto element = [&](int i) { return (4 * (i / W::PER) + quarter) * 16 + (i % W::PER) * T::PE; };
+    char* vt = shared.lds + wave * OneShared<DT, ND>::SLOT;
+
+    // Whole lines of a tile a load, which go through LDS: an operand's own 16 bytes of each key would take
+    // half a line a load, and be fetched twice past the caches (115 instead of 127 us, see below).
+    // Loads are issued in any case, past the last tile out of bounds: where a branch may leave
+    // them out, the next wait is for every load instead of the oldest ones.
+    uint4 kr[R::LOADS], vr[R::LOADS];
+    TileScales ks, vs;
+    auto fetch = [&](int t) {
+        const int key0 = first + t * 32, some = t < p8 ? 32 : 0;
+        const RowView kv(kbase + key0 * a.k.ss, (int)a.k.ss, some, 32, a.D);
+        const RowView vv(vbase + key0 * a.v.ss, (int)a.v.ss, some, 32, a.D);
+#pragma unroll
+        for (int j = 0; j < R::LOADS; ++j) {
+            const int at = l + 64 * j, r = at / R::GROUPS, g = at % R::GROUPS;
+            kr[j] = kv.load_once(g * 16 < a.D ? r * (int)a.k.ss + g * 16 : kOutside);
+        }
+#pragma unroll
+        for (int j = 0; j < R::LOADS; ++j) {
+            const int at = l + 64 * j, r = at / R::GROUPS, g = at % R::GROUPS;
+            vr[j] = vv.load_once(g * 16 < a.D && key0 + r >= br.begin ? r * (int)a.v.ss + g * 16 : kOutside);
+        }
+    };
+    auto put = [&] {
+#pragma unroll
+        for (int j = 0; j < R::LOADS; ++j) {
+            const int at = l + 64 * j, to = R::offset(at / R::GROUPS, at % R::GROUPS);
+            *reinterpret_cast<uint4*>(vt + to) = kr[j];
+            *reinterpret_cast<uint4*>(vt + R::SIZE + to) = vr[j];
+        }
+    };
+    // those of this wave's next 64 tiles
+    auto scales = [&](int t) {
+        const int mine = t + 4 * l, block = (first + mine * 32) >> c8.block_log;
+        ks.load(c8.ks, b, hk, block, mine < p8);
+        vs.load(c8.vs, b, hk, block, mine < p8);
+    };
+    int t = p0 + wave;
+    scales(t);
+    fetch(t);
+    uint4 qf[NJ * W::PER];
+    const char* q = a.q.p + b * a.q.sb + pos * a.q.ss + head * a.q.sh;
+#pragma unroll
+    for (int i = 0; i < NJ * W::PER; ++i) {
+        const int e = element(i);
+        qf[i] = make_uint4(0, 0, 0, 0);
+        if (live && pos < Lq && e < a.D) qf[i] = *reinterpret_cast<const uint4*>(q + e * T::ES);
+    }
+    if (a.scale < 0.0f)
+#pragma unroll
+        for (int i = 0; i < NJ * W::PER; ++i) qf[i] = negate16<DT>(qf[i]);
+    ks.arrived(), vs.arrived();
+    const float c = score_factor(a.scale);
+    f32x4 acc[NB];
+#pragma unroll
+    for (int db = 0; db < NB; ++db) acc[db] = f32x4{};
+    Running st{-INFINITY, 0.0f};
+
+    // the softmax of a tile's scores: probabilities times the values' scale
+    auto softmax = [&](f32x4 (&s)[2], float (&p)[8], int key0, float kscale, float vscale) {
+        if (key0 < br.all_lo || key0 + 32 > br.all_hi)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t k = (uint32_t)(key0 + 16 * kb + 4 * quarter + i - mine.lo);
+                    if (k >= (uint32_t)(mine.hi - mine.lo)) s[kb][i] = -INFINITY;
+                }
+        const float f = c * kscale;
+        float top = s[0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i >> 2][i & 3]);
+        top = quarters(top, [](float x, float y) { return fmaxf(x, y); }) * f;
+        if (__any(top > st.m + kSlack)) {
+            const float m = fmaxf(st.m, top), g = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
+            st.l *= g;
+#pragma unroll
+            for (int db = 0; db < NB; ++db) acc[db] *= g;
+            st.m = m;
+        }
+        const float ref = st.m == -INFINITY ? 0.0f : st.m;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(fmaf(s[i >> 2][i & 3], f, -ref));
+            sum += p[i];
+            p[i] *= vscale;
+        }
+        st.l += sum;
+    };
+    // acc[db] += 16 columns of the values x p.  Contraction place 8 (l / 16) + i is key
+    // 4 (l / 16) + i, 16 more for i >= 4, for both operands.
+    auto product = [&](int db, const auto& x, const float (&p)[8]) {
+        if constexpr (DT == DT_BF16) {
+            bf16x8 pk;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pk[i] = (__bf16)p[i];
+            acc[db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, pk, acc[db], 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[db] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], p[i], acc[db], 0, 0, 0);
+        }
+    };
+    // where this lane's part of the transposing reads lies
+    const int vrow = 4 * quarter + ((l & 15) >> 1 & 3) + 16 * ((l & 15) >> 3);
+    const int vbase8 = R::SIZE + R::offset(vrow, 0) + (l & 1) * 8, kbase8 = R::offset(row, 0);
+
+    for (int nth = 0; t < p8; t += 4, ++nth) {
+        const int key0 = first + t * 32;
+        if (nth == 64) {
+            scales(t);
+            ks.arrived(), vs.arrived();
+            nth = 0;
+        }
+        __builtin_amdgcn_wave_barrier();
+        put();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        fetch(t + 4);
+        const int kat = opaque(kbase8), vat = opaque(vbase8);
+        f32x4 s[2] = {f32x4{}, f32x4{}};
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                // rows 16 apart share a key; a quarter's group is 4 j + quarter
+                const int slot = 4 * j + quarter;
+                uint4 raw = *reinterpret_cast<const uint4*>(vt + 16 * kb * R::PITCH + (kat ^ (slot << 4)));
+                if (ND == 1 && quarter > 1) raw = make_uint4(0, 0, 0, 0);  // past the row
+                uint4 kf[W::PER];
+                widen16<DT>(raw, kf);
+#pragma unroll
+                for (int i = 0; i < W::PER; ++i) s[kb] = mma16_step<DT>(kf[i], qf[W::PER * j + i], s[kb]);
+            }
+        settle16(s[0]);
+        settle16(s[1]);
+        float p[8];
+        softmax(s, p, key0, ks.at(nth), vs.at(nth));
+#pragma unroll
+        for (int db = 0; db < NB; ++db) {
+            typedef int i32x2 __attribute__((ext_vector_type(2)));
+            typedef __attribute__((address_space(3))) i32x2* lds_i2;
+            const i32x2 raw = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i2)(vt + (vat ^ (db << 4))));
+            product(db, widen8<DT>(raw[0], raw[1]), p);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    for (; t < p1; t += 4) {  // the tail: at most one tile a wave
+        const int key0 = first + t * 32, at = key0 - whole;
+        const RowView kv(c8.kt.p + b * c8.kt.sb + hk * c8.kt.sh + at * c8.kt.ss, (int)c8.kt.ss, Lk - key0, 32, a.D * T::ES);
+        const RowView vv(c8.vt.p + b * c8.vt.sb + hk * c8.vt.sh + at * c8.vt.ss, (int)c8.vt.ss, Lk - key0, 32, a.D * T::ES);
+        f32x4 s[2] = {f32x4{}, f32x4{}};
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            uint4 kf[NJ * W::PER];
+#pragma unroll
+            for (int i = 0; i < NJ * W::PER; ++i) {
+                const int e = element(i);
+                kf[i] = kv.load(e < a.D ? (16 * kb + row) * (int)c8.kt.ss + e * T::ES : kOutside);
+            }
+#pragma unroll
+            for (int i = 0; i < NJ * W::PER; ++i) s[kb] = mma16_step<DT>(kf[i], qf[i], s[kb]);
+        }
+        settle16(s[0]);
+        settle16(s[1]);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 4
+        for (int i = 0; i < 32 * T::CPR / 64; ++i) {
+            const int at2 = l + 64 * i, r = at2 / T::CPR, g = at2 % T::CPR;
+            const uint4 v = vv.load(g * T::PE < a.D && key0 + r >= br.begin ? r * (int)c8.vt.ss + g * 16 : kOutside);
+            *reinterpret_cast<uint4*>(vt + T::offset(r, g)) = v;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        float p[8];
+        softmax(s, p, key0, 1.0f, 1.0f);
+        const int base = T::offset(4 * quarter + ((l & 15) >> 2), (l & 3) >> 1) + (l & 1) * 8;
+#pragma unroll
+        for (int db = 0; db < NB; ++db) {
+            if constexpr (DT == DT_BF16) {
+                typedef __attribute__((address_space(3))) s16x4* lds_s4;
+                typedef short s16x8 __attribute__((ext_vector_type(8)));
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(vt + (base ^ (db << 5))));
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(vt + 16 * T::PITCH + (base ^ (db << 5))));
+                const s16x8 x = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                product(db, __builtin_bit_cast(bf16x8, x), p);
+            } else {
+                Eight x;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int key = 16 * (i >> 2) + 4 * quarter + (i & 3), e = 16 * db + row;
+                    x[i] = *reinterpret_cast<const float*>(vt + T::offset(key, e >> 2) + (e & 3) * 4);
+                }
+                product(db, x, p);
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+
+    uint32_t big = 0;
+#pragma unroll
+    for (int db = 0; db < NB; ++db) {
+        settle16(acc[db]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) big = max(big, __float_as_uint(acc[db][i]) & 0x7fffffffu);
+    }
+    const bool marked = a.hides && !__all(big < 0x7f800000u);
+
+    // join the four waves: the common reference first, then the sums in order
+    constexpr int OP = OneShared<DT, ND>::OP, SLOT = OneShared<DT, ND>::SLOT;
+    const float sum = marked ? NAN : quarters(st.l, [](float x, float y) { return x + y; });
+    if (l < 16) {
+        shared.stat[wave][0][l] = sum == 0.0f ? -INFINITY : st.m;
+        shared.stat[wave][1][l] = sum;
+    }
+    __syncthreads();
+    float m = -INFINITY, total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, shared.stat[i][0][row]);
+    const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) total += shared.stat[i][1][row] * __builtin_amdgcn_exp2f(shared.stat[i][0][row] - ref);
+    const float f = sum == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(st.m - ref) / total;
+    if (live)
+#pragma unroll
+        for (int db = 0; db < NB; ++db) {
+            float4 x = make_float4(acc[db][0] * f, acc[db][1] * f, acc[db][2] * f, acc[db][3] * f);
+            if (sum == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            *reinterpret_cast<float4*>(vt + (row * OP + 16 * db + 4 * quarter) * 4) = x;
+        }
+    const float lse2 = total == 0.0f ? -INFINITY : m + __builtin_amdgcn_logf(total);
+    const int64_t at = ((int64_t)b * a.H + head) * a.Sq + pos;
+    if (tid < 16 && live) {
+        if (a.nsplit > 1)
+            a.part_lse[at * a.nsplit + split] = lse2;
+        else
+            a.lse[at] = lse2 * kLn2;
+    }
+    __syncthreads();
+    const int per_row = a.D / 4;
+    for (int e = tid; e < rows * per_row; e += 256) {
+        const int r = e / per_row, x = (e - r * per_row) * 4, p = r / a.G, h = hk * a.G + r % a.G;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 u = *reinterpret_cast<const float4*>(shared.lds + i * SLOT + (r * OP + x) * 4);
+            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        }
+        if (a.nsplit > 1) {
+            *reinterpret_cast<float4*>(a.part_o + ((((int64_t)b * a.H + h) * a.Sq + p) * a.nsplit + split) * a.D + x) = v;
+            continue;
+        }
+        char* o = a.o.p + b * a.o.sb + p * a.o.ss + h * a.o.sh + x * T::ES;
+        if constexpr (DT == DT_BF16) {
+            bf16x2 y, z;
+            y[0] = (__bf16)v.x, y[1] = (__bf16)v.y, z[0] = (__bf16)v.z, z[1] = (__bf16)v.w;
+            *reinterpret_cast<uint2*>(o) = make_uint2(__builtin_bit_cast(uint32_t, y), __builtin_bit_cast(uint32_t, z));
+        } else {
+            *reinterpret_cast<float4*>(o) = v;
+        }
+    }
+}
+
+template <int DT, int ND>
+__global__ __launch_bounds__(256, DT == DT_BF16 ? 3 : 2) void attention8_one_kernel(AttnArgs a, Cache8Args c) {
+    __shared__ __attribute__((aligned(16))) OneShared<DT, ND> shared;
+    attention8_one<DT, ND>(a, c, blockIdx.x, shared);
+}
+
+// Few rows: two workgroups a unit, and parts of at least 1024 keys.  A second launch and the
+// parts' memory cost a call 7 us (1 x 1024 keys, 12 heads of 64: 16.9 us whole, 22 to 24 in
+// parts; 8192, 8 heads of 128: 57.7 whole, 26.9 in 4, 25.2 in 8, 24.5 in 16).  Where the
+// heads fill the device, parts gain nothing, though lengths differ (64 sequences of up to 8192 keys,
+// 8 heads of 128: 101 us whole, 99, 99 and 103 in 2, 4 and 8; of 8192 each: 161, 177, 171 and 177).
+// Many rows are cut as over a cache that is not in 8 bits.
 int attention8_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, bool lengths, int num_cus) {
-    return attention_splits(B, Sq, Sk, Hkv, G, lengths, num_cus);
+    if (Sq * G > kFewRows) return attention_splits(B, Sq, Sk, Hkv, G, lengths, num_cus);
+    const int64_t blocks = B * Hkv, want = 2 * (int64_t)num_cus;
+    if (blocks == 0 || blocks >= want) return 1;
+    const int64_t n = std::min((want + blocks - 1) / blocks, (Sk + 1023) / 1024);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(n, kMaxSplits));
 }
 
 template <int DT, int ND>
@@ -388,7 +858,10 @@ static void launch_attention8(const AttnArgs& a, const Cache8Args& c, hipStream_
     const int items = (int)((int64_t)a.B * a.Hkv * tiles * a.nsplit);
     const dim3 grid((unsigned)items), again((unsigned)std::min(items, a.num_cus));
     if (rows <= kFewRows) {
-        hipLaunchKernelGGL((attention8_few_kernel<DT, ND>), grid, dim3(256), 0, st, a, c);
+        if (rows <= 16)
+            hipLaunchKernelGGL((attention8_one_kernel<DT, ND>), grid, dim3(256), 0, st, a, c);
+        else
+            hipLaunchKernelGGL((attention8_few_kernel<DT, ND>), grid, dim3(256), 0, st, a, c);
         if (a.hides) hipLaunchKernelGGL((attention8_few_again_kernel<DT, ND>), again, dim3(256), 0, st, a, c, items);
     } else {
         hipLaunchKernelGGL((attention8_kernel<DT, ND>), grid, dim3(256), 0, st, a, c, (int)tiles);

@@ -328,6 +328,10 @@ struct RowView {
     __device__ __forceinline__ uint4 load(int offset) const {
         return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, offset, 0, 0));
     }
+    // the same for what is read once: it does not push other lines out of the caches
+    __device__ __forceinline__ uint4 load_once(int offset) const {
+        return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, offset, 0, 2));
+    }
 };
 constexpr int kOutside = (int)0x80000000u;  // an offset past every view's end
 

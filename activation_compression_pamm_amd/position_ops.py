@@ -138,7 +138,7 @@ def _like(where, name, t, like):
 
 def _problem(where, q, k, qo, ko, q_weight, k_weight, inv_freq, positions, offset, interleaved, magnitude, eps, inverse,
              **others):
-    """The checked arguments as a packed pamm_rotary_t; qo and ko are (tensor, layout)."""
+    """The GPU, and the checked arguments as a packed pamm_rotary_t; qo and ko are (tensor, layout)."""
     qh, (B, S, H, D) = _heads_tensor(where, "q" if k is not None else "x", q), q.shape
     kh = koh = (0, 0, 0, 0)
     Hk = 0
@@ -157,9 +157,12 @@ def _problem(where, q, k, qo, ko, q_weight, k_weight, inv_freq, positions, offse
         wq, wk = q_weight.data_ptr(), k_weight.data_ptr()
     rot, freq = _frequencies(where, inv_freq, D)
     *pos, off = _positions(where, positions, offset, B, S)
-    _on_gpu(where, q=q, k=k, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq, positions=positions,
-            offset=offset, **others)
-    return _pack_rotary(code, int(bool(interleaved)), int(bool(inverse)), pos[1], B, S, H, Hk, D, rot,
+    index = q.get_device()
+    for t in (q, k, q_weight, k_weight, inv_freq, positions, offset, *others.values()):
+        if t is not None and (index < 0 or t.get_device() != index):
+            _on_gpu(where, q=q, k=k, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq, positions=positions,
+                    offset=offset, **others)  # says which
+    return index, _pack_rotary(code, int(bool(interleaved)), int(bool(inverse)), pos[1], B, S, H, Hk, D, rot,
                         float(magnitude), float(eps), freq, pos[0], pos[2], pos[3], off, wq, wk, *qh, *kh, *qo[1], *koh)
 
 
@@ -188,9 +191,8 @@ def rotary(x, inv_freq, *, positions=None, offset=None, interleaved: bool = Fals
     if inv_freq is None:
         raise ValueError(f"{where}: inv_freq is needed")
     o = _like(where, "out", out, x)
-    p = _problem(where, x, None, o, None, None, None, inv_freq, positions, offset, interleaved, magnitude, 0.0, inverse,
+    index, p = _problem(where, x, None, o, None, None, None, inv_freq, positions, offset, interleaved, magnitude, 0.0, inverse,
                  out=o[0])
-    index = x.get_device()
     _launch("pamm_rotary", index, _lib().pamm_rotary, p, _stream_of(index))
     return o[0]
 
@@ -217,9 +219,8 @@ def qk_norm_rotary(q, k, q_weight, k_weight, inv_freq, *, positions=None, offset
     _heads_tensor(where, "k", k)
     _weights(where, q_weight, k_weight)
     qo, ko = _like(where, "q_out", q_out, q), _like(where, "k_out", k_out, k)
-    p = _problem(where, q, k, qo, ko, q_weight, k_weight, inv_freq, positions, offset, interleaved, magnitude, eps,
+    index, p = _problem(where, q, k, qo, ko, q_weight, k_weight, inv_freq, positions, offset, interleaved, magnitude, eps,
                  False, q_out=qo[0], k_out=ko[0])
-    index = q.get_device()
     _launch("pamm_rotary", index, _lib().pamm_rotary, p, _stream_of(index))
     return qo[0], ko[0]
 
@@ -261,12 +262,12 @@ def qk_norm_rotary_backward(dq, dk, q, k, q_weight, k_weight, inv_freq, *, posit
                              f"{t.dtype}")
         grads.append(_pack_heads(*layout))
     qo, ko = _like(where, "dq_out", dq_out, q), _like(where, "dk_out", dk_out, k)
-    p = _problem(where, q, k, qo, ko, q_weight, k_weight, inv_freq, positions, offset, interleaved, magnitude, eps,
+    index, p = _problem(where, q, k, qo, ko, q_weight, k_weight, inv_freq, positions, offset, interleaved, magnitude, eps,
                  False, dq=dq, dk=dk, dq_out=qo[0], dk_out=ko[0], workspace=workspace)
     _check_workspace(where, workspace)
     dw = torch.empty((2, q.shape[3]), dtype=torch.float32, device=q.device)
     dwq, dwk = dw.unbind(0)
-    lib, index = _lib(), q.get_device()
+    lib = _lib()
     ws, nbytes = _ws(lib.pamm_rotary_backward_workspace_size(p), q.device, workspace, where)
     _launch("pamm_rotary_backward", index, lib.pamm_rotary_backward, p, *grads, dwq.data_ptr(), dwk.data_ptr(), ws,
             nbytes, _stream_of(index))

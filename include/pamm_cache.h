@@ -66,7 +66,7 @@ size_t pamm_cache8_attention_workspace_size(const pamm_attention_t *a_host, cons
  * is the cache's room at most (keys past it are not read), kv_len the lengths
  * (NULL: seq_k).  Scores are formed of exact 8-bit values and scaled in 32 bits; bf16:
  * probabilities are multiplied by the values' scale before their one rounding.
- * Scales have to be finite.  What a mask hides does not come through, not even a NaN.
+ * Scales have to be positive, normal numbers.  What a mask hides does not come through, not even a NaN.
  * Errors as pamm_attention; _SHAPE, _DTYPE where the two do not fit each other.
  */
 int pamm_cache8_attention(const pamm_attention_t *a_host, const pamm_cache8_t *cache_host, void *ws, size_t ws_bytes,
