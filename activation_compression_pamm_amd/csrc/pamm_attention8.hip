@@ -40,6 +40,21 @@ __device__ __forceinline__ void widen16(const uint4& r, uint4* out, float power 
     }
 }
 
+// 16 8-bit floats as two vectors of fp16; exact.
+__device__ __forceinline__ void widen16_half(const uint4& r, uint4* out) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            u[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[2 * i + j], 1.0f, false));
+            u[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[2 * i + j], 1.0f, true));
+        }
+        out[i] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+}
+
 // Where 16-byte groups of 8-bit rows (2 ND of them, D / 16 in use) become
 // vectors of the type.
 template <int DT, int ND>
@@ -54,6 +69,12 @@ struct Wide {
         widen16<DT>(raw, v, power);
 #pragma unroll
         for (int i = 0; i < PER; ++i) *reinterpret_cast<uint4*>(tile + T::offset(r, PER * c + i)) = v[i];
+    }
+    __device__ static __forceinline__ void put_half(char* tile, int r, int c, const uint4& raw) {
+        uint4 v[2];
+        widen16_half(raw, v);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(tile + T::offset(r, 2 * c + i)) = v[i];
     }
 };
 
@@ -73,21 +94,38 @@ struct TileScales {
     }
 };
 
-// The values' scales of 64 tiles as many rows take them: 2^exponent times `power`, a power of two
-// that the values take on their way into LDS, exactly; the exponent, within 48 of 0, is added to
-// the probabilities' (one addition a tile instead of 16 multiplications), and `inverse` turns
-// their sum back into one of plain probabilities.
+// The values' scales of 64 tiles as many rows take them.  What is summed is in units of the
+// largest of these scales, `unit`, which changes with the 64 tiles, and a tile's scale is
+// unit * 2^exponent * power.  The exponent is added to its probabilities' (one addition a tile
+// instead of 16 multiplications, 4% of the time), and `inverse` turns their sum back into one of
+// plain probabilities.
+//
+// Tiles of at least 2^-10 units take their products in fp16, which holds the 8-bit values
+// exactly and the probabilities to 2^-12 instead of bf16's 2^-9 at the same rate; they are at most
+// 2^8.  Smaller ones, which would leave fp16's range, and the tail take them in bf16.  Scales
+// too far from the unit for fp32's probabilities leave `power` of two to the values, exactly.
 struct TileExponents {
     TileScales exponent, inverse, power;
+    float unit;
     __device__ __forceinline__ void load(const ScalesArg& s, int b, int h, int block, bool ok) {
         exponent.load(s, b, h, block, ok);
     }
-    __device__ __forceinline__ void arrived() {
-        const float v = exponent.v, near = v < 0x1p-40f ? v * 0x1p86f : v > 0x1p40f ? v * 0x1p-80f : v;
-        power.v = v < 0x1p-40f ? 0x1p-86f : v > 0x1p40f ? 0x1p80f : 1.0f;
+    // `eight`: this lane's tile is in 8 bits
+    __device__ __forceinline__ void arrived(bool eight) {
+        exponent.arrived();
+        float top = eight ? exponent.v : 0.0f;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, shfl_xor(top, m));
+        // the tail's scale is 1, and has to be near as well
+        unit = top == 0.0f ? 1.0f : fminf(fmaxf(top, 0x1p-40f), 0x1p40f);
+        unit = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(unit)));
+        const float v = exponent.v / unit, near = v < 0x1p-40f ? v * 0x1p86f : v > 0x1p40f ? v * 0x1p-80f : v;
+        power.v = v < 0x1p-40f ? 0x1p-86f : v > 0x1p40f ? 0x1p80f : eight && v >= 0x1p-10f && v <= 1.0f ? 0.0f : 1.0f;
         exponent.v = __builtin_amdgcn_logf(near);
         inverse.v = __builtin_amdgcn_rcpf(near);
     }
+    // The values' power of two, or 0: in fp16.
+    __device__ __forceinline__ float power_at(int i) const { return power.at(i); }
 };
 
 // The start of the tail.
@@ -120,6 +158,22 @@ __device__ __forceinline__ void softmax_update8(f32x16& s, float f, float expone
         sum += s[i];
     }
     st.l = fmaf(sum, inverse, st.l);
+}
+
+// acc += (32 rows of fp16 values, transposed) x probabilities, rounded to fp16.
+template <int ND>
+__device__ __forceinline__ void half_product(const char* tile, int base, const f32x16& s, f32x16* acc) {
+    typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+    f16x8 p[2];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i >> 3][i & 7] = (_Float16)s[i];
+    Columns<DT_BF16, ND> c;  // two bytes an element, whatever they hold
+    c.load(tile, 0, base);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int db = 0; db < ND; ++db)
+            acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, c.v[t][db]), p[t], acc[db], 0, 0, 0);
 }
 
 template <int DT, int ND>
@@ -172,35 +226,10 @@ __device__ __forceinline__ void attention8_rows(const AttnArgs& a, const Cache8A
 
     const char* kbase = a.k.p + b * a.k.sb + hk * a.k.sh;
     const char* vbase = a.v.p + b * a.v.sb + hk * a.v.sh;
-    uint4 kr, vr;
     TileScales ks, vs;     // fp32
     TileExponents ve;      // bf16
+    ve.unit = 1.0f;
     int base = t0;         // the tile of the first lane's scales
-    const int group_row = tid / W::GROUPS, group = tid % W::GROUPS;
-    const bool takes = (W::N >= 256 || tid < W::N) && group * 16 < a.D;
-    const int kat = takes ? group_row * (int)a.k.ss + group * 16 : kOutside;
-    const int vat = takes ? group_row * (int)a.v.ss + group * 16 : kOutside;
-    auto fetch = [&](int t) {
-        const int key0 = t * 32, some = t < t1 && key0 < whole ? 32 : 0;
-        kr = RowView(kbase + key0 * a.k.ss, (int)a.k.ss, some, 32, a.D).load(kat);
-        vr = RowView(vbase + key0 * a.v.ss, (int)a.v.ss, some, 32, a.D).load(vat);
-    };
-    auto put = [&](int t, int to) {
-        const int key0 = t * 32;
-        if (key0 < whole) {
-            if (W::N >= 256 || tid < W::N) {
-                W::put(lds[to][0], group_row, group, kr);
-                W::put(lds[to][1], group_row, group, vr, DT == DT_BF16 ? ve.power.at(t - base) : 1.0f);
-            }
-        } else {  // four tiles at most, which are waited for
-            const int at = key0 - whole;
-            TileCopy<DT, ND, 32, 256> copy;
-            copy.fetch(c8.kt.p + b * c8.kt.sb + hk * c8.kt.sh + at * c8.kt.ss, (int)c8.kt.ss, Lk - key0, a.D, tid);
-            copy.put(lds[to][0], tid);
-            copy.fetch(c8.vt.p + b * c8.vt.sb + hk * c8.vt.sh + at * c8.vt.ss, (int)c8.vt.ss, Lk - key0, a.D, tid);
-            copy.put(lds[to][1], tid);
-        }
-    };
     auto scales = [&](int t) {
         const int at = (t + l) * 32;
         ks.load(c8.ks, b, hk, at >> c8.block_log, at < whole);
@@ -210,50 +239,129 @@ __device__ __forceinline__ void attention8_rows(const AttnArgs& a, const Cache8A
             vs.load(c8.vs, b, hk, at >> c8.block_log, at < whole);
         base = t;
     };
-    auto scales_arrived = [&] {
+    auto scales_arrived = [&] {  // and what was summed is put into their unit
         ks.arrived();
-        if constexpr (DT == DT_BF16)
-            ve.arrived();
-        else
-            vs.arrived();
-    };
-    scales(t0);
-    fetch(t0);
-    scales_arrived();
-    if (t0 < t1) put(t0, 0);
-    __syncthreads();
-    int cur = 0;
-    for (int t = t0; t < t1; ++t, cur ^= 1) {
-        const bool more = t + 1 < t1;
-        fetch(t + 1);
-        const int rb = opaque(row_base<DT, ND>()), tb = opaque(trans_base<DT, ND>());
-        const int key0 = t * 32;
-        if (t + 1 - base > 63) {  // this tile's are used, and the next one's
-            scales(t);
-            scales_arrived();
-        }
-        if (key0 < wr.end && key0 + 32 > wr.begin) {
-            const bool part = key0 < wr.all_lo || key0 + 32 > wr.all_hi;
-            f32x16 s{};
+        if constexpr (DT == DT_BF16) {
+            const float before = ve.unit;
+            ve.arrived((base + l) * 32 < whole);
+            const float f = before / ve.unit;
 #pragma unroll
-            for (int i = 0; i < T::NS; ++i) s = mma_step<DT>(row_operand<DT, ND>(lds[cur][0], 0, rb, i), qf[i], s);
-            settle<DT>(s);
-            if (part) mask_block(s, key0, mine);
+            for (int db = 0; db < ND; ++db)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[db][i] *= f;
+        } else {
+            vs.arrived();
+        }
+    };
+    auto scores = [&](const char* keys, int key0, bool part) {
+        const int rb = opaque(row_base<DT, ND>());
+        f32x16 s{};
+#pragma unroll
+        for (int i = 0; i < T::NS; ++i) s = mma_step<DT>(row_operand<DT, ND>(keys, 0, rb, i), qf[i], s);
+        settle<DT>(s);
+        if (part) mask_block(s, key0, mine);
+        return s;
+    };
+
+    // the tiles in 8 bits; in bf16 those that fp16 can take, which are all but for scales very far apart
+    const int group_row = tid / W::GROUPS, group = tid % W::GROUPS;
+    const bool takes = (W::N >= 256 || tid < W::N) && group * 16 < a.D;
+    const int kat = takes ? group_row * (int)a.k.ss + group * 16 : kOutside;
+    const int vat = takes ? group_row * (int)a.v.ss + group * 16 : kOutside;
+    const int te = SAFE ? t0 : whole / 32 < t0 ? t0 : whole / 32 < t1 ? whole / 32 : t1;
+    bool left = SAFE;
+    uint4 kr, vr;
+    auto fetch = [&](int t) {
+        const int key0 = t * 32, some = t < te ? 32 : 0;
+        kr = RowView(kbase + key0 * a.k.ss, (int)a.k.ss, some, 32, a.D).load(kat);
+        vr = RowView(vbase + key0 * a.v.ss, (int)a.v.ss, some, 32, a.D).load(vat);
+    };
+    auto put = [&](int to) {
+        if (W::N < 256 && tid >= W::N) return;
+        W::put(lds[to][0], group_row, group, kr);
+        if constexpr (DT == DT_BF16)
+            W::put_half(lds[to][1], group_row, group, vr);
+        else
+            W::put(lds[to][1], group_row, group, vr);
+    };
+    if (t0 < te) {
+        scales(t0);
+        fetch(t0);
+        scales_arrived();
+        put(0);
+        __syncthreads();
+    }
+    int cur = 0;
+    for (int t = t0; t < te; ++t, cur ^= 1) {
+        fetch(t + 1);
+        const int key0 = t * 32;
+        const bool fits = DT == DT_F32 || ve.power_at(t - base) == 0.0f;
+        left |= !fits;
+        if (fits && key0 < wr.end && key0 + 32 > wr.begin) {
+            const bool part = key0 < wr.all_lo || key0 + 32 > wr.all_hi;
+            f32x16 s = scores(lds[cur][0], key0, part);
             const float f = c * ks.at(t - base);
+            const int tb = opaque(trans_base<DT, ND>());
             if constexpr (DT == DT_BF16) {
                 softmax_update8<ND>(s, f, ve.exponent.at(t - base), ve.inverse.at(t - base), st, acc);
+                half_product<ND>(lds[cur][1], tb, s, acc);
             } else {  // whose precision the exponent's rounding would reach
                 softmax_update<ND>(s, f, st, acc);
                 const float vscale = vs.at(t - base);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[i] *= vscale;
+                Packed<DT> p;
+                p.set(s);
+                trans_product<DT, ND, true, false>(lds[cur][1], 0, tb, p, part, key0, mine, acc);
             }
-            Packed<DT> p;
-            p.set(s);
-            trans_product<DT, ND, true, SAFE>(lds[cur][1], 0, tb, p, part, key0, mine, acc);
         }
-        if (more) put(t + 1, cur ^ 1);
+        if (t + 1 < te) {
+            if (t + 1 - base > 63) {
+                scales(t + 1);
+                scales_arrived();
+            }
+            put(cur ^ 1);
+        }
         __syncthreads();
+    }
+
+    // the tail, and what was left: one tile at a time, bf16 products in bf16
+    for (int t = left ? t0 : te, first = 1; t < t1; ++t, first = 0) {
+        const int in = (t - t0) & 63, key0 = t * 32;
+        if (first || in == 0) {
+            scales(t - in);
+            scales_arrived();
+        }
+        const bool eight = key0 < whole;
+        const float power = DT == DT_BF16 ? ve.power_at(t - base) : 1.0f;
+        if (!SAFE && eight && (DT == DT_F32 || power == 0.0f)) continue;
+        __syncthreads();
+        if (eight) {
+            if (W::N >= 256 || tid < W::N) {
+                const uint4 k = RowView(kbase + key0 * a.k.ss, (int)a.k.ss, 32, 32, a.D).load(kat);
+                const uint4 v = RowView(vbase + key0 * a.v.ss, (int)a.v.ss, 32, 32, a.D).load(vat);
+                W::put(lds[0][0], group_row, group, k);
+                W::put(lds[0][1], group_row, group, v, power == 0.0f ? 1.0f : power);
+            }
+        } else {
+            const int at = key0 - whole;
+            TileCopy<DT, ND, 32, 256> copy;
+            copy.fetch(c8.kt.p + b * c8.kt.sb + hk * c8.kt.sh + at * c8.kt.ss, (int)c8.kt.ss, Lk - key0, a.D, tid);
+            copy.put(lds[0][0], tid);
+            copy.fetch(c8.vt.p + b * c8.vt.sb + hk * c8.vt.sh + at * c8.vt.ss, (int)c8.vt.ss, Lk - key0, a.D, tid);
+            copy.put(lds[0][1], tid);
+        }
+        __syncthreads();
+        if (key0 >= wr.end || key0 + 32 <= wr.begin) continue;
+        const bool part = key0 < wr.all_lo || key0 + 32 > wr.all_hi;
+        f32x16 s = scores(lds[0][0], key0, part);
+        softmax_update<ND>(s, c * ks.at(t - base), st, acc);
+        const float vscale = DT == DT_BF16 ? __builtin_amdgcn_exp2f(ve.exponent.at(t - base)) : vs.at(t - base);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] *= vscale;
+        Packed<DT> p;
+        p.set(s);
+        trans_product<DT, ND, true, SAFE>(lds[0][1], 0, opaque(trans_base<DT, ND>()), p, part, key0, mine, acc);
     }
 
 #pragma unroll
@@ -261,7 +369,7 @@ __device__ __forceinline__ void attention8_rows(const AttnArgs& a, const Cache8A
     const bool marked = !SAFE && a.hides && !sums_finite<ND>(acc);
     if (!live) return;
     const float sum = half_sum(st.l);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float inv = sum == 0.0f ? 0.0f : (DT == DT_BF16 ? ve.unit : 1.0f) / sum;
     float lse2 = sum == 0.0f ? -INFINITY : st.m + __builtin_amdgcn_logf(sum);
     if (marked) lse2 = NAN;
     const int64_t at = ((int64_t)b * a.H + head) * a.Sq + pos;
@@ -275,7 +383,7 @@ __device__ __forceinline__ void attention8_rows(const AttnArgs& a, const Cache8A
 }
 
 template <int DT, int ND>
-__global__ __launch_bounds__(256, DT == DT_BF16 ? 3 : 1) void attention8_kernel(AttnArgs a, Cache8Args c, int row_tiles) {
+__global__ __launch_bounds__(256, DT == DT_BF16 ? (ND <= 2 ? 4 : 3) : 1) void attention8_kernel(AttnArgs a, Cache8Args c, int row_tiles) {
     __shared__ __attribute__((aligned(16))) Rows8Shared<DT, ND> shared;
     attention8_rows<DT, ND, false>(a, c, blockIdx.x, row_tiles, shared);
 }
@@ -351,11 +459,18 @@ __device__ __forceinline__ void attention8_few(const AttnArgs& a, const Cache8Ar
         const bool part = key0 < br.all_lo || key0 + 32 > br.all_hi;
         if (part) mask_block(s, key0, mine);
         softmax_update<ND>(s, c * ks, st, acc);
+        Packed<DT> p;
+        f32x16 rest;
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[i] *= vs;
-        Packed<DT> p;
         p.set(s);
         trans_product<DT, ND, true, SAFE>(vt, 0, opaque(trans_base<DT, ND>()), p, part, key0, mine, acc);
+        if constexpr (DT == DT_BF16) {  // what bf16 left of them: the matrix unit is idle otherwise
+#pragma unroll
+            for (int i = 0; i < 16; ++i) rest[i] = s[i] - (float)p.v[i >> 3][i & 7];
+            p.set(rest);
+            trans_product<DT, ND, true, SAFE>(vt, 0, opaque(trans_base<DT, ND>()), p, part, key0, mine, acc);
+        }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
 
@@ -663,10 +778,11 @@ __device__ __forceinline__ void attention8_one(const AttnArgs& a, const Cache8Ar
     // 4 (l / 16) + i, 16 more for i >= 4, for both operands.
     auto product = [&](int db, const auto& x, const float (&p)[8]) {
         if constexpr (DT == DT_BF16) {
-            bf16x8 pk;
+            bf16x8 pk, rest;  // what bf16 leaves of the probabilities, too: the matrix unit is idle otherwise
 #pragma unroll
-            for (int i = 0; i < 8; ++i) pk[i] = (__bf16)p[i];
+            for (int i = 0; i < 8; ++i) pk[i] = (__bf16)p[i], rest[i] = (__bf16)(p[i] - (float)pk[i]);
             acc[db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, pk, acc[db], 0, 0, 0);
+            acc[db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, rest, acc[db], 0, 0, 0);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[db] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], p[i], acc[db], 0, 0, 0);

@@ -172,9 +172,17 @@ struct Row {
     }
 };
 
-// Sum over the lanes of a row, the same in each.
-__device__ __forceinline__ float lanes_sum(float v, int lanes) {
-    for (int m = 1; m < lanes; m <<= 1) v += shfl_xor(v, m);
+// Sum over the lanes of a row (up to 16), the same in each: with the neighbour,
+// the neighbouring pair, four and eight.
+template <int CTRL>
+__device__ __forceinline__ float with_lane(float v) {
+    return v + __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float lanes_sum(float v, int lanes_log) {
+    if (lanes_log > 0) v = with_lane<0xb1>(v);   // lanes 1, 0, 3, 2 of each four
+    if (lanes_log > 1) v = with_lane<0x4e>(v);   // 2, 3, 0, 1
+    if (lanes_log > 2) v = with_lane<0x141>(v);  // 7, 6, ... of each eight: the other four
+    if (lanes_log > 3) v = with_lane<0x140>(v);  // 15, 14, ... of each sixteen: the other eight
     return v;
 }
 
@@ -204,7 +212,7 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a) {
     __shared__ float2 table[kTablePairs];
     __shared__ float exchange[PAIRS == PAIRS_FAR ? kThreads * 2 * P : 1];
     Row<DT, PAIRS> row(a);
-    const int lanes = 1 << a.lanes_log, heads = a.Hq + a.Hk;
+    const int heads = a.Hq + a.Hk;
     float wq[NORM ? 2 * P : 1], wk[NORM ? 2 * P : 1];
     if constexpr (NORM) {
         row.load(a.wq, wq);
@@ -231,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a) {
                 float ss = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 2 * P; ++i) ss = fmaf(x[i], x[i], ss);
-                const float rstd = 1.0f / sqrtf(lanes_sum(ss, lanes) / (float)a.D + a.eps);
+                const float rstd = 1.0f / sqrtf(lanes_sum(ss, a.lanes_log) / (float)a.D + a.eps);
 #pragma unroll
                 for (int i = 0; i < 2 * P; ++i) x[i] = x[i] * rstd * (second ? wk[i] : wq[i]);
             }
@@ -242,95 +250,89 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a) {
     }
 }
 
+// The first `blocks_q` workgroups take the queries' heads, the others the keys':
+// one weight's sums a thread, which leaves three waves a SIMD instead of two.
 template <int DT, int PAIRS>
 __global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a) {
     constexpr int P = Elem<DT>::per16;
     __shared__ float2 table[kTablePairs];
     __shared__ float exchange[PAIRS == PAIRS_FAR ? kThreads * 2 * P : 1];
-    __shared__ float sums[kThreads / 64][2][kMaxHeadDim];
+    __shared__ float sums[kThreads / 64][kMaxHeadDim];
     Row<DT, PAIRS> row(a);
-    const int lanes = 1 << a.lanes_log;
-    float dw[2][2 * P];
+    const bool keys = (int)blockIdx.x >= a.blocks_q;
+    const int lanes = 1 << a.lanes_log, heads = keys ? a.Hk : a.Hq, block = blockIdx.x - (keys ? a.blocks_q : 0);
+    const HeadsArg x_in = keys ? a.k : a.q, g_in = keys ? a.dk : a.dq, out = keys ? a.ko : a.qo;
+    float dw[2 * P], wt[2 * P];
+    row.load(keys ? a.wk : a.wq, wt);
 #pragma unroll
-    for (int i = 0; i < 2 * P; ++i) dw[0][i] = dw[1][i] = 0.0f;
-    const int64_t step = (int64_t)gridDim.x << a.tokens_log;
-    for (int64_t first = (int64_t)blockIdx.x << a.tokens_log; first < a.tokens; first += step) {
+    for (int i = 0; i < 2 * P; ++i) dw[i] = 0.0f;
+    const int64_t step = (int64_t)(keys ? gridDim.x - a.blocks_q : a.blocks_q) << a.tokens_log;
+    for (int64_t first = (int64_t)block << a.tokens_log; first < a.tokens; first += step) {
         fill_table(a, first, table);
         __syncthreads();
         const Share w(a, first);
         row.angles(a, table + w.tk * a.R2, -1.0f);
+        for (int h0 = 0; h0 < heads; h0 += w.step) {
+            const int h = h0 + w.head;
+            const bool live = w.live && h < heads;
+            float x[2 * P], g[2 * P];
+            if (live) {
+                row.load(head_row(x_in, w, h), x);
+                row.load(head_row(g_in, w, h), g);
+            } else {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int heads = t ? a.Hk : a.Hq;
-            if (heads == 0) continue;
-            float wt[2 * P];
-            row.load(t ? a.wk : a.wq, wt);
-            for (int h0 = 0; h0 < heads; h0 += w.step) {
-                const int h = h0 + w.head;
-                const bool live = w.live && h < heads;
-                float x[2 * P], g[2 * P];
-                if (live) {
-                    row.load(head_row(t ? a.k : a.q, w, h), x);
-                    row.load(head_row(t ? a.dk : a.dq, w, h), g);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2 * P; ++i) x[i] = g[i] = 0.0f;
-                }
-                row.rotate(a, g, exchange);
-                float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 2 * P; ++i) {
-                    ss = fmaf(x[i], x[i], ss);
-                    dot = fmaf(g[i] * wt[i], x[i], dot);
-                }
-                ss = lanes_sum(ss, lanes), dot = lanes_sum(dot, lanes);
-                const float rstd = 1.0f / sqrtf(ss / (float)a.D + a.eps), mean = dot * rstd / (float)a.D;
-#pragma unroll
-                for (int i = 0; i < 2 * P; ++i) {
-                    const float xhat = x[i] * rstd;
-                    if (live) dw[t][i] = fmaf(g[i], xhat, dw[t][i]);
-                    x[i] = rstd * fmaf(-xhat, mean, g[i] * wt[i]);
-                }
-                if (live) row.store(head_row(t ? a.ko : a.qo, w, h), x);
+                for (int i = 0; i < 2 * P; ++i) x[i] = g[i] = 0.0f;
             }
+            row.rotate(a, g, exchange);
+            float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2 * P; ++i) {
+                ss = fmaf(x[i], x[i], ss);
+                dot = fmaf(g[i] * wt[i], x[i], dot);
+            }
+            ss = lanes_sum(ss, a.lanes_log), dot = lanes_sum(dot, a.lanes_log);
+            const float rstd = 1.0f / sqrtf(ss / (float)a.D + a.eps), mean = dot * rstd / (float)a.D;
+#pragma unroll
+            for (int i = 0; i < 2 * P; ++i) {
+                const float xhat = x[i] * rstd;
+                if (live) dw[i] = fmaf(g[i], xhat, dw[i]);
+                x[i] = rstd * fmaf(-xhat, mean, g[i] * wt[i]);
+            }
+            if (live) row.store(head_row(out, w, h), x);
         }
         __syncthreads();
     }
-    // the weights' gradients of this workgroup: over the wave's rows by a fixed
-    // tree, then over the waves in order
+    // the weight's gradient of this workgroup: over the wave's rows by a fixed tree, then over the waves in order
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 2 * P; ++i) {
-            float v = dw[t][i];
-            for (int m = lanes; m < 64; m <<= 1) v += shfl_xor(v, m);
-            if ((threadIdx.x & 63) < lanes && row.at[i / P] >= 0)
-                sums[threadIdx.x >> 6][t][row.at[i / P] * P + i % P] = v;
-        }
+    for (int i = 0; i < 2 * P; ++i) {
+        float v = dw[i];
+        for (int m = lanes; m < 64; m <<= 1) v += shfl_xor(v, m);
+        if ((threadIdx.x & 63) < lanes && row.at[i / P] >= 0) sums[threadIdx.x >> 6][row.at[i / P] * P + i % P] = v;
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.D; i += kThreads) {
-        const int t = i / a.D, e = i - t * a.D;
-        float v = sums[0][t][e];
+    for (int e = threadIdx.x; e < a.D; e += kThreads) {
+        float v = sums[0][e];
 #pragma unroll
-        for (int k = 1; k < kThreads / 64; ++k) v += sums[k][t][e];
-        a.part[(int64_t)blockIdx.x * 2 * a.D + i] = v;
+        for (int k = 1; k < kThreads / 64; ++k) v += sums[k][e];
+        a.part[(int64_t)blockIdx.x * a.D + e] = v;
     }
 }
 
 // The weights' gradients: 64 lanes of 16 columns each take every 64th of the
-// `blocks` partial rows, then add up in order.
-__global__ __launch_bounds__(1024) void rotary_dw_kernel(const float* part, int blocks, int D, float* dwq, float* dwk) {
+// partial rows of their weight, then add up in order.
+__global__ __launch_bounds__(1024) void rotary_dw_kernel(RotaryArgs a, int blocks) {
     __shared__ float sums[64][17];
     const int c = threadIdx.x & 15, g = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
+    const bool keys = blockIdx.y != 0;
+    const int from = keys ? a.blocks_q : 0, to = keys ? blocks : a.blocks_q;
     float s = 0.0f;
-    if (col < 2 * D)
-        for (int b = g; b < blocks; b += 64) s += part[(int64_t)b * 2 * D + col];
+    if (col < a.D)
+        for (int b = from + g; b < to; b += 64) s += a.part[(int64_t)b * a.D + col];
     sums[g][c] = s;
     __syncthreads();
-    if (g == 0 && col < 2 * D) {
+    if (g == 0 && col < a.D) {
         for (int i = 1; i < 64; ++i) s += sums[i][c];
-        float* to = col < D ? dwq + col : dwk ? dwk + (col - D) : nullptr;
-        if (to) *to = s;
+        (keys ? a.dwk : a.dwq)[col] = s;
     }
 }
 
@@ -374,13 +376,18 @@ hipError_t run_rotary(const RotaryArgs& a, int dtype, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Each workgroup leaves a row of partial sums for each weight: four a unit,
-// looping over their tokens.
-int rotary_backward_blocks(const RotaryArgs& a) {
-    return a.tokens == 0 ? 0 : (int)std::min<int64_t>(token_groups(a), 4 * a.num_cus);
+// Each workgroup leaves a row of partial sums of its weight: four a unit, looping
+// over their tokens, dealt to queries and keys as they have heads.
+int rotary_backward_blocks(RotaryArgs& a) {
+    if (a.tokens == 0) return a.blocks_q = 0;
+    const int64_t groups = token_groups(a), most = 4 * a.num_cus;
+    if (a.Hk == 0) return a.blocks_q = (int)std::min(groups, most);
+    const int64_t keys = std::min(groups, std::max<int64_t>(1, most * a.Hk / (a.Hq + a.Hk)));
+    a.blocks_q = (int)std::min(groups, std::max<int64_t>(1, most - keys));
+    return a.blocks_q + (int)keys;
 }
 
-hipError_t run_rotary_backward(const RotaryArgs& a, int dtype, hipStream_t st) {
+hipError_t run_rotary_backward(RotaryArgs a, int dtype, hipStream_t st) {
     const int blocks = rotary_backward_blocks(a), pairs = pairs_of(a, dtype);
     if (blocks > 0) {
 #define PAMM_CASE(DT, PAIRS)                                                                                    \
@@ -389,8 +396,7 @@ hipError_t run_rotary_backward(const RotaryArgs& a, int dtype, hipStream_t st) {
         PAMM_CASES
 #undef PAMM_CASE
     }
-    hipLaunchKernelGGL(rotary_dw_kernel, dim3((2 * a.D + 15) / 16), dim3(1024), 0, st, a.part, blocks, a.D, a.dwq,
-                       a.dwk);
+    hipLaunchKernelGGL(rotary_dw_kernel, dim3((a.D + 15) / 16, a.Hk > 0 ? 2 : 1), dim3(1024), 0, st, a, blocks);
     return hipGetLastError();
 }
 #undef PAMM_CASES

@@ -107,8 +107,8 @@ int pamm_rotary(const pamm_rotary_t* a, void* stream) {
 
 size_t pamm_rotary_backward_workspace_size(const pamm_rotary_t* a) {
     if (rotary_sizes(a) != PAMM_OK) return 0;
-    const pamm::RotaryArgs r = sizes_arg(a);
-    return up256((size_t)pamm::rotary_backward_blocks(r) * 2 * (size_t)r.D * sizeof(float));
+    pamm::RotaryArgs r = sizes_arg(a);
+    return up256((size_t)pamm::rotary_backward_blocks(r) * (size_t)r.D * sizeof(float));
 }
 
 int pamm_rotary_backward(const pamm_rotary_t* a, const pamm_heads_t* dq, const pamm_heads_t* dk, float* dwq,

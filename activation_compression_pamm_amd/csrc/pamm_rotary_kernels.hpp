@@ -12,7 +12,7 @@ struct RotaryArgs {
     int64_t psb, pss;        // elements
     const int32_t* offset;
     const char *wq, *wk;
-    float* part;             // [blocks][2][D]: partial sums of the weights' gradients
+    float* part;             // [blocks][D]: partial sums of the weights' gradients, queries' blocks first
     float *dwq, *dwk;
     int64_t tokens;          // batch * seq
     int S, Hq, Hk, D, R2;    // R2: rotated pairs of a row
@@ -20,12 +20,14 @@ struct RotaryArgs {
     float magnitude, eps;
     int lanes_log, tokens_log;  // lanes a row, tokens a workgroup at a time
     int num_cus;
+    int blocks_q;            // backward: workgroups that take the queries
 };
 
 // Fills in how the work is cut.
 void rotary_shape(RotaryArgs& a, int dtype);
-int rotary_backward_blocks(const RotaryArgs& a);
+// Workgroups of the backward pass; fills in those for the queries.
+int rotary_backward_blocks(RotaryArgs& a);
 hipError_t run_rotary(const RotaryArgs& a, int dtype, hipStream_t st);
-hipError_t run_rotary_backward(const RotaryArgs& a, int dtype, hipStream_t st);
+hipError_t run_rotary_backward(RotaryArgs a, int dtype, hipStream_t st);
 
 }  // namespace pamm

@@ -354,6 +354,42 @@ def test_what_lies_behind_the_length_is_never_seen(dtype, Sq):
     assert torch.isfinite(o).all()
 
 
+@BOTH
+@pytest.mark.parametrize("Sq,H,Hkv", [(1, 4, 2), (1, 20, 1), (40, 2, 1), (200, 2, 1)])
+@pytest.mark.parametrize("window", [0, 20])
+def test_scales_far_apart(dtype, Sq, H, Hkv, window):
+    """Values of neighbouring blocks up to 2^150 apart, blocks of zeros among them: the window leaves some queries
+    nothing but small ones, whose results have to be as exact as the others'."""
+    block, n = 32, 24
+    rng = np.random.default_rng(5)
+    powers = rng.permutation([0, -3, -9, -11, -14, -24, -26, -45, -60, -90, 20, 50, 60, 5, 0, -1, -100, 30, -50, 1, 0, 0, 2, -7])
+    L = block * n + 7
+    ks = [values(rng, (L, Hkv, 32), dtype)]
+    vs = [values(rng, (L, Hkv, 32), dtype)]
+    for i, p in enumerate(powers):
+        vs[0][i * block:(i + 1) * block] *= 2.0 ** p
+    vs[0][3 * block:4 * block] = 0
+    ks, vs = rounded(ks, dtype), rounded(vs, dtype)
+    c, at = filled(1, L, Hkv, 32, block, dtype), lens([0])
+    pamm.cache_append_fp8(c, dev(ks[0][None], dtype), dev(vs[0][None], dtype), at)
+    k, v = meant(c, [L], L)
+    for end in (L, L - 7, 5 * block, 11 * block + 3):
+        say("scales", dtype, Sq, H, window, end)
+        n_q = min(Sq, end)
+        q = values(np.random.default_rng(6), (1, n_q, H, 32), dtype)
+        whole = end // block * block
+        kk, vv = k.copy(), v.copy()
+        if end < L:  # the tail is that of the whole cache: put the block's tokens there
+            for x, t in ((kk, c.k_tail), (vv, c.v_tail)):
+                x[0, whole:end] = host(t.float())[0, :end - whole]
+        ref = bo.attention(q, kk, vv, dtype=dtype, causal=True, window=window, kv_len=[end])
+        o, lse = pamm.attention_fp8(dev(q, dtype), c, lens([end]), causal=True, window=window)
+        # one more product for each probability: 4 u of a row's sum of P |v|, which the bound's P part holds 2^-8
+        # or E >= 16 u of
+        close("o", o, ref["o"], 1.5 * ref["o_tol"])
+        close("lse", lse, ref["lse"], ref["lse_tol"])
+
+
 def test_far_rows():
     """Byte offsets past 2^32: two sequences of 8-bit rows more than that apart, and a long one."""
     big = torch.empty((1 << 32) + (1 << 20), dtype=torch.uint8, device="cuda")
