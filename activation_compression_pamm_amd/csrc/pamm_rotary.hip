@@ -128,6 +128,15 @@ struct Row {
             unpack16<DT>(v, x + i * P);
         }
     }
+    // The same without unpacking, from a row that can be read in any case.
+    __device__ __forceinline__ void fetch(const char* row, uint4 (&v)[2]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[i] = *reinterpret_cast<const uint4*>(row + (at[i] >= 0 ? at[i] * 16 : 0));
+    }
+    __device__ __forceinline__ void unpack(const uint4 (&v)[2], float* x) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) unpack16<DT>(at[i] >= 0 ? v[i] : make_uint4(0, 0, 0, 0), x + i * P);
+    }
     __device__ __forceinline__ void store(char* row, const float* x) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -250,10 +259,13 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a) {
     }
 }
 
+// Workgroups a unit, all of which are resident: 168 registers a thread, 128 in fp32.
+template <int DT> constexpr int kBackwardGroups = DT == DT_BF16 ? 3 : 4;
+
 // The first `blocks_q` workgroups take the queries' heads, the others the keys':
 // one weight's sums a thread, which leaves three waves a SIMD instead of two.
 template <int DT, int PAIRS>
-__global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a) {
+__global__ __launch_bounds__(kThreads, kBackwardGroups<DT>) void rotary_backward_kernel(RotaryArgs a) {
     constexpr int P = Elem<DT>::per16;
     __shared__ float2 table[kTablePairs];
     __shared__ float exchange[PAIRS == PAIRS_FAR ? kThreads * 2 * P : 1];
@@ -267,22 +279,28 @@ __global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a)
 #pragma unroll
     for (int i = 0; i < 2 * P; ++i) dw[i] = 0.0f;
     const int64_t step = (int64_t)(keys ? gridDim.x - a.blocks_q : a.blocks_q) << a.tokens_log;
+    // the next row's loads are under way while a row is worked on, also from one
+    // group of tokens to the next; lanes without a row read the first one
+    uint4 nx[2], ng[2];
+    auto fetch = [&](const Share& w, int h) {
+        const bool live = w.live && h < heads;
+        row.fetch(live ? head_row(x_in, w, h) : x_in.p, nx);
+        row.fetch(live ? head_row(g_in, w, h) : g_in.p, ng);
+    };
+    Share w(a, (int64_t)block << a.tokens_log);
+    fetch(w, w.head);
     for (int64_t first = (int64_t)block << a.tokens_log; first < a.tokens; first += step) {
         fill_table(a, first, table);
         __syncthreads();
-        const Share w(a, first);
         row.angles(a, table + w.tk * a.R2, -1.0f);
-        for (int h0 = 0; h0 < heads; h0 += w.step) {
-            const int h = h0 + w.head;
+        for (int h = w.head, h0 = 0; h0 < heads; h0 += w.step, h += w.step) {
+            const Share now = w;
             const bool live = w.live && h < heads;
             float x[2 * P], g[2 * P];
-            if (live) {
-                row.load(head_row(x_in, w, h), x);
-                row.load(head_row(g_in, w, h), g);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2 * P; ++i) x[i] = g[i] = 0.0f;
-            }
+            row.unpack(nx, x);
+            row.unpack(ng, g);
+            if (h0 + w.step >= heads) w = Share(a, first + step);
+            fetch(w, h0 + w.step >= heads ? w.head : h + w.step);
             row.rotate(a, g, exchange);
             float ss = 0.0f, dot = 0.0f;
 #pragma unroll
@@ -298,7 +316,7 @@ __global__ __launch_bounds__(kThreads) void rotary_backward_kernel(RotaryArgs a)
                 if (live) dw[i] = fmaf(g[i], xhat, dw[i]);
                 x[i] = rstd * fmaf(-xhat, mean, g[i] * wt[i]);
             }
-            if (live) row.store(head_row(out, w, h), x);
+            if (live) row.store(head_row(out, now, h), x);
         }
         __syncthreads();
     }
@@ -347,15 +365,16 @@ int64_t token_groups(const RotaryArgs& a) { return ((a.tokens - 1) >> a.tokens_l
 // A row's vectors two a lane.  Tokens a workgroup: as many as leave each token
 // enough groups of lanes for its heads in about four rounds (the angles are
 // formed once a token, and a lane's share of them is fetched once), but no
-// fewer workgroups than two a unit, and no more angles than the table holds.
-void rotary_shape(RotaryArgs& a, int dtype) {
+// fewer workgroups than two a unit, and no more angles than the table holds.  In the
+// backward pass, whose workgroups stay, no fewer groups of tokens than eight a unit.
+void rotary_shape(RotaryArgs& a, int dtype, bool backward) {
     const int nv = a.D / (dtype == DT_BF16 ? 8 : 4), need = (nv + 1) / 2;
     a.lanes_log = 0;
     while ((1 << a.lanes_log) < need) ++a.lanes_log;
     const int groups = kThreads >> a.lanes_log, heads = a.Hq + a.Hk;
     a.tokens_log = 0;
     while ((2 << a.tokens_log) <= groups && (a.R2 << (a.tokens_log + 1)) <= kTablePairs &&
-           (groups >> a.tokens_log) * 4 > heads && (a.tokens >> (a.tokens_log + 1)) >= 2 * a.num_cus)
+           (groups >> a.tokens_log) * 4 > heads && (a.tokens >> (a.tokens_log + 1)) >= (backward ? 8 : 2) * a.num_cus)
         ++a.tokens_log;
 }
 
@@ -376,11 +395,12 @@ hipError_t run_rotary(const RotaryArgs& a, int dtype, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Each workgroup leaves a row of partial sums of its weight: four a unit, looping
-// over their tokens, dealt to queries and keys as they have heads.
-int rotary_backward_blocks(RotaryArgs& a) {
+// Each workgroup leaves a row of partial sums of its weight: as many as are
+// resident, looping over their tokens, dealt to queries and keys as they have heads.
+int rotary_backward_blocks(RotaryArgs& a, int dtype) {
     if (a.tokens == 0) return a.blocks_q = 0;
-    const int64_t groups = token_groups(a), most = 4 * a.num_cus;
+    const int64_t groups = token_groups(a);
+    const int64_t most = (int64_t)a.num_cus * (dtype == DT_BF16 ? kBackwardGroups<DT_BF16> : kBackwardGroups<DT_F32>);
     if (a.Hk == 0) return a.blocks_q = (int)std::min(groups, most);
     const int64_t keys = std::min(groups, std::max<int64_t>(1, most * a.Hk / (a.Hq + a.Hk)));
     a.blocks_q = (int)std::min(groups, std::max<int64_t>(1, most - keys));
@@ -388,7 +408,7 @@ int rotary_backward_blocks(RotaryArgs& a) {
 }
 
 hipError_t run_rotary_backward(RotaryArgs a, int dtype, hipStream_t st) {
-    const int blocks = rotary_backward_blocks(a), pairs = pairs_of(a, dtype);
+    const int blocks = rotary_backward_blocks(a, dtype), pairs = pairs_of(a, dtype);
     if (blocks > 0) {
 #define PAMM_CASE(DT, PAIRS)                                                                                    \
     if (dtype == DT && pairs == PAIRS)                                                                          \

@@ -58,7 +58,7 @@ pamm::HeadsArg heads_arg(const pamm_rotary_t* a, const pamm_heads_t& t, int64_t 
 }
 
 // What the workspace's size goes by: sizes alone.
-pamm::RotaryArgs sizes_arg(const pamm_rotary_t* a) {
+pamm::RotaryArgs sizes_arg(const pamm_rotary_t* a, bool backward) {
     pamm::RotaryArgs r;
     memset(&r, 0, sizeof r);
     r.tokens = a->batch * a->seq;
@@ -68,12 +68,12 @@ pamm::RotaryArgs sizes_arg(const pamm_rotary_t* a) {
     r.D = (int)a->head_dim;
     r.R2 = (int)(a->rot_dim / 2);
     r.num_cus = num_cus();
-    pamm::rotary_shape(r, a->dtype);
+    pamm::rotary_shape(r, a->dtype, backward);
     return r;
 }
 
-pamm::RotaryArgs rotary_args(const pamm_rotary_t* a) {
-    pamm::RotaryArgs r = sizes_arg(a);
+pamm::RotaryArgs rotary_args(const pamm_rotary_t* a, bool backward) {
+    pamm::RotaryArgs r = sizes_arg(a, backward);
     r.q = heads_arg(a, a->q, a->heads_q);
     r.qo = heads_arg(a, a->q_out, a->heads_q);
     if (a->heads_k > 0) {
@@ -102,13 +102,13 @@ extern "C" {
 int pamm_rotary(const pamm_rotary_t* a, void* stream) {
     if (int e = rotary_check(a)) return e;
     if (a->batch == 0 || a->seq == 0) return PAMM_OK;
-    return status(pamm::run_rotary(rotary_args(a), a->dtype, reinterpret_cast<hipStream_t>(stream)));
+    return status(pamm::run_rotary(rotary_args(a, false), a->dtype, reinterpret_cast<hipStream_t>(stream)));
 }
 
 size_t pamm_rotary_backward_workspace_size(const pamm_rotary_t* a) {
     if (rotary_sizes(a) != PAMM_OK) return 0;
-    pamm::RotaryArgs r = sizes_arg(a);
-    return up256((size_t)pamm::rotary_backward_blocks(r) * (size_t)r.D * sizeof(float));
+    pamm::RotaryArgs r = sizes_arg(a, true);
+    return up256((size_t)pamm::rotary_backward_blocks(r, a->dtype) * (size_t)r.D * sizeof(float));
 }
 
 int pamm_rotary_backward(const pamm_rotary_t* a, const pamm_heads_t* dq, const pamm_heads_t* dk, float* dwq,
@@ -118,7 +118,7 @@ int pamm_rotary_backward(const pamm_rotary_t* a, const pamm_heads_t* dq, const p
     if (int e = both_check(a, *dq, a->heads_k > 0 ? *dk : *dq)) return e;
     if (!aligned(dwq, 4) || !aligned(dwk, 4)) return PAMM_ERR_ALIGN;
     if (int e = ws_check(ws, ws_bytes, pamm_rotary_backward_workspace_size(a))) return e;
-    pamm::RotaryArgs r = rotary_args(a);
+    pamm::RotaryArgs r = rotary_args(a, true);
     r.dq = heads_arg(a, *dq, a->heads_q);
     if (a->heads_k > 0) r.dk = heads_arg(a, *dk, a->heads_k);
     r.part = reinterpret_cast<float*>(ws);

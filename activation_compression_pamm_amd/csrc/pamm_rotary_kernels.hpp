@@ -24,9 +24,9 @@ struct RotaryArgs {
 };
 
 // Fills in how the work is cut.
-void rotary_shape(RotaryArgs& a, int dtype);
+void rotary_shape(RotaryArgs& a, int dtype, bool backward);
 // Workgroups of the backward pass; fills in those for the queries.
-int rotary_backward_blocks(RotaryArgs& a);
+int rotary_backward_blocks(RotaryArgs& a, int dtype);
 hipError_t run_rotary(const RotaryArgs& a, int dtype, hipStream_t st);
 hipError_t run_rotary_backward(RotaryArgs a, int dtype, hipStream_t st);
 
