@@ -7,10 +7,10 @@
 //
 // Bound by memory: a head row is read once, held by `lanes` neighbouring lanes
 // (two 16-byte vectors each, in the half layout the two that are rotated with
-// each other) and written once.  The angles are the same for all heads of a
-// token: a workgroup forms its tokens' cosines and sines once, one pair a
-// thread, into LDS, and each lane keeps those of its elements while it goes
-// over the token's heads.
+// each other) and written once.  A workgroup takes the heads of some tokens of
+// one of the two tensors, row after row over all of them, with the next row's
+// loads under way; the angles, the same for all heads of a token, it forms once,
+// a pair a thread, into LDS, with where each token's rows lie.
 #include <algorithm>
 
 #include "pamm_device.hpp"
@@ -21,7 +21,7 @@ namespace pamm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTablePairs = 1024;
+constexpr int kTablePairs = 2048, kTokens = 64;  // of a workgroup at a time
 constexpr int kMaxHeadDim = 128;
 
 enum : int { PAIRS_INTER = 0, PAIRS_HALF = 1, PAIRS_FAR = 2 };  // FAR: half, R2 not a whole number of vectors
@@ -49,10 +49,10 @@ __device__ __forceinline__ float2 turn(double p, double f, float magnitude) {
 }
 
 __device__ __forceinline__ double position(const RotaryArgs& a, int64_t token) {
-    const int64_t b = token / a.S, s = token - b * a.S;
+    const uint32_t b = (uint32_t)token / (uint32_t)a.S, s = (uint32_t)token - b * (uint32_t)a.S;
     int64_t p = s;
     if (a.positions) {
-        const int64_t at = b * a.psb + s * a.pss;
+        const int64_t at = (int64_t)b * a.psb + (int64_t)s * a.pss;
         p = a.positions_64 ? reinterpret_cast<const int64_t*>(a.positions)[at]
                            : (int64_t)reinterpret_cast<const int32_t*>(a.positions)[at];
     }
@@ -61,15 +61,27 @@ __device__ __forceinline__ double position(const RotaryArgs& a, int64_t token) {
     return (double)p;
 }
 
-// The cosines and sines of the tokens [first, first + 2^tokens_log).
-__device__ __forceinline__ void fill_table(const RotaryArgs& a, int64_t first, float2* table) {
-    const int n = a.R2 << a.tokens_log;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const int tk = i / a.R2, j = i - tk * a.R2;
-        const int64_t token = first + tk;
-        if (token < a.tokens) table[i] = turn(position(a, token), a.inv_freq[j], a.magnitude);
+// The tokens of a workgroup: cosines and sines, `width` a token of which those
+// from R2 on are 1 and 0, and offsets of the tokens' rows in each of N tensors.
+template <int N>
+struct Tokens {
+    __attribute__((aligned(16))) float2 table[kTablePairs];
+    int64_t at[N][kTokens];
+    __device__ __forceinline__ void fill(const RotaryArgs& a, int64_t first, int n, const HeadsArg* const (&t)[N]) {
+        const float inv = 1.0f / (float)a.width;
+        for (int i = threadIdx.x; i < n * a.width; i += kThreads) {
+            const int tk = quotient(i, inv), j = i - tk * a.width;
+            table[i] = j < a.R2 ? turn(position(a, first + tk), a.inv_freq[j], a.magnitude) : make_float2(1.0f, 0.0f);
+        }
+        if ((int)threadIdx.x < n) {
+            const uint32_t token = (uint32_t)first + threadIdx.x, b = token / (uint32_t)a.S, s = token - b * (uint32_t)a.S;
+#pragma unroll
+            for (int i = 0; i < N; ++i) at[i][threadIdx.x] = b * t[i]->sb + s * t[i]->ss;
+        }
     }
-}
+    // i / d for i < 2^20, given 1 / d
+    __device__ static __forceinline__ int quotient(int i, float inv) { return (int)(((float)i + 0.5f) * inv); }
+};
 
 // What a lane has of a head row: vectors `at[0]` and `at[1]`, the elements of
 // them, and how they are rotated.
@@ -77,65 +89,65 @@ template <int DT, int PAIRS>
 struct Row {
     static constexpr int P = Elem<DT>::per16;
     int at[2];   // vector of the row, or -1
+    bool full;   // every lane of a row has two vectors
     int lane, base;  // lane of the row; the lane group's first element in the exchange buffer
+    int angle;       // where this lane's cosines and sines begin in a token's
     float c[2 * P], s[2 * P];  // per element (FAR), per pair of the two vectors (HALF), per pair (INTER)
 
     __device__ __forceinline__ Row(const RotaryArgs& a) {
         const int nv = a.D / P;
         lane = threadIdx.x & ((1 << a.lanes_log) - 1);
         base = (threadIdx.x >> a.lanes_log) * a.D;
+        full = nv == 2 << a.lanes_log;
         if (PAIRS == PAIRS_HALF) {
             const int r = a.R2 / P;
             at[0] = lane < r ? lane : 2 * lane;
             at[1] = lane < r ? lane + r : 2 * lane + 1;
+            angle = lane < r ? lane * P : a.R2;
         } else {
             at[0] = 2 * lane, at[1] = 2 * lane + 1;
+            angle = lane * P;
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (at[i] >= nv) at[i] = -1;
     }
 
-    // The cosines and sines of this lane's elements; 1 and 0 where nothing is rotated.
+    // The cosines and sines of this lane's elements of a token.
     __device__ __forceinline__ void angles(const RotaryArgs& a, const float2* table, float sign) {
-        auto take = [&](int i, int j, bool turned) {
-            const float2 t = turned ? table[j] : make_float2(1.0f, 0.0f);
-            c[i] = t.x, s[i] = sign * t.y;
-        };
-        if constexpr (PAIRS == PAIRS_HALF) {
-#pragma unroll
-            for (int e = 0; e < P; ++e) take(e, lane * P + e, lane < a.R2 / P);
-        } else if constexpr (PAIRS == PAIRS_INTER) {
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int j = lane * P + i;
-                take(i, j, j < a.R2);
-            }
-        } else {
+        if constexpr (PAIRS == PAIRS_FAR) {
 #pragma unroll
             for (int i = 0; i < 2 * P; ++i) {
                 const int e = 2 * lane * P + i;
-                take(i, e < a.R2 ? e : e - a.R2, e < 2 * a.R2);
-                if (e < a.R2) s[i] = -s[i];
+                const float2 t = table[e < a.R2 ? e : e < 2 * a.R2 ? e - a.R2 : a.R2];
+                c[i] = t.x, s[i] = e < a.R2 ? -sign * t.y : sign * t.y;
+            }
+        } else {
+            const float4* from = reinterpret_cast<const float4*>(table + angle);
+#pragma unroll
+            for (int i = 0; i < P; i += 2) {
+                const float4 t = from[i / 2];
+                c[i] = t.x, s[i] = sign * t.y, c[i + 1] = t.z, s[i + 1] = sign * t.w;
             }
         }
     }
 
-    __device__ __forceinline__ void load(const char* row, float* x) const {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 v = at[i] >= 0 ? *reinterpret_cast<const uint4*>(row + at[i] * 16) : make_uint4(0, 0, 0, 0);
-            unpack16<DT>(v, x + i * P);
-        }
-    }
-    // The same without unpacking, from a row that can be read in any case.
+    // The vectors of a row that can be read in any case.
     __device__ __forceinline__ void fetch(const char* row, uint4 (&v)[2]) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i) v[i] = *reinterpret_cast<const uint4*>(row + (at[i] >= 0 ? at[i] * 16 : 0));
     }
-    __device__ __forceinline__ void unpack(const uint4 (&v)[2], float* x) const {
+    __device__ __forceinline__ void unpack(uint4 (&v)[2], float* x) const {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) unpack16<DT>(at[i] >= 0 ? v[i] : make_uint4(0, 0, 0, 0), x + i * P);
+        for (int i = 0; i < 2; ++i) {
+            if (!full && at[i] < 0) v[i] = make_uint4(0, 0, 0, 0);
+            unpack16<DT>(v[i], x + i * P);
+        }
+    }
+    __device__ __forceinline__ void load(const char* row, float* x) const {
+        uint4 v[2];
+        fetch(row, v);
+        unpack(v, x);
     }
     __device__ __forceinline__ void store(char* row, const float* x) const {
 #pragma unroll
@@ -195,112 +207,121 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes_log) {
     return v;
 }
 
-// Which part of the work a thread has: of the workgroup's 2^tokens_log tokens
-// the one `token`, of its heads every `step`th from `head` on.
-struct Share {
-    int64_t token, b, s;
-    int head, step, tk;
-    bool live;
-    __device__ __forceinline__ Share(const RotaryArgs& a, int64_t first) {
-        const int group = threadIdx.x >> a.lanes_log, per_log = 8 - a.lanes_log - a.tokens_log;
-        step = 1 << per_log;
-        tk = group >> per_log, head = group & (step - 1);
-        token = first + tk;
-        live = token < a.tokens;
-        b = token / a.S, s = token - b * a.S;
+// Workgroups a unit of the backward pass, all of which are resident: 168 registers
+// a thread, 128 in fp32.
+template <int DT> constexpr int kBackwardGroups = DT == DT_BF16 ? 3 : 4;
+
+// Which tensor a workgroup takes, and of which tokens: the first `blocks_q`
+// workgroups the queries, the others the keys.
+struct Part {
+    bool keys;
+    int heads, block, blocks;
+    __device__ __forceinline__ Part(const RotaryArgs& a) {
+        keys = (int)blockIdx.x >= a.blocks_q;
+        heads = keys ? a.Hk : a.Hq;
+        block = (int)blockIdx.x - (keys ? a.blocks_q : 0);
+        blocks = keys ? (int)gridDim.x - a.blocks_q : a.blocks_q;
     }
 };
-
-__device__ __forceinline__ char* head_row(const HeadsArg& t, const Share& w, int h) {
-    return t.p + w.b * t.sb + w.s * t.ss + h * t.sh;
-}
 
 template <int DT, int PAIRS, bool NORM>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a) {
     constexpr int P = Elem<DT>::per16;
-    __shared__ float2 table[kTablePairs];
+    __shared__ Tokens<2> tokens;
     __shared__ float exchange[PAIRS == PAIRS_FAR ? kThreads * 2 * P : 1];
     Row<DT, PAIRS> row(a);
-    const int heads = a.Hq + a.Hk;
-    float wq[NORM ? 2 * P : 1], wk[NORM ? 2 * P : 1];
-    if constexpr (NORM) {
-        row.load(a.wq, wq);
-        row.load(a.Hk ? a.wk : a.wq, wk);
-    }
-    const int64_t step = (int64_t)gridDim.x << a.tokens_log;
-    for (int64_t first = (int64_t)blockIdx.x << a.tokens_log; first < a.tokens; first += step) {
-        fill_table(a, first, table);
+    const Part part(a);
+    const HeadsArg in = part.keys ? a.k : a.q, out = part.keys ? a.ko : a.qo;
+    const float sign = a.inverse ? -1.0f : 1.0f, inv_d = 1.0f / (float)a.D, inv_heads = 1.0f / (float)part.heads;
+    float w[NORM ? 2 * P : 1];
+    if constexpr (NORM) row.load(part.keys ? a.wk : a.wq, w);
+    const int group = threadIdx.x >> a.lanes_log, groups = kThreads >> a.lanes_log;
+    for (int64_t first = (int64_t)part.block * a.T; first < a.tokens; first += (int64_t)part.blocks * a.T) {
+        const int n = a.tokens - first < a.T ? (int)(a.tokens - first) : a.T, rows = n * part.heads;
+        const HeadsArg* const both[2] = {&in, &out};
+        tokens.fill(a, first, n, both);
         __syncthreads();
-        const Share w(a, first);
-        row.angles(a, table + w.tk * a.R2, a.inverse ? -1.0f : 1.0f);
         // every lane goes round as often: sums and exchanges take all lanes of a row's wave
-        for (int h0 = 0; h0 < heads; h0 += w.step) {
-            const int h = h0 + w.head;
-            const bool live = w.live && h < heads, second = h >= a.Hq;
-            float x[2 * P];
-            if (live) {
-                row.load(second ? head_row(a.k, w, h - a.Hq) : head_row(a.q, w, h), x);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2 * P; ++i) x[i] = 0.0f;
-            }
-            if constexpr (NORM) {
+        if constexpr (NORM) {
+            int tk, h;
+            uint4 next[2];
+            auto fetch = [&](int r) {  // lanes without a row read the first one
+                const int some = r < rows ? r : 0;
+                tk = a.T > 1 ? tokens.quotient(some, inv_heads) : 0, h = some - tk * part.heads;
+                row.fetch(in.p + tokens.at[0][tk] + h * in.sh, next);
+            };
+            fetch(group);
+            for (int r = group, r0 = 0; r0 < rows; r0 += groups, r += groups) {
+                float x[2 * P];
+                row.unpack(next, x);
+                row.angles(a, tokens.table + tk * a.width, sign);
+                char* to = out.p + tokens.at[1][tk] + h * out.sh;
+                if (r0 + groups < rows) fetch(r + groups);
                 float ss = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 2 * P; ++i) ss = fmaf(x[i], x[i], ss);
-                const float rstd = 1.0f / sqrtf(lanes_sum(ss, a.lanes_log) / (float)a.D + a.eps);
+                const float rstd = 1.0f / sqrtf(lanes_sum(ss, a.lanes_log) * inv_d + a.eps);
 #pragma unroll
-                for (int i = 0; i < 2 * P; ++i) x[i] = x[i] * rstd * (second ? wk[i] : wq[i]);
+                for (int i = 0; i < 2 * P; ++i) x[i] = x[i] * rstd * w[i];
+                row.rotate(a, x, exchange);
+                if (r < rows) row.store(to, x);
             }
-            row.rotate(a, x, exchange);
-            if (live) row.store(second ? head_row(a.ko, w, h - a.Hq) : head_row(a.qo, w, h), x);
+        } else {
+            // the rotation alone does little for a row: each group of lanes stays with one token, whose angles
+            // it keeps (4 x 2048 tokens, 64 heads of 128: 45 us; 49 with rows as above)
+            const int per = groups / a.T, tk = group / per, h0 = group - tk * per, some = tk < n ? tk : 0;
+            row.angles(a, tokens.table + some * a.width, sign);
+            const char* from = in.p + tokens.at[0][some] + h0 * in.sh;
+            char* to = out.p + tokens.at[1][some] + h0 * out.sh;
+            const int64_t in_step = per * in.sh, out_step = per * out.sh;
+            for (int h = h0, i = 0; i < part.heads; i += per, h += per, from += in_step, to += out_step) {
+                const bool live = tk < n && h < part.heads;
+                float x[2 * P];
+                row.load(live ? from : in.p, x);
+                row.rotate(a, x, exchange);
+                if (live) row.store(to, x);
+            }
         }
         __syncthreads();  // the table is filled again
     }
 }
 
-// Workgroups a unit, all of which are resident: 168 registers a thread, 128 in fp32.
-template <int DT> constexpr int kBackwardGroups = DT == DT_BF16 ? 3 : 4;
-
-// The first `blocks_q` workgroups take the queries' heads, the others the keys':
-// one weight's sums a thread, which leaves three waves a SIMD instead of two.
 template <int DT, int PAIRS>
 __global__ __launch_bounds__(kThreads, kBackwardGroups<DT>) void rotary_backward_kernel(RotaryArgs a) {
     constexpr int P = Elem<DT>::per16;
-    __shared__ float2 table[kTablePairs];
+    __shared__ Tokens<3> tokens;
     __shared__ float exchange[PAIRS == PAIRS_FAR ? kThreads * 2 * P : 1];
     __shared__ float sums[kThreads / 64][kMaxHeadDim];
     Row<DT, PAIRS> row(a);
-    const bool keys = (int)blockIdx.x >= a.blocks_q;
-    const int lanes = 1 << a.lanes_log, heads = keys ? a.Hk : a.Hq, block = blockIdx.x - (keys ? a.blocks_q : 0);
-    const HeadsArg x_in = keys ? a.k : a.q, g_in = keys ? a.dk : a.dq, out = keys ? a.ko : a.qo;
+    const Part part(a);
+    const HeadsArg x_in = part.keys ? a.k : a.q, g_in = part.keys ? a.dk : a.dq, out = part.keys ? a.ko : a.qo;
+    const float inv_d = 1.0f / (float)a.D, inv_heads = 1.0f / (float)part.heads;
     float dw[2 * P], wt[2 * P];
-    row.load(keys ? a.wk : a.wq, wt);
+    row.load(part.keys ? a.wk : a.wq, wt);
 #pragma unroll
     for (int i = 0; i < 2 * P; ++i) dw[i] = 0.0f;
-    const int64_t step = (int64_t)(keys ? gridDim.x - a.blocks_q : a.blocks_q) << a.tokens_log;
-    // the next row's loads are under way while a row is worked on, also from one
-    // group of tokens to the next; lanes without a row read the first one
-    uint4 nx[2], ng[2];
-    auto fetch = [&](const Share& w, int h) {
-        const bool live = w.live && h < heads;
-        row.fetch(live ? head_row(x_in, w, h) : x_in.p, nx);
-        row.fetch(live ? head_row(g_in, w, h) : g_in.p, ng);
-    };
-    Share w(a, (int64_t)block << a.tokens_log);
-    fetch(w, w.head);
-    for (int64_t first = (int64_t)block << a.tokens_log; first < a.tokens; first += step) {
-        fill_table(a, first, table);
+    const int group = threadIdx.x >> a.lanes_log, groups = kThreads >> a.lanes_log;
+    for (int64_t first = (int64_t)part.block * a.T; first < a.tokens; first += (int64_t)part.blocks * a.T) {
+        const int n = a.tokens - first < a.T ? (int)(a.tokens - first) : a.T, rows = n * part.heads;
+        const HeadsArg* const three[3] = {&x_in, &g_in, &out};
+        tokens.fill(a, first, n, three);
         __syncthreads();
-        row.angles(a, table + w.tk * a.R2, -1.0f);
-        for (int h = w.head, h0 = 0; h0 < heads; h0 += w.step, h += w.step) {
-            const Share now = w;
-            const bool live = w.live && h < heads;
+        int tk, h;
+        uint4 nx[2], ng[2];
+        auto fetch = [&](int r) {  // lanes without a row read the first one
+            const int some = r < rows ? r : 0;
+            tk = a.T > 1 ? tokens.quotient(some, inv_heads) : 0, h = some - tk * part.heads;
+            row.fetch(x_in.p + tokens.at[0][tk] + h * x_in.sh, nx);
+            row.fetch(g_in.p + tokens.at[1][tk] + h * g_in.sh, ng);
+        };
+        fetch(group);
+        for (int r = group, r0 = 0; r0 < rows; r0 += groups, r += groups) {
             float x[2 * P], g[2 * P];
             row.unpack(nx, x);
             row.unpack(ng, g);
-            if (h0 + w.step >= heads) w = Share(a, first + step);
-            fetch(w, h0 + w.step >= heads ? w.head : h + w.step);
+            row.angles(a, tokens.table + tk * a.width, -1.0f);
+            char* to = out.p + tokens.at[2][tk] + h * out.sh;
+            if (r0 + groups < rows) fetch(r + groups);
             row.rotate(a, g, exchange);
             float ss = 0.0f, dot = 0.0f;
 #pragma unroll
@@ -309,24 +330,27 @@ __global__ __launch_bounds__(kThreads, kBackwardGroups<DT>) void rotary_backward
                 dot = fmaf(g[i] * wt[i], x[i], dot);
             }
             ss = lanes_sum(ss, a.lanes_log), dot = lanes_sum(dot, a.lanes_log);
-            const float rstd = 1.0f / sqrtf(ss / (float)a.D + a.eps), mean = dot * rstd / (float)a.D;
+            const float rstd = 1.0f / sqrtf(ss * inv_d + a.eps), mean = dot * rstd * inv_d;
+            if (r < rows) {
 #pragma unroll
-            for (int i = 0; i < 2 * P; ++i) {
-                const float xhat = x[i] * rstd;
-                if (live) dw[i] = fmaf(g[i], xhat, dw[i]);
-                x[i] = rstd * fmaf(-xhat, mean, g[i] * wt[i]);
+                for (int i = 0; i < 2 * P; ++i) {
+                    const float xhat = x[i] * rstd;
+                    dw[i] = fmaf(g[i], xhat, dw[i]);
+                    x[i] = rstd * fmaf(-xhat, mean, g[i] * wt[i]);
+                }
+                row.store(to, x);
             }
-            if (live) row.store(head_row(out, now, h), x);
         }
         __syncthreads();
     }
     // the weight's gradient of this workgroup: over the wave's rows by a fixed tree, then over the waves in order
+    for (int m = 1 << a.lanes_log; m < 64; m <<= 1)
 #pragma unroll
-    for (int i = 0; i < 2 * P; ++i) {
-        float v = dw[i];
-        for (int m = lanes; m < 64; m <<= 1) v += shfl_xor(v, m);
-        if ((threadIdx.x & 63) < lanes && row.at[i / P] >= 0) sums[threadIdx.x >> 6][row.at[i / P] * P + i % P] = v;
-    }
+        for (int i = 0; i < 2 * P; ++i) dw[i] += shfl_xor(dw[i], m);
+    if ((threadIdx.x & 63) < 1 << a.lanes_log)
+#pragma unroll
+        for (int i = 0; i < 2 * P; ++i)
+            if (row.at[i / P] >= 0) sums[threadIdx.x >> 6][row.at[i / P] * P + i % P] = dw[i];
     __syncthreads();
     for (int e = threadIdx.x; e < a.D; e += kThreads) {
         float v = sums[0][e];
@@ -358,30 +382,56 @@ int pairs_of(const RotaryArgs& a, int dtype) {
     return a.interleaved ? PAIRS_INTER : a.R2 % (dtype == DT_BF16 ? 8 : 4) == 0 ? PAIRS_HALF : PAIRS_FAR;
 }
 
-int64_t token_groups(const RotaryArgs& a) { return ((a.tokens - 1) >> a.tokens_log) + 1; }
-
 }  // namespace
 
-// A row's vectors two a lane.  Tokens a workgroup: as many as leave each token
-// enough groups of lanes for its heads in about four rounds (the angles are
-// formed once a token, and a lane's share of them is fetched once), but no
-// fewer workgroups than two a unit, and no more angles than the table holds.  In the
-// backward pass, whose workgroups stay, no fewer groups of tokens than eight a unit.
-void rotary_shape(RotaryArgs& a, int dtype, bool backward) {
-    const int nv = a.D / (dtype == DT_BF16 ? 8 : 4), need = (nv + 1) / 2;
+// A row's vectors two a lane.
+//
+// Forward: tokens for about eight rows a group of lanes, so that there are many
+// workgroups of which some load while others form angles, but at least two a unit
+// (4 x 2048 tokens, 64 heads of 128: 50 us with five workgroups a unit that stay).
+// Backward: workgroups that stay, as each leaves a row of partial sums: as many as are
+// resident, dealt to queries and keys as they have heads, each with its tokens in as few
+// equal parts as the table holds, so that all end together (8 x 1024 tokens, 12 heads of
+// 64: 19 us; 24 with parts of four tokens).
+int rotary_shape(RotaryArgs& a, int dtype, bool norm, bool backward) {
+    const int per16 = dtype == DT_BF16 ? 8 : 4, nv = a.D / per16, pairs = pairs_of(a, dtype);
     a.lanes_log = 0;
-    while ((1 << a.lanes_log) < need) ++a.lanes_log;
-    const int groups = kThreads >> a.lanes_log, heads = a.Hq + a.Hk;
-    a.tokens_log = 0;
-    while ((2 << a.tokens_log) <= groups && (a.R2 << (a.tokens_log + 1)) <= kTablePairs &&
-           (groups >> a.tokens_log) * 4 > heads && (a.tokens >> (a.tokens_log + 1)) >= (backward ? 8 : 2) * a.num_cus)
-        ++a.tokens_log;
+    while ((2 << a.lanes_log) < nv) ++a.lanes_log;
+    a.width = pairs == PAIRS_HALF ? a.R2 + per16 : pairs == PAIRS_INTER ? per16 << a.lanes_log : a.R2 + 1;
+    const int64_t heads = std::max(a.Hq, a.Hk), most_tokens = std::max<int64_t>(
+        1, std::min<int64_t>({kTokens, kTablePairs / a.width, ((int64_t)1 << 20) / heads}));
+    const int groups = kThreads >> a.lanes_log;
+    if (!backward && !norm) {  // a power of two, that divides the groups of lanes; about four rows a group
+        a.T = 1;
+        while (2 * a.T <= std::min<int64_t>(groups, most_tokens) && groups / a.T * 4 > a.Hq &&
+               a.tokens / (2 * a.T) >= 2 * a.num_cus)
+            a.T *= 2;
+    } else if (!backward) {
+        a.T = (int)std::max<int64_t>(1, std::min<int64_t>({most_tokens, 8 * groups / a.Hq,
+                                                           a.tokens / (2 * a.num_cus)}));
+    }
+    if (!backward) {
+        const int64_t all = (a.tokens + a.T - 1) / a.T;
+        a.blocks_q = (int)std::min<int64_t>(all, (int64_t)1 << 20);
+        if (a.Hk == 0) return a.blocks_q;
+        return a.blocks_q + (int)std::max<int64_t>(all > 0, std::min<int64_t>(a.blocks_q, all * a.Hk / a.Hq));
+    }
+    const int64_t blocks = (int64_t)a.num_cus * (dtype == DT_BF16 ? kBackwardGroups<DT_BF16> : kBackwardGroups<DT_F32>);
+    const int64_t keys = a.Hk == 0 ? 0 : std::max<int64_t>(1, blocks * a.Hk / (a.Hq + a.Hk));
+    const int64_t queries = std::max<int64_t>(1, blocks - keys);
+    // tokens a workgroup of the queries has, in equal parts
+    const int64_t share = std::max<int64_t>(1, (a.tokens + queries - 1) / queries);
+    const int64_t parts = (share + most_tokens - 1) / most_tokens;
+    a.T = (int)((share + parts - 1) / parts);
+    const int64_t all = (a.tokens + a.T - 1) / a.T;
+    a.blocks_q = (int)std::min(all, queries);
+    return a.blocks_q + (int)std::min(all, keys);
 }
 
-hipError_t run_rotary(const RotaryArgs& a, int dtype, hipStream_t st) {
+hipError_t run_rotary(const RotaryArgs& a, int blocks, int dtype, hipStream_t st) {
     const int pairs = pairs_of(a, dtype);
     const bool norm = a.wq != nullptr;
-    const dim3 grid((unsigned)std::min<int64_t>(token_groups(a), (int64_t)1 << 20));
+    const dim3 grid((unsigned)blocks);
 #define PAMM_CASE(DT, PAIRS)                                                                                    \
     if (dtype == DT && pairs == PAIRS) {                                                                        \
         auto* kernel = norm ? rotary_kernel<DT, PAIRS, true> : rotary_kernel<DT, PAIRS, false>;                 \
@@ -395,20 +445,8 @@ hipError_t run_rotary(const RotaryArgs& a, int dtype, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Each workgroup leaves a row of partial sums of its weight: as many as are
-// resident, looping over their tokens, dealt to queries and keys as they have heads.
-int rotary_backward_blocks(RotaryArgs& a, int dtype) {
-    if (a.tokens == 0) return a.blocks_q = 0;
-    const int64_t groups = token_groups(a);
-    const int64_t most = (int64_t)a.num_cus * (dtype == DT_BF16 ? kBackwardGroups<DT_BF16> : kBackwardGroups<DT_F32>);
-    if (a.Hk == 0) return a.blocks_q = (int)std::min(groups, most);
-    const int64_t keys = std::min(groups, std::max<int64_t>(1, most * a.Hk / (a.Hq + a.Hk)));
-    a.blocks_q = (int)std::min(groups, std::max<int64_t>(1, most - keys));
-    return a.blocks_q + (int)keys;
-}
-
-hipError_t run_rotary_backward(RotaryArgs a, int dtype, hipStream_t st) {
-    const int blocks = rotary_backward_blocks(a, dtype), pairs = pairs_of(a, dtype);
+hipError_t run_rotary_backward(const RotaryArgs& a, int blocks, int dtype, hipStream_t st) {
+    const int pairs = pairs_of(a, dtype);
     if (blocks > 0) {
 #define PAMM_CASE(DT, PAIRS)                                                                                    \
     if (dtype == DT && pairs == PAIRS)                                                                          \

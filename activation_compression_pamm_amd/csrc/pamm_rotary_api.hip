@@ -57,8 +57,8 @@ pamm::HeadsArg heads_arg(const pamm_rotary_t* a, const pamm_heads_t& t, int64_t 
             heads > 1 ? t.stride_h * e : 0};
 }
 
-// What the workspace's size goes by: sizes alone.
-pamm::RotaryArgs sizes_arg(const pamm_rotary_t* a, bool backward) {
+// What the workspace's size goes by: sizes and the layout alone.
+pamm::RotaryArgs sizes_arg(const pamm_rotary_t* a, bool backward, int& blocks) {
     pamm::RotaryArgs r;
     memset(&r, 0, sizeof r);
     r.tokens = a->batch * a->seq;
@@ -67,13 +67,14 @@ pamm::RotaryArgs sizes_arg(const pamm_rotary_t* a, bool backward) {
     r.Hk = (int)a->heads_k;
     r.D = (int)a->head_dim;
     r.R2 = (int)(a->rot_dim / 2);
+    r.interleaved = a->interleaved;
     r.num_cus = num_cus();
-    pamm::rotary_shape(r, a->dtype, backward);
+    blocks = pamm::rotary_shape(r, a->dtype, a->q_weight != nullptr, backward);
     return r;
 }
 
-pamm::RotaryArgs rotary_args(const pamm_rotary_t* a, bool backward) {
-    pamm::RotaryArgs r = sizes_arg(a, backward);
+pamm::RotaryArgs rotary_args(const pamm_rotary_t* a, bool backward, int& blocks) {
+    pamm::RotaryArgs r = sizes_arg(a, backward, blocks);
     r.q = heads_arg(a, a->q, a->heads_q);
     r.qo = heads_arg(a, a->q_out, a->heads_q);
     if (a->heads_k > 0) {
@@ -89,7 +90,6 @@ pamm::RotaryArgs rotary_args(const pamm_rotary_t* a, bool backward) {
     r.wk = reinterpret_cast<const char*>(a->k_weight);
     r.positions_64 = a->positions_64;
     r.inverse = a->inverse;
-    r.interleaved = a->interleaved;
     r.magnitude = a->magnitude;
     r.eps = a->eps;
     return r;
@@ -102,13 +102,16 @@ extern "C" {
 int pamm_rotary(const pamm_rotary_t* a, void* stream) {
     if (int e = rotary_check(a)) return e;
     if (a->batch == 0 || a->seq == 0) return PAMM_OK;
-    return status(pamm::run_rotary(rotary_args(a, false), a->dtype, reinterpret_cast<hipStream_t>(stream)));
+    int blocks;
+    const pamm::RotaryArgs r = rotary_args(a, false, blocks);
+    return status(pamm::run_rotary(r, blocks, a->dtype, reinterpret_cast<hipStream_t>(stream)));
 }
 
 size_t pamm_rotary_backward_workspace_size(const pamm_rotary_t* a) {
     if (rotary_sizes(a) != PAMM_OK) return 0;
-    pamm::RotaryArgs r = sizes_arg(a, true);
-    return up256((size_t)pamm::rotary_backward_blocks(r, a->dtype) * (size_t)r.D * sizeof(float));
+    int blocks;
+    const pamm::RotaryArgs r = sizes_arg(a, true, blocks);
+    return up256((size_t)blocks * (size_t)r.D * sizeof(float));
 }
 
 int pamm_rotary_backward(const pamm_rotary_t* a, const pamm_heads_t* dq, const pamm_heads_t* dk, float* dwq,
@@ -118,13 +121,14 @@ int pamm_rotary_backward(const pamm_rotary_t* a, const pamm_heads_t* dq, const p
     if (int e = both_check(a, *dq, a->heads_k > 0 ? *dk : *dq)) return e;
     if (!aligned(dwq, 4) || !aligned(dwk, 4)) return PAMM_ERR_ALIGN;
     if (int e = ws_check(ws, ws_bytes, pamm_rotary_backward_workspace_size(a))) return e;
-    pamm::RotaryArgs r = rotary_args(a, true);
+    int blocks;
+    pamm::RotaryArgs r = rotary_args(a, true, blocks);
     r.dq = heads_arg(a, *dq, a->heads_q);
     if (a->heads_k > 0) r.dk = heads_arg(a, *dk, a->heads_k);
     r.part = reinterpret_cast<float*>(ws);
     r.dwq = dwq;
     r.dwk = a->heads_k > 0 ? dwk : nullptr;
-    return status(pamm::run_rotary_backward(r, a->dtype, reinterpret_cast<hipStream_t>(stream)));
+    return status(pamm::run_rotary_backward(r, blocks, a->dtype, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -18,16 +18,15 @@ struct RotaryArgs {
     int S, Hq, Hk, D, R2;    // R2: rotated pairs of a row
     int positions_64, inverse, interleaved;
     float magnitude, eps;
-    int lanes_log, tokens_log;  // lanes a row, tokens a workgroup at a time
     int num_cus;
-    int blocks_q;            // backward: workgroups that take the queries
+    // how the work is cut: lanes of a row, tokens of a workgroup at a time, entries a token has in
+    // the table, and workgroups that take the queries
+    int lanes_log, T, width, blocks_q;
 };
 
-// Fills in how the work is cut.
-void rotary_shape(RotaryArgs& a, int dtype, bool backward);
-// Workgroups of the backward pass; fills in those for the queries.
-int rotary_backward_blocks(RotaryArgs& a, int dtype);
-hipError_t run_rotary(const RotaryArgs& a, int dtype, hipStream_t st);
-hipError_t run_rotary_backward(RotaryArgs a, int dtype, hipStream_t st);
+// Fills in how the work is cut; the number of workgroups.
+int rotary_shape(RotaryArgs& a, int dtype, bool norm, bool backward);
+hipError_t run_rotary(const RotaryArgs& a, int blocks, int dtype, hipStream_t st);
+hipError_t run_rotary_backward(const RotaryArgs& a, int blocks, int dtype, hipStream_t st);
 
 }  // namespace pamm

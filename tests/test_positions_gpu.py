@@ -249,6 +249,24 @@ def test_workspace_and_stream():
         assert all(torch.equal(a, b) for a, b in zip(got, ref))
 
 
+@BOTH
+@KINDS
+@pytest.mark.parametrize("B,S,H,Hkv", [(1, 1, 4, 2), (2, 700, 8, 1), (3, 5, 2, 9)])
+def test_queries_and_keys_without_weights_in_one_call(dtype, interleaved, B, S, H, Hkv):
+    """The C call takes both without a norm, too."""
+    from activation_compression_pamm_amd import position_ops as ops
+    from activation_compression_pamm_amd.block_ops import _code, _heads_tensor
+
+    q, k = (torch.randn(B, S, h, 64, device="cuda").to(DT[dtype]) for h in (H, Hkv))
+    f, qo, ko = freqs(32), torch.empty_like(q), torch.empty_like(k)
+    h = [x for t in (q, k, qo, ko) for x in _heads_tensor("", "", t)]
+    p = ops._pack_rotary(_code("", q), int(interleaved), 0, 0, B, S, H, Hkv, 64, 32, 1.0, 0.0, f.data_ptr(), 0, 0, 0, 0, 0,
+                         0, *h)
+    assert ops._lib().pamm_rotary(p, torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(qo, pamm.rotary(q, f, interleaved=interleaved))
+    assert torch.equal(ko, pamm.rotary(k, f, interleaved=interleaved))
+
+
 def test_far_rows():
     """Byte offsets past 2^32 between tokens and heads."""
     big = torch.empty(3 * (1 << 30) + (1 << 10), dtype=torch.bfloat16, device="cuda")
