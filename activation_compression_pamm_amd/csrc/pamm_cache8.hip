@@ -31,13 +31,54 @@ struct Extent {
     }
 };
 
+// The largest |x| of a vector's elements as bits, with what is not finite above all else.
+template <int DT>
+__device__ __forceinline__ uint32_t top_bits(const uint4& v, uint32_t top) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (DT == DT_BF16) {  // two at a time, each half in place
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        u16x2 t = __builtin_bit_cast(u16x2, top);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t = __builtin_elementwise_max(t, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+        return __builtin_bit_cast(uint32_t, t);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, w[i] & 0x7fffffffu);
+        return top;
+    }
+}
+
+constexpr float kLeast = 1.17549435e-38f;  // of a scale
+
+// A vector's elements as they are stored.
+template <int DT, bool FINITE>
+__device__ __forceinline__ void eight_bits(const uint4& v, float inv, float part, float seven, uint32_t* o) {
+    constexpr int P = Elem<DT>::per16;
+    float u[P];
+    unpack16<DT>(v, u);
+#pragma unroll
+    for (int k = 0; k < P; k += 4) {
+        float w[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            // at most 448 but for a rounding, which the conversion takes back
+            const float n = u[k + m] * seven, q = n * inv;
+            w[m] = fmaf(fmaf(-q, part, n), inv, q);
+            if (!FINITE && !isfinite(u[k + m])) w[m] = NAN;
+        }
+        o[k / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(w[2], w[3], __builtin_amdgcn_cvt_pk_fp8_f32(w[0], w[1], 0, false), true);
+    }
+}
+
 // Keys and values of a block of one head together: twice the loads under way in
 // a workgroup, which lives only for one block.
 template <int DT, int VPT>
 __global__ __launch_bounds__(kThreads) void cache8_append_kernel(AppendArgs a, int64_t items) {
     constexpr int P = Elem<DT>::per16;
-    __shared__ float tops[2][2][kThreads / 64];
+    __shared__ uint32_t tops[2][2][kThreads / 64];
     const int tid = threadIdx.x, per_row = a.D / P, block = 1 << a.block_log, vectors = block * per_row;
+    const float inv_row = 1.0f / (float)per_row;
+    auto row_of = [&](int at) { return (int)(((float)at + 0.5f) * inv_row); };  // at / per_row, for at < 2^20
     int slot = 0;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int h = (int)(item % a.Hkv);
@@ -45,53 +86,69 @@ __global__ __launch_bounds__(kThreads) void cache8_append_kernel(AppendArgs a, i
         const int j = (int)(left % a.touched), b = (int)(left / a.touched);
         const Extent e(a, b);
         const int first = (e.have >> a.block_log) + j, start = first << a.block_log, end = e.have + e.get;
-        const char* x[2];
+        const char* x[2];  // the new tokens
         char* tail[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            // row of token p: x + p * ss
-            x[t] = a.t[t].x.p + b * a.t[t].x.sb + h * a.t[t].x.sh - e.have * a.t[t].x.ss;
+            x[t] = a.t[t].x.p + b * a.t[t].x.sb + h * a.t[t].x.sh;
             tail[t] = a.t[t].tail.p + b * a.t[t].tail.sb + h * a.t[t].tail.sh;
         }
         if (e.get > 0 && start + block <= end) {
+            // rows of the block that wait in the tail; those behind them begin at this token of the call's
+            const int waiting = e.have > start ? e.have - start : 0, from = start + waiting - e.have;
             uint4 v[2][VPT];
+            uint32_t top[2] = {0, 0};
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t) {
+                const char* rows = x[t] + (from - waiting) * a.t[t].x.ss;
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
-                    const int at = tid + i * kThreads, r = at / per_row, c = at - r * per_row;
+                    const int at = tid + i * kThreads, r = row_of(at), c = at - r * per_row;
                     v[t][i] = make_uint4(0, 0, 0, 0);
-                    if (at < vectors)
-                        v[t][i] = *reinterpret_cast<const uint4*>((start + r < e.have ? tail[t] + r * a.t[t].tail.ss
-                                                                                      : x[t] + (start + r) * a.t[t].x.ss) +
-                                                                  c * 16);
+                    if (at >= vectors) continue;
+                    // a row's distance, 128 times, is below 2^32
+                    if (waiting == 0)
+                        v[t][i] = *reinterpret_cast<const uint4*>(rows + ((uint32_t)r * (uint32_t)a.t[t].x.ss + c * 16));
+                    else
+                        v[t][i] = *reinterpret_cast<const uint4*>((r < waiting ? tail[t] + r * a.t[t].tail.ss
+                                                                               : rows + r * a.t[t].x.ss) + c * 16);
                 }
-            float top[2] = {0.0f, 0.0f};
+            }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    float u[P];
-                    unpack16<DT>(v[t][i], u);
+                for (int i = 0; i < VPT; ++i) top[t] = top_bits<DT>(v[t][i], top[t]);
+                if constexpr (DT == DT_BF16) top[t] = max(top[t] & 0xffffu, top[t] >> 16) << 16;
 #pragma unroll
-                    for (int k = 0; k < P; ++k) top[t] = fmaxf(top[t], isfinite(u[k]) ? fabsf(u[k]) : 0.0f);
-                }
-#pragma unroll
-                for (int m = 1; m < 64; m <<= 1) top[t] = fmaxf(top[t], shfl_xor(top[t], m));
+                for (int m = 1; m < 64; m <<= 1) top[t] = max(top[t], (uint32_t)shfl_xor((int)top[t], m));
                 if ((tid & 63) == 0) tops[slot][t][tid >> 6] = top[t];
             }
             __syncthreads();
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                float most = tops[slot][t][0];
+                uint32_t bits = tops[slot][t][0];
 #pragma unroll
-                for (int k = 1; k < kThreads / 64; ++k) most = fmaxf(most, tops[slot][t][k]);
+                for (int k = 1; k < kThreads / 64; ++k) bits = max(bits, tops[slot][t][k]);
+                const bool finite = bits < 0x7f800000u;
+                if (!finite) {  // rarely: the largest of the others, by every wave for itself
+                    float most = 0.0f;
+                    const char* rows = x[t] + (from - waiting) * a.t[t].x.ss;
+                    for (int at = tid & 63; at < vectors; at += 64) {
+                        const int r = row_of(at), c = at - r * per_row;
+                        float u[P];
+                        unpack16<DT>(*reinterpret_cast<const uint4*>((r < waiting ? tail[t] + r * a.t[t].tail.ss
+                                                                                  : rows + r * a.t[t].x.ss) + c * 16), u);
+#pragma unroll
+                        for (int k = 0; k < P; ++k) most = fmaxf(most, isfinite(u[k]) ? fabsf(u[k]) : 0.0f);
+                    }
+#pragma unroll
+                    for (int m = 1; m < 64; m <<= 1) most = fmaxf(most, shfl_xor(most, m));
+                    bits = __float_as_uint(most);
+                }
                 // 448 x / most = (7/8 x) / (most / 512): a quotient and its correction by the remainder, which for
                 // bf16 (products of 3 and 8 bits) is rounded as the definition is; tiny numbers are raised by a power
                 // of two first, below which the products would lose bits
-                constexpr float kLeast = 1.17549435e-38f;
-                most = fmaxf(most, 448.0f * kLeast);
-                const float raise = most < 0x1p-60f ? 0x1p64f : 1.0f;
+                const float most = fmaxf(__uint_as_float(bits), 448.0f * kLeast), raise = most < 0x1p-60f ? 0x1p64f : 1.0f;
                 const float inv = 512.0f / (most * raise), part = most * raise * (1.0f / 512.0f), seven = 0.875f * raise;
                 const ScalesArg& sc = a.t[t].scale;
                 if (tid == 0) sc.p[b * sc.sb + first * sc.ss + h * sc.sh] = most / 448.0f;
@@ -99,40 +156,33 @@ __global__ __launch_bounds__(kThreads) void cache8_append_kernel(AppendArgs a, i
                 char* to = out.p + b * out.sb + h * out.sh + start * out.ss;
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
-                    const int at = tid + i * kThreads, r = at / per_row, c = at - r * per_row;
+                    const int at = tid + i * kThreads, r = row_of(at), c = at - r * per_row;
                     if (at >= vectors) continue;
-                    float u[P];
-                    unpack16<DT>(v[t][i], u);
                     uint32_t o[P / 4];
-#pragma unroll
-                    for (int k = 0; k < P; k += 4) {
-                        float w[4];
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const float n = u[k + m] * seven, q = n * inv, f = fmaf(fmaf(-q, part, n), inv, q);
-                            w[m] = isfinite(u[k + m]) ? fminf(fmaxf(f, -448.0f), 448.0f) : NAN;
-                        }
-                        o[k / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(
-                            w[2], w[3], __builtin_amdgcn_cvt_pk_fp8_f32(w[0], w[1], 0, false), true);
-                    }
-                    if constexpr (P == 8)
-                        *reinterpret_cast<uint2*>(to + r * out.ss + c * P) = make_uint2(o[0], o[1]);
+                    if (finite)
+                        eight_bits<DT, true>(v[t][i], inv, part, seven, o);
                     else
-                        *reinterpret_cast<uint32_t*>(to + r * out.ss + c * P) = o[0];
+                        eight_bits<DT, false>(v[t][i], inv, part, seven, o);
+                    char* place = to + ((uint32_t)r * (uint32_t)out.ss + c * P);
+                    if constexpr (P == 8)
+                        *reinterpret_cast<uint2*>(place) = make_uint2(o[0], o[1]);
+                    else
+                        *reinterpret_cast<uint32_t*>(place) = o[0];
                 }
             }
-            slot ^= 1;  // the next block's maxima: between two uses of one place lies a barrier
+            slot ^= 1;           // the next block's maxima: between two uses of one place lies a barrier
+            if (waiting > 0) __syncthreads();  // the tail is written below: every wave has read it, also for a second time
         }
         // the tokens behind the last whole block
-        const int rest = end >> a.block_log << a.block_log, from = e.have > rest ? e.have : rest;
-        if (j == 0 && from < end) {
-            const int n = (end - from) * per_row;
+        const int rest = end >> a.block_log << a.block_log, behind = e.have > rest ? e.have : rest;
+        if (j == 0 && behind < end) {
+            const int n = (end - behind) * per_row;
             for (int i = tid; i < 2 * n; i += kThreads) {
                 const bool second = i >= n;
-                const int at = second ? i - n : i, r = at / per_row, c = at - r * per_row;
+                const int at = second ? i - n : i, r = row_of(at), c = at - r * per_row;
                 const int64_t ts = second ? a.t[1].tail.ss : a.t[0].tail.ss, xs = second ? a.t[1].x.ss : a.t[0].x.ss;
-                *reinterpret_cast<uint4*>((second ? tail[1] : tail[0]) + (from - rest + r) * ts + c * 16) =
-                    *reinterpret_cast<const uint4*>((second ? x[1] : x[0]) + (from + r) * xs + c * 16);
+                *reinterpret_cast<uint4*>((second ? tail[1] : tail[0]) + (behind - rest + r) * ts + c * 16) =
+                    *reinterpret_cast<const uint4*>((second ? x[1] : x[0]) + (behind - e.have + r) * xs + c * 16);
             }
         }
     }

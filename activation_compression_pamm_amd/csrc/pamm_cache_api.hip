@@ -81,7 +81,7 @@ int pamm_cache8_append(const pamm_cache8_t* c, const pamm_heads_t* k, const pamm
     if (advance != 0 && advance != 1) return PAMM_ERR_VALUE;
     const int es = elem_size(c->dtype);
     for (const pamm_heads_t* t : {k, v})
-        if (int e = heads_check(*t, c->batch, n, c->heads_kv, es, false)) return e;
+        if (int e = heads_check(*t, c->batch, n, c->heads_kv, es)) return e;
     if (c->batch > 0 && !lengths) return PAMM_ERR_NULL;
     if (!aligned(new_len, 4) || !aligned(lengths, 4)) return PAMM_ERR_ALIGN;
     if (mul(c->batch, c->heads_kv) > kMaxSize) return PAMM_ERR_SHAPE;

@@ -53,7 +53,7 @@ typedef struct {
  * lengths (at most room), else it is left.
  *
  * No written tensor may meet another tensor of the call, or itself.  Errors: PAMM_ERR_NULL, _DTYPE, _SHAPE, _ALIGN
- * (head_dim, addresses or strides off 16 bytes), _VALUE (block, advance).
+ * (head_dim, addresses or strides off 16 bytes), _VALUE (block, advance), _UNSUPPORTED (64 rows span 2 GiB or more).
  */
 int pamm_cache8_append(const pamm_cache8_t *cache_host, const pamm_heads_t *k_host, const pamm_heads_t *v_host,
                        int64_t n, const int32_t *new_len, int32_t *lengths, int32_t advance, void *stream);
