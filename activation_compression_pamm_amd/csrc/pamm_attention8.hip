@@ -80,8 +80,7 @@ struct Wide {
 
 // The scales of 64 tiles to come, one a lane, from which each tile's are read
 // into scalar registers.  Loaded tile by tile, a scale on its way is copied to
-// where the current one was at the loop's end, and that copy waits for all loads
-// (64 queries over ragged 8192 keys, 32/8 heads of 128: 135 us instead of TODO).
+// where the current one was at the loop's end, and that copy waits for all loads.
 struct TileScales {
     float v;
     __device__ __forceinline__ void load(const ScalesArg& s, int b, int h, int block, bool ok) {
@@ -134,7 +133,10 @@ __device__ __forceinline__ int whole_blocks(const Cache8Args& c, int Lk) { retur
 // ---------------------------------------------------------------- many rows
 
 // As attention_rows: four waves of 32 rows share tiles of 32 keys in two LDS
-// buffers, the next tile under way in registers.
+// buffers, the next tile under way in registers.  2 x 512 queries over 8192 keys, 32/8
+// heads of 128: 164 us and 12 for the join; the same over bf16, whose tiles are not widened, 159 and 12.
+// Widening takes 16 conversions a thread and tile.  One loop with the products in fp16 and in bf16 side by
+// side spills the sums (827 us): tiles that need bf16 have a loop of their own.
 //
 // The softmax of a tile and its probabilities times the values' scale, in the
 // exponent, from which the sum is turned back; otherwise as softmax_update.
@@ -583,7 +585,13 @@ __global__ __launch_bounds__(256, 1) void attention8_few_again_kernel(AttnArgs a
 
 // Single tokens whose key/value heads are shared by up to 16 query heads: 16 x 16
 // products, which take half the registers, exponentials and matrix cycles of the
-// 32 x 32 ones, so four waves a SIMD have loads under way instead of two.
+// 32 x 32 ones.
+//
+// Bound by reading the cache.  64 sequences of 64 to 8192 keys, 8 heads of 128, 0.56
+// GB: 98 us with the join (5.7 TB/s); all of 8192, 1.07 GB: 162 us whole (6.6 TB/s).  Both
+// with three waves a SIMD; four spill, and a reload in the loop waits for all loads (124 and
+// 205 us).  Without the hint that lines are read once the loads alone take 16% more
+// (193 us for 167).  With the 32 x 32 products and two waves a SIMD 125 us.
 //
 // A lane holds row (A) or column (B) l % 16 of a product and the 16-byte vector
 // of quarter l / 16 of each step; result element i is D[4 (l / 16) + i][l % 16].
@@ -687,7 +695,8 @@ __device__ __forceinline__ void attention8_one(const AttnArgs& a, const Cache8Ar
     char* vt = shared.lds + wave * OneShared<DT, ND>::SLOT;
 
     // Whole lines of a tile a load, which go through LDS: an operand's own 16 bytes of each key would take
-    // half a line a load, and be fetched twice past the caches (115 instead of 127 us, see below).
+    // half a line a load, and with the hint for what is read once be fetched twice (127 us instead of 114 in
+    // the case above, both with spills).
     // Loads are issued in any case, past the last tile out of bounds: where a branch may leave
     // them out, the next wait is for every load instead of the oldest ones.
     uint4 kr[R::LOADS], vr[R::LOADS];
@@ -956,15 +965,17 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 3 : 2) void attention8_one_ker
 
 // Few rows: two workgroups a unit, and parts of at least 1024 keys.  A second launch and the
 // parts' memory cost a call 7 us (1 x 1024 keys, 12 heads of 64: 16.9 us whole, 22 to 24 in
-// parts; 8192, 8 heads of 128: 57.7 whole, 26.9 in 4, 25.2 in 8, 24.5 in 16).  Where the
-// heads fill the device, parts gain nothing, though lengths differ (64 sequences of up to 8192 keys,
-// 8 heads of 128: 101 us whole, 99, 99 and 103 in 2, 4 and 8; of 8192 each: 161, 177, 171 and 177).
+// parts; 8192, 8 heads of 128: 63 whole, 27 in 4, 25 in 8).  Where lengths are given, which
+// then differ as a rule, eight a unit even them out, as long as parts have 2048 keys (64
+// sequences of up to 8192, 8 heads of 128: 104 us whole, 100 and 98 in 2 and 4, 105 in 8; of
+// up to 2048: 30 whole, 37 in 2; where all have 8192 after all: 162 whole, 178 and 172 in 2 and 4).
 // Many rows are cut as over a cache that is not in 8 bits.
 int attention8_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, bool lengths, int num_cus) {
     if (Sq * G > kFewRows) return attention_splits(B, Sq, Sk, Hkv, G, lengths, num_cus);
-    const int64_t blocks = B * Hkv, want = 2 * (int64_t)num_cus;
-    if (blocks == 0 || blocks >= want) return 1;
-    const int64_t n = std::min((want + blocks - 1) / blocks, (Sk + 1023) / 1024);
+    const int64_t blocks = B * Hkv, units = num_cus;
+    if (blocks == 0) return 1;
+    int64_t n = std::min((2 * units + blocks - 1) / blocks, (Sk + 1023) / 1024);
+    if (lengths) n = std::max(n, std::min((8 * units + blocks - 1) / blocks, Sk / 2048));
     return (int)std::max<int64_t>(1, std::min<int64_t>(n, kMaxSplits));
 }
 

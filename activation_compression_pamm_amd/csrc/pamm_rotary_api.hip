@@ -50,11 +50,11 @@ int rotary_check(const pamm_rotary_t* a) {
     return both_check(a, a->q_out, a->k_out);
 }
 
-// Strides in bytes; that of a dimension with one entry may be anything.
+// Strides in bytes; that of a dimension with one entry may be anything, as may all without a token.
 pamm::HeadsArg heads_arg(const pamm_rotary_t* a, const pamm_heads_t& t, int64_t heads) {
-    const int64_t e = elem_size(a->dtype);
-    return {reinterpret_cast<char*>(t.data), a->batch > 1 ? t.stride_b * e : 0, a->seq > 1 ? t.stride_s * e : 0,
-            heads > 1 ? t.stride_h * e : 0};
+    const int64_t e = a->batch > 0 && a->seq > 0 ? elem_size(a->dtype) : 0;
+    return {reinterpret_cast<char*>(t.data), e && a->batch > 1 ? t.stride_b * e : 0, e && a->seq > 1 ? t.stride_s * e : 0,
+            e && heads > 1 ? t.stride_h * e : 0};
 }
 
 // What the workspace's size goes by: sizes and the layout alone.

@@ -116,9 +116,10 @@ def test_attention_validation(lib):
     assert call(problem(window=-1)) == EVALUE and call(problem(window=4, causal=0)) == EVALUE
     assert call(problem(q=_Heads(None, 768, 256, 64))) == ENULL and call(problem(o=_Heads(FAKE + 2, 768, 256, 64))) == EALIGN
     assert call(problem(lse=None)) == ENULL and call(problem(kv_len=FAKE + 2)) == EALIGN
-    need = size(problem())
+    p, c = problem(seq_k=8192), cache(room=8192)  # long enough to be cut into parts
+    need = size(p, c)
     assert need > 0 and need % 256 == 0 and size(problem(seq_k=32)) == 0
-    assert call(problem(), ws=None) == EWS and call(problem(), n=need - 1) == EWS and call(problem(), ws=FAKE + 16) == EALIGN
+    assert call(p, c, ws=None) == EWS and call(p, c, n=need - 1) == EWS and call(p, c, ws=FAKE + 16) == EALIGN
     assert call(problem(batch=0), cache(batch=0)) == OK and call(problem(seq_q=0)) == OK
 
 
