@@ -24,7 +24,9 @@ constexpr int kThreads = 256;
 constexpr int kTablePairs = 2048, kTokens = 64;  // of a workgroup at a time
 constexpr int kMaxHeadDim = 128;
 
-enum : int { PAIRS_INTER = 0, PAIRS_HALF = 1, PAIRS_FAR = 2 };  // FAR: half, R2 not a whole number of vectors
+// FAR: either layout, R2 not a whole number of vectors, so that a lane's elements are rotated in part.  (A choice for
+// each pair in the interleaved kernel took norm and rotation of 4 x 2048 tokens, 32/8 heads of 128, from 32 to 38 us.)
+enum : int { PAIRS_INTER = 0, PAIRS_HALF = 1, PAIRS_FAR = 2 };
 
 // cos and sin of p * f radians.  The angle in turns and its reduction to
 // within an eighth of one are exact to 64 bits, so that positions of millions
@@ -119,8 +121,9 @@ struct Row {
 #pragma unroll
             for (int i = 0; i < 2 * P; ++i) {
                 const int e = 2 * lane * P + i;
-                const float2 t = table[e < a.R2 ? e : e < 2 * a.R2 ? e - a.R2 : a.R2];
-                c[i] = t.x, s[i] = e < a.R2 ? -sign * t.y : sign * t.y;
+                const bool first = a.interleaved ? e % 2 == 0 : e < a.R2;
+                const float2 t = table[e >= 2 * a.R2 ? a.R2 : a.interleaved ? e / 2 : first ? e : e - a.R2];
+                c[i] = t.x, s[i] = first ? -sign * t.y : sign * t.y;
             }
         } else {
             const float4* from = reinterpret_cast<const float4*>(table + angle);
@@ -155,24 +158,24 @@ struct Row {
             if (at[i] >= 0) *reinterpret_cast<uint4*>(row + at[i] * 16) = pack16<DT>(x + i * P);
     }
 
-    // Rotates this lane's elements.  `exchange` holds a row for each group of
-    // lanes: in the FAR layout an element's partner is in another lane.  All
+    // Rotates this lane's elements; those past the rotated ones are left alone, as what is not
+    // finite in one of them must not reach another.  `exchange` holds a row for each group of
+    // lanes: in the FAR layout an element's partner may be in another lane.  All
     // lanes of the wave take part.
     __device__ __forceinline__ void rotate(const RotaryArgs& a, float* x, float* exchange) const {
+        auto turned = [&](float& u0, float& v0, int i) {
+            const float u = u0, v = v0;
+            u0 = fmaf(u, c[i], -(v * s[i]));
+            v0 = fmaf(u, s[i], v * c[i]);
+        };
         if constexpr (PAIRS == PAIRS_HALF) {
+            if (lane * P >= a.R2) return;
 #pragma unroll
-            for (int e = 0; e < P; ++e) {
-                const float u = x[e], v = x[P + e];
-                x[e] = fmaf(u, c[e], -(v * s[e]));
-                x[P + e] = fmaf(u, s[e], v * c[e]);
-            }
+            for (int e = 0; e < P; ++e) turned(x[e], x[P + e], e);
         } else if constexpr (PAIRS == PAIRS_INTER) {
+            if (lane * P >= a.R2) return;
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float u = x[2 * i], v = x[2 * i + 1];
-                x[2 * i] = fmaf(u, c[i], -(v * s[i]));
-                x[2 * i + 1] = fmaf(u, s[i], v * c[i]);
-            }
+            for (int i = 0; i < P; ++i) turned(x[2 * i], x[2 * i + 1], i);
         } else {
             const int first = 2 * lane * P;
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // what the row before was read for
@@ -186,7 +189,7 @@ struct Row {
             for (int i = 0; i < 2 * P; ++i) {
                 const int e = first + i;
                 if (e >= 2 * a.R2) continue;
-                const float other = exchange[base + (e < a.R2 ? e + a.R2 : e - a.R2)];
+                const float other = exchange[base + (a.interleaved ? e ^ 1 : e < a.R2 ? e + a.R2 : e - a.R2)];
                 x[i] = fmaf(x[i], c[i], other * s[i]);
             }
         }
@@ -379,7 +382,7 @@ __global__ __launch_bounds__(1024) void rotary_dw_kernel(RotaryArgs a, int block
 }
 
 int pairs_of(const RotaryArgs& a, int dtype) {
-    return a.interleaved ? PAIRS_INTER : a.R2 % (dtype == DT_BF16 ? 8 : 4) == 0 ? PAIRS_HALF : PAIRS_FAR;
+    return a.R2 % (dtype == DT_BF16 ? 8 : 4) != 0 ? PAIRS_FAR : a.interleaved ? PAIRS_INTER : PAIRS_HALF;
 }
 
 }  // namespace

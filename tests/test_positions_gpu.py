@@ -187,6 +187,33 @@ def test_what_is_not_finite_stays_in_its_row(dtype, D, rot, interleaved):
     assert torch.equal(pamm.rotary(x, f, positions=pos, interleaved=interleaved), x)
 
 
+@BOTH
+@KINDS
+@pytest.mark.parametrize("D,rot", [(48, 32), (64, 30), (16, 2), (128, 64), (40, 8)])
+def test_elements_that_are_not_rotated_stand_alone(dtype, interleaved, D, rot):
+    """They are copied one by one: none is reached by another's infinity, and a zero keeps its sign."""
+    say("not rotated", dtype, interleaved, D, rot)
+    f, w = freqs(rot), torch.ones(D, device="cuda", dtype=DT[dtype])
+    x = torch.randn(2, 5, 3, D, device="cuda").to(DT[dtype])
+    bad = x.clone()
+    bad[..., rot + 1], bad[..., D - 1], bad[..., D - 2] = -0.0, float("inf"), -1.0
+    bad[0, 1, :, rot] = float("nan")
+    y, clean = (pamm.rotary(t, f, interleaved=interleaved) for t in (bad, x))
+    assert torch.equal(y[..., :rot], clean[..., :rot])
+    assert torch.equal(y[..., rot:].nan_to_num(7.0, 8.0), bad[..., rot:].nan_to_num(7.0, 8.0))
+    assert torch.signbit(y[..., rot + 1]).all()
+    # a norm's row with one infinity: NaN in its place, zeros elsewhere
+    one = x.clone()
+    one[..., D - 1] = float("inf")
+    y = pamm.qk_norm_rotary(one, x, w, w, f, interleaved=interleaved)[0]
+    assert torch.isnan(y[..., D - 1]).all() and not y[..., :D - 1].any()
+    # a gradient that is not finite reaches its own element of the weight's
+    dy = torch.randn_like(x)
+    dy[1, 2, 0, D - 1] = float("inf")
+    dw = pamm.qk_norm_rotary_backward(dy, x, x, x, w, w, f, interleaved=interleaved)[2]
+    assert torch.isfinite(dw[:D - 1]).all() and not torch.isfinite(dw[D - 1])
+
+
 def test_zero_rows_and_eps():
     x, w, f = torch.zeros(1, 4, 2, 32, device="cuda"), torch.ones(32, device="cuda"), freqs(32)
     y, _ = pamm.qk_norm_rotary(x, x, w, w, f)
