@@ -93,6 +93,9 @@ struct TileScales {
     }
 };
 
+// What a tile's scores are multiplied by: never 0, with which a masked score would be a NaN.
+__device__ __forceinline__ float tile_factor(float c, float kscale) { return fmaxf(c * kscale, 0x1p-126f); }
+
 // The values' scales of 64 tiles as many rows take them.  What is summed is in units of the
 // largest of these scales, `unit`, which changes with the 64 tiles, and a tile's scale is
 // unit * 2^exponent * power.  The exponent is added to its probabilities' (one addition a tile
@@ -302,7 +305,7 @@ __device__ __forceinline__ void attention8_rows(const AttnArgs& a, const Cache8A
         if (fits && key0 < wr.end && key0 + 32 > wr.begin) {
             const bool part = key0 < wr.all_lo || key0 + 32 > wr.all_hi;
             f32x16 s = scores(lds[cur][0], key0, part);
-            const float f = c * ks.at(t - base);
+            const float f = tile_factor(c, ks.at(t - base));
             const int tb = opaque(trans_base<DT, ND>());
             if constexpr (DT == DT_BF16) {
                 softmax_update8<ND>(s, f, ve.exponent.at(t - base), ve.inverse.at(t - base), st, acc);
@@ -357,7 +360,7 @@ __device__ __forceinline__ void attention8_rows(const AttnArgs& a, const Cache8A
         if (key0 >= wr.end || key0 + 32 <= wr.begin) continue;
         const bool part = key0 < wr.all_lo || key0 + 32 > wr.all_hi;
         f32x16 s = scores(lds[0][0], key0, part);
-        softmax_update<ND>(s, c * ks.at(t - base), st, acc);
+        softmax_update<ND>(s, tile_factor(c, ks.at(t - base)), st, acc);
         const float vscale = DT == DT_BF16 ? __builtin_amdgcn_exp2f(ve.exponent.at(t - base)) : vs.at(t - base);
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[i] *= vscale;
@@ -460,7 +463,7 @@ __device__ __forceinline__ void attention8_few(const AttnArgs& a, const Cache8Ar
     auto consume = [&](f32x16& s, int key0, float ks, float vs) {
         const bool part = key0 < br.all_lo || key0 + 32 > br.all_hi;
         if (part) mask_block(s, key0, mine);
-        softmax_update<ND>(s, c * ks, st, acc);
+        softmax_update<ND>(s, tile_factor(c, ks), st, acc);
         Packed<DT> p;
         f32x16 rest;
 #pragma unroll
@@ -761,7 +764,7 @@ __device__ __forceinline__ void attention8_one(const AttnArgs& a, const Cache8Ar
                     const uint32_t k = (uint32_t)(key0 + 16 * kb + 4 * quarter + i - mine.lo);
                     if (k >= (uint32_t)(mine.hi - mine.lo)) s[kb][i] = -INFINITY;
                 }
-        const float f = c * kscale;
+        const float f = tile_factor(c, kscale);
         float top = s[0][0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i >> 2][i & 3]);

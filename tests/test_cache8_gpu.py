@@ -390,6 +390,28 @@ def test_scales_far_apart(dtype, Sq, H, Hkv, window):
         close("lse", lse, ref["lse"], ref["lse_tol"])
 
 
+@BOTH
+@pytest.mark.parametrize("Sq", [1, 8, 12, 130])
+@pytest.mark.parametrize("scale", [0.0, 1e-12, None])
+def test_blocks_of_zeros(dtype, Sq, scale):
+    """Their scale is the least one, whose product with a small factor of the scores leaves fp32's range: masked
+    scores stay masked, the others 0."""
+    say("zeros", dtype, Sq, scale)
+    L = 140
+    c, _, _, n = build(1, L, 1, 32, 64, dtype, [L], [L])
+    c.k[:, 64:128] = 0
+    c.k_scale[:, 1] = 2.0 ** -126
+    k, v = meant(c, [L], L)
+    q = values(np.random.default_rng(1), (1, Sq, 2, 32), dtype)
+    kw = dict(causal=True, window=30)
+    if scale is not None:
+        kw["scale"] = scale
+    ref = bo.attention(q, k, v, dtype=dtype, kv_len=[L], **kw)
+    o, lse = pamm.attention_fp8(dev(q, dtype), c, n, **kw)
+    close("o", o, ref["o"], ref["o_tol"] + 4 * bo.U * np.abs(v).max())
+    close("lse", lse, ref["lse"], ref["lse_tol"])
+
+
 def test_far_rows():
     """Byte offsets past 2^32: two sequences of 8-bit rows more than that apart, and a long one."""
     big = torch.empty((1 << 32) + (1 << 20), dtype=torch.uint8, device="cuda")
