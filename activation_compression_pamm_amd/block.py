@@ -307,6 +307,8 @@ class PammAttentionBlock(torch.nn.Module):
         return self._inv_freq
 
     def forward(self, x, residual=None, lengths=None, positions=None):
+        if positions is not None and not self.rotary_dim:
+            raise ValueError("PammAttentionBlock: positions are given, but the block has no rotary positions")
         y, h = self.norm(x, residual)
         qkv = self._heads(self.qkv(y))
         if self.rotary_dim or self.q_norm is not None:
@@ -314,8 +316,6 @@ class PammAttentionBlock(torch.nn.Module):
                                                   self.heads, self.heads_kv, True, self.window, None, lengths,
                                                   self.interleaved, self.magnitude, self.norm.eps)
         else:
-            if positions is not None:
-                raise ValueError("PammAttentionBlock: positions are given, but the block has no rotary positions")
             o = PackedAttentionFunction.apply(qkv, self.heads, self.heads_kv, True, self.window, None, lengths)
         return self.out(o.reshape(*x.shape[:2], -1)), h
 

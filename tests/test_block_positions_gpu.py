@@ -137,6 +137,12 @@ def test_refusals():
         cache.append(torch.ones(2, 1, 1, 16, device="cuda"), torch.ones(2, 1, 1, 16, device="cuda"))
 
 
+def test_positions_without_a_rotation_are_refused():
+    block = PammAttentionBlock(64, 2, qk_norm=True, device="cuda")
+    with pytest.raises(ValueError, match="positions"):
+        block(torch.zeros(1, 3, 64, device="cuda"), positions=torch.arange(3, device="cuda"))
+
+
 def test_second_derivatives_are_refused():
     block = PammAttentionBlock(64, 2, rotary=True, qk_norm=True, device="cuda")
     x = torch.randn(1, 4, 64, device="cuda", requires_grad=True)
