@@ -200,7 +200,11 @@ def attention_fp8(q, cache: CacheFP8, kv_len, *, causal: bool = False, window: i
                   lse=None, workspace=None, stream=None):
     """``attention`` of q [B x Sq x H x D] over a cache in 8 bits, with kv_len [B]
     int32 tokens in each sequence (None: the cache's rows are all valid; those
-    of a last, partial block are the tail's).  Masks, heads, results (o, lse)
+    of a last, partial block are the tail's).  These have to be the cache's own
+    lengths: the tail holds the tokens behind its last whole block, so a length may
+    be lowered (to take the last tokens back) as far as the end of that
+    block, but a prefix that ends before it cannot be looked at.  Scales have to be
+    positive, normal numbers, as cache_append_fp8 writes them.  Masks, heads, results (o, lse)
     and splitting over the device are those of ``attention``.
 
     Products of the 8-bit values are exact, their scales are applied in 32

@@ -3,7 +3,13 @@
 //
 //   scale = max |x| / 448 over a block of tokens of one head, value = e4m3(x / scale)
 //
-// Bound by memory: one workgroup holds a block of one head, keys and values, in
+// Bound by memory and by the vector unit (maxima, quotients with their
+// remainders): ragged prompts of 4 x 2048 tokens, 32 heads of 128, blocks of 32,
+// bf16, 33 us, 4.2 TB/s with vector issue in 81% of the cycles; a look at each
+// element for what is not finite made it 37, and keys and values in
+// workgroups of their own 41 of those.  One token of 64 sequences, 8 heads of 128: 4 us.
+//
+// One workgroup holds a block of one head, keys and values, in
 // registers through the maximum, so each token is read once and written once.
 // A block is taken when its last token arrives; its first ones may wait in the
 // tail.  The workgroup of the first block that a call touches also writes the

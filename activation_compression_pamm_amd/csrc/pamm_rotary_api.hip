@@ -44,8 +44,9 @@ int rotary_check(const pamm_rotary_t* a) {
     if (!aligned(a->inv_freq, 8) || !aligned(a->positions, a->positions_64 ? 8 : 4) || !aligned(a->offset, 4))
         return PAMM_ERR_ALIGN;
     if (a->positions)
-        for (int64_t s : {a->position_stride_b, a->position_stride_s})
-            if (s < 0 || s > kMaxSpan) return PAMM_ERR_SHAPE;
+        if (a->position_stride_b < 0 || a->position_stride_s < 0 || mul(a->batch - 1, a->position_stride_b) > kMaxSpan ||
+            mul(a->seq - 1, a->position_stride_s) > kMaxSpan)
+            return PAMM_ERR_SHAPE;
     if (int e = both_check(a, a->q, a->k)) return e;
     return both_check(a, a->q_out, a->k_out);
 }

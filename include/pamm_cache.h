@@ -64,7 +64,9 @@ size_t pamm_cache8_attention_workspace_size(const pamm_attention_t *a_host, cons
 /*
  * pamm_attention over the cache: a_host's k and v are not looked at, its seq_k
  * is the cache's room at most (keys past it are not read), kv_len the lengths
- * (NULL: seq_k).  Scores are formed of exact 8-bit values and scaled in 32 bits; bf16:
+ * (NULL: seq_k).  The lengths have to be those of the cache: the tail holds the tokens behind its last whole
+ * block, so a length may be lowered (to take the last tokens back) as far as the end of that block, but a
+ * prefix that ends before it cannot be looked at.  Scores are formed of exact 8-bit values and scaled in 32 bits; bf16:
  * probabilities are multiplied by the values' scale before their one rounding.
  * Scales have to be positive, normal numbers.  What a mask hides does not come through, not even a NaN.
  * Errors as pamm_attention; _SHAPE, _DTYPE where the two do not fit each other.

@@ -205,6 +205,22 @@ def test_any_layout(dtype):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@BOTH
+def test_the_last_tokens_can_be_taken_back(dtype):
+    """Lengths lowered as far as the end of the last whole block, and other tokens appended behind them."""
+    rng = np.random.default_rng(3)
+    first, second = (rounded(tokens(rng, [80, 75], 2, 32, dtype), dtype) for _ in range(2))
+    c, n = filled(2, 160, 2, 32, 64, dtype), lens([0, 0])
+    kv = [dev(np.stack([x[:75] for x in xs]), dtype) for xs in (first, second)]
+    pamm.cache_append_fp8(c, kv[0], kv[1], n)
+    n.copy_(lens([70, 64]))
+    pamm.cache_append_fp8(c, kv[1][:, :70], kv[0][:, :70], n)
+    assert n.tolist() == [140, 134]
+    for name, a, b in (("k", first, second), ("v", second, first)):
+        want = [np.concatenate([a[0][:70], b[0][:70]]), np.concatenate([a[1][:64], b[1][:70]])]
+        holds(c, name, want, dtype)
+
+
 # ------------------------------------------------------------------ attention
 
 def meant(c, lengths, room):
