@@ -9,6 +9,7 @@
 // lie in one block, so that their scales are two numbers a tile.  Keys behind
 // the last whole block come from the tail, in the queries' type.
 #include <algorithm>
+#include <type_traits>
 
 #include "pamm_attention_forward.hpp"
 #include "pamm_cache_kernels.hpp"
@@ -460,7 +461,8 @@ __device__ __forceinline__ void attention8_few(const AttnArgs& a, const Cache8Ar
     Running st{-INFINITY, 0.0f};
     char* vt = shared.lds + wave * VT;
 
-    auto consume = [&](f32x16& s, int key0, float ks, float vs) {
+    // `tail`: the values are not in 8 bits
+    auto consume = [&](f32x16& s, int key0, float ks, float vs, auto tail) {
         const bool part = key0 < br.all_lo || key0 + 32 > br.all_hi;
         if (part) mask_block(s, key0, mine);
         softmax_update<ND>(s, tile_factor(c, ks), st, acc);
@@ -474,7 +476,11 @@ __device__ __forceinline__ void attention8_few(const AttnArgs& a, const Cache8Ar
 #pragma unroll
             for (int i = 0; i < 16; ++i) rest[i] = s[i] - (float)p.v[i >> 3][i & 7];
             p.set(rest);
-            trans_product<DT, ND, true, SAFE>(vt, 0, opaque(trans_base<DT, ND>()), p, part, key0, mine, acc);
+            // 8 bits have no infinities, a tail may; times what may be 0 they would be NaNs
+            if constexpr (decltype(tail)::value)
+                finite_product<DT, ND>(vt, 0, trans_base<DT, ND>(), p, acc);
+            else
+                trans_product<DT, ND, true, SAFE>(vt, 0, opaque(trans_base<DT, ND>()), p, part, key0, mine, acc);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
@@ -531,7 +537,7 @@ __device__ __forceinline__ void attention8_few(const AttnArgs& a, const Cache8Ar
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         fetch(t + 4);
-        consume(s, key0, ks.at(nth), vs.at(nth));
+        consume(s, key0, ks.at(nth), vs.at(nth), std::false_type{});
     }
     for (; t < p1; t += 4) {  // the tail: at most one tile a wave
         const int key0 = first + t * 32, at = key0 - whole;
@@ -557,7 +563,7 @@ __device__ __forceinline__ void attention8_few(const AttnArgs& a, const Cache8Ar
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        consume(s, key0, 1.0f, 1.0f);
+        consume(s, key0, 1.0f, 1.0f, std::true_type{});
     }
 
 #pragma unroll
@@ -787,14 +793,17 @@ __device__ __forceinline__ void attention8_one(const AttnArgs& a, const Cache8Ar
         st.l += sum;
     };
     // acc[db] += 16 columns of the values x p.  Contraction place 8 (l / 16) + i is key
-    // 4 (l / 16) + i, 16 more for i >= 4, for both operands.
-    auto product = [&](int db, const auto& x, const float (&p)[8]) {
+    // 4 (l / 16) + i, 16 more for i >= 4, for both operands.  `tail`: the values are not in 8 bits.
+    auto product = [&](int db, const auto& x, const float (&p)[8], auto tail) {
         if constexpr (DT == DT_BF16) {
             bf16x8 pk, rest;  // what bf16 leaves of the probabilities, too: the matrix unit is idle otherwise
 #pragma unroll
             for (int i = 0; i < 8; ++i) pk[i] = (__bf16)p[i], rest[i] = (__bf16)(p[i] - (float)pk[i]);
             acc[db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, pk, acc[db], 0, 0, 0);
-            acc[db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, rest, acc[db], 0, 0, 0);
+            bf16x8 y = x;  // 8 bits have no infinities, a tail may; times what may be 0 they would be NaNs
+            if constexpr (decltype(tail)::value)
+                y = Columns<DT_BF16, ND>::each(x, [](float e) { return isfinite(e) ? e : 0.0f; });
+            acc[db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y, rest, acc[db], 0, 0, 0);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[db] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], p[i], acc[db], 0, 0, 0);
@@ -840,7 +849,7 @@ __device__ __forceinline__ void attention8_one(const AttnArgs& a, const Cache8Ar
             typedef int i32x2 __attribute__((ext_vector_type(2)));
             typedef __attribute__((address_space(3))) i32x2* lds_i2;
             const i32x2 raw = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i2)(vt + (vat ^ (db << 4))));
-            product(db, widen8<DT>(raw[0], raw[1]), p);
+            product(db, widen8<DT>(raw[0], raw[1]), p, std::false_type{});
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
@@ -882,7 +891,7 @@ __device__ __forceinline__ void attention8_one(const AttnArgs& a, const Cache8Ar
                 const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(vt + (base ^ (db << 5))));
                 const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(vt + 16 * T::PITCH + (base ^ (db << 5))));
                 const s16x8 x = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                product(db, __builtin_bit_cast(bf16x8, x), p);
+                product(db, __builtin_bit_cast(bf16x8, x), p, std::true_type{});
             } else {
                 Eight x;
 #pragma unroll
@@ -890,7 +899,7 @@ __device__ __forceinline__ void attention8_one(const AttnArgs& a, const Cache8Ar
                     const int key = 16 * (i >> 2) + 4 * quarter + (i & 3), e = 16 * db + row;
                     x[i] = *reinterpret_cast<const float*>(vt + T::offset(key, e >> 2) + (e & 3) * 4);
                 }
-                product(db, x, p);
+                product(db, x, p, std::true_type{});
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
