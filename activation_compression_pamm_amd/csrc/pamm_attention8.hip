@@ -41,21 +41,6 @@ __device__ __forceinline__ void widen16(const uint4& r, uint4* out, float power 
     }
 }
 
-// 16 8-bit floats as two vectors of fp16; exact.
-__device__ __forceinline__ void widen16_half(const uint4& r, uint4* out) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t u[4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            u[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[2 * i + j], 1.0f, false));
-            u[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[2 * i + j], 1.0f, true));
-        }
-        out[i] = make_uint4(u[0], u[1], u[2], u[3]);
-    }
-}
-
 // Where 16-byte groups of 8-bit rows (2 ND of them, D / 16 in use) become
 // vectors of the type.
 template <int DT, int ND>
@@ -70,12 +55,6 @@ struct Wide {
         widen16<DT>(raw, v, power);
 #pragma unroll
         for (int i = 0; i < PER; ++i) *reinterpret_cast<uint4*>(tile + T::offset(r, PER * c + i)) = v[i];
-    }
-    __device__ static __forceinline__ void put_half(char* tile, int r, int c, const uint4& raw) {
-        uint4 v[2];
-        widen16_half(raw, v);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(tile + T::offset(r, 2 * c + i)) = v[i];
     }
 };
 
@@ -97,38 +76,24 @@ struct TileScales {
 // What a tile's scores are multiplied by: never 0, with which a masked score would be a NaN.
 __device__ __forceinline__ float tile_factor(float c, float kscale) { return fmaxf(c * kscale, 0x1p-126f); }
 
-// The values' scales of 64 tiles as many rows take them.  What is summed is in units of the
-// largest of these scales, `unit`, which changes with the 64 tiles, and a tile's scale is
-// unit * 2^exponent * power.  The exponent is added to its probabilities' (one addition a tile
-// instead of 16 multiplications, 4% of the time), and `inverse` turns their sum back into one of
-// plain probabilities.
-//
-// Tiles of at least 2^-10 units take their products in fp16, which holds the 8-bit values
-// exactly and the probabilities to 2^-12 instead of bf16's 2^-9 at the same rate; they are at most
-// 2^8.  Smaller ones, which would leave fp16's range, and the tail take them in bf16.  Scales
-// too far from the unit for fp32's probabilities leave `power` of two to the values, exactly.
+// The values' scales of 64 tiles as many rows take them in bf16: 2^k m, with 1 <= m < 2.  2^k goes
+// to the values as they are widened, exactly; the logarithm of m to the exponent of the
+// probabilities (one addition a tile instead of 16 multiplications, 4% of the time), whose sum is
+// turned back by 1 / m.  So bf16 rounds in relation to each probability, however small it
+// is beside the largest (a key that draws nearly all of the weight may have values of 0).
 struct TileExponents {
-    TileScales exponent, inverse, power;
-    float unit;
+    TileScales power, exponent, inverse;
     __device__ __forceinline__ void load(const ScalesArg& s, int b, int h, int block, bool ok) {
-        exponent.load(s, b, h, block, ok);
+        power.load(s, b, h, block, ok);
     }
-    // `eight`: this lane's tile is in 8 bits
-    __device__ __forceinline__ void arrived(bool eight) {
-        exponent.arrived();
-        float top = eight ? exponent.v : 0.0f;
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, shfl_xor(top, m));
-        // the tail's scale is 1, and has to be near as well
-        unit = top == 0.0f ? 1.0f : fminf(fmaxf(top, 0x1p-40f), 0x1p40f);
-        unit = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(unit)));
-        const float v = exponent.v / unit, near = v < 0x1p-40f ? v * 0x1p86f : v > 0x1p40f ? v * 0x1p-80f : v;
-        power.v = v < 0x1p-40f ? 0x1p-86f : v > 0x1p40f ? 0x1p80f : eight && v >= 0x1p-10f && v <= 1.0f ? 0.0f : 1.0f;
-        exponent.v = __builtin_amdgcn_logf(near);
-        inverse.v = __builtin_amdgcn_rcpf(near);
+    __device__ __forceinline__ void arrived() {
+        power.arrived();
+        const uint32_t v = __float_as_uint(power.v);
+        const float m = __uint_as_float((v & 0x7fffffu) | 0x3f800000u);
+        power.v = __uint_as_float(v & 0x7f800000u);
+        exponent.v = __builtin_amdgcn_logf(m);
+        inverse.v = __builtin_amdgcn_rcpf(m);
     }
-    // The values' power of two, or 0: in fp16.
-    __device__ __forceinline__ float power_at(int i) const { return power.at(i); }
 };
 
 // The start of the tail.
@@ -137,10 +102,13 @@ __device__ __forceinline__ int whole_blocks(const Cache8Args& c, int Lk) { retur
 // ---------------------------------------------------------------- many rows
 
 // As attention_rows: four waves of 32 rows share tiles of 32 keys in two LDS
-// buffers, the next tile under way in registers.  2 x 512 queries over 8192 keys, 32/8
-// heads of 128: 164 us and 12 for the join; the same over bf16, whose tiles are not widened, 159 and 12.
-// Widening takes 16 conversions a thread and tile.  One loop with the products in fp16 and in bf16 side by
-// side spills the sums (827 us): tiles that need bf16 have a loop of their own.
+// buffers, the next tile under way in registers.  Widening takes 16 conversions a
+// thread and tile.
+//
+// In bf16 each probability is rounded once, as in attention.  2 x 512 queries over
+// 8192 keys, 32/8 heads of 128: 170 us a call.  Two bf16 parts a probability, as few
+// rows have them: 227 us.  Probabilities in fp16: 178 us, and no bound to what they lose
+// once they are below fp16's range.
 //
 // The softmax of a tile and its probabilities times the values' scale, in the
 // exponent, from which the sum is turned back; otherwise as softmax_update.
@@ -164,22 +132,6 @@ __device__ __forceinline__ void softmax_update8(f32x16& s, float f, float expone
         sum += s[i];
     }
     st.l = fmaf(sum, inverse, st.l);
-}
-
-// acc += (32 rows of fp16 values, transposed) x probabilities, rounded to fp16.
-template <int ND>
-__device__ __forceinline__ void half_product(const char* tile, int base, const f32x16& s, f32x16* acc) {
-    typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-    f16x8 p[2];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) p[i >> 3][i & 7] = (_Float16)s[i];
-    Columns<DT_BF16, ND> c;  // two bytes an element, whatever they hold
-    c.load(tile, 0, base);
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int db = 0; db < ND; ++db)
-            acc[db] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, c.v[t][db]), p[t], acc[db], 0, 0, 0);
 }
 
 template <int DT, int ND>
@@ -234,7 +186,6 @@ __device__ __forceinline__ void attention8_rows(const AttnArgs& a, const Cache8A
     const char* vbase = a.v.p + b * a.v.sb + hk * a.v.sh;
     TileScales ks, vs;     // fp32
     TileExponents ve;      // bf16
-    ve.unit = 1.0f;
     int base = t0;         // the tile of the first lane's scales
     auto scales = [&](int t) {
         const int at = (t + l) * 32;
@@ -245,18 +196,23 @@ __device__ __forceinline__ void attention8_rows(const AttnArgs& a, const Cache8A
             vs.load(c8.vs, b, hk, at >> c8.block_log, at < whole);
         base = t;
     };
-    auto scales_arrived = [&] {  // and what was summed is put into their unit
+    auto scales_arrived = [&] {
         ks.arrived();
-        if constexpr (DT == DT_BF16) {
-            const float before = ve.unit;
-            ve.arrived((base + l) * 32 < whole);
-            const float f = before / ve.unit;
-#pragma unroll
-            for (int db = 0; db < ND; ++db)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[db][i] *= f;
-        } else {
+        if constexpr (DT == DT_BF16)
+            ve.arrived();
+        else
             vs.arrived();
+    };
+    // the softmax of a tile, its probabilities times the values' scale (in bf16 but for the power of two)
+    auto softmax = [&](f32x16& s, int t) {
+        const float f = tile_factor(c, ks.at(t - base));
+        if constexpr (DT == DT_BF16) {
+            softmax_update8<ND>(s, f, ve.exponent.at(t - base), ve.inverse.at(t - base), st, acc);
+        } else {  // whose precision the exponent's rounding would reach
+            softmax_update<ND>(s, f, st, acc);
+            const float vscale = vs.at(t - base);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] *= vscale;
         }
     };
     auto scores = [&](const char* keys, int key0, bool part) {
@@ -269,85 +225,68 @@ __device__ __forceinline__ void attention8_rows(const AttnArgs& a, const Cache8A
         return s;
     };
 
-    // the tiles in 8 bits; in bf16 those that fp16 can take, which are all but for scales very far apart
+    // the tiles in 8 bits
     const int group_row = tid / W::GROUPS, group = tid % W::GROUPS;
     const bool takes = (W::N >= 256 || tid < W::N) && group * 16 < a.D;
     const int kat = takes ? group_row * (int)a.k.ss + group * 16 : kOutside;
     const int vat = takes ? group_row * (int)a.v.ss + group * 16 : kOutside;
     const int te = SAFE ? t0 : whole / 32 < t0 ? t0 : whole / 32 < t1 ? whole / 32 : t1;
-    bool left = SAFE;
     uint4 kr, vr;
     auto fetch = [&](int t) {
         const int key0 = t * 32, some = t < te ? 32 : 0;
         kr = RowView(kbase + key0 * a.k.ss, (int)a.k.ss, some, 32, a.D).load(kat);
         vr = RowView(vbase + key0 * a.v.ss, (int)a.v.ss, some, 32, a.D).load(vat);
     };
-    auto put = [&](int to) {
+    auto put = [&](int to, int t) {
         if (W::N < 256 && tid >= W::N) return;
         W::put(lds[to][0], group_row, group, kr);
-        if constexpr (DT == DT_BF16)
-            W::put_half(lds[to][1], group_row, group, vr);
-        else
-            W::put(lds[to][1], group_row, group, vr);
+        W::put(lds[to][1], group_row, group, vr, DT == DT_BF16 ? ve.power.at(t - base) : 1.0f);
     };
     if (t0 < te) {
         scales(t0);
         fetch(t0);
         scales_arrived();
-        put(0);
+        put(0, t0);
         __syncthreads();
     }
     int cur = 0;
     for (int t = t0; t < te; ++t, cur ^= 1) {
         fetch(t + 1);
         const int key0 = t * 32;
-        const bool fits = DT == DT_F32 || ve.power_at(t - base) == 0.0f;
-        left |= !fits;
-        if (fits && key0 < wr.end && key0 + 32 > wr.begin) {
+        if (key0 < wr.end && key0 + 32 > wr.begin) {
             const bool part = key0 < wr.all_lo || key0 + 32 > wr.all_hi;
             f32x16 s = scores(lds[cur][0], key0, part);
-            const float f = tile_factor(c, ks.at(t - base));
+            softmax(s, t);
             const int tb = opaque(trans_base<DT, ND>());
-            if constexpr (DT == DT_BF16) {
-                softmax_update8<ND>(s, f, ve.exponent.at(t - base), ve.inverse.at(t - base), st, acc);
-                half_product<ND>(lds[cur][1], tb, s, acc);
-            } else {  // whose precision the exponent's rounding would reach
-                softmax_update<ND>(s, f, st, acc);
-                const float vscale = vs.at(t - base);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[i] *= vscale;
-                Packed<DT> p;
-                p.set(s);
-                trans_product<DT, ND, true, false>(lds[cur][1], 0, tb, p, part, key0, mine, acc);
-            }
+            Packed<DT> p;
+            p.set(s);
+            trans_product<DT, ND, true, false>(lds[cur][1], 0, tb, p, part, key0, mine, acc);
         }
         if (t + 1 < te) {
             if (t + 1 - base > 63) {
                 scales(t + 1);
                 scales_arrived();
             }
-            put(cur ^ 1);
+            put(cur ^ 1, t + 1);
         }
         __syncthreads();
     }
 
-    // the tail, and what was left: one tile at a time, bf16 products in bf16
-    for (int t = left ? t0 : te, first = 1; t < t1; ++t, first = 0) {
+    // the tail, with SAFE all of it: one tile at a time
+    for (int t = te, first = 1; t < t1; ++t, first = 0) {
         const int in = (t - t0) & 63, key0 = t * 32;
         if (first || in == 0) {
             scales(t - in);
             scales_arrived();
         }
-        const bool eight = key0 < whole;
-        const float power = DT == DT_BF16 ? ve.power_at(t - base) : 1.0f;
-        if (!SAFE && eight && (DT == DT_F32 || power == 0.0f)) continue;
+        const bool eight = SAFE && key0 < whole;
         __syncthreads();
         if (eight) {
             if (W::N >= 256 || tid < W::N) {
                 const uint4 k = RowView(kbase + key0 * a.k.ss, (int)a.k.ss, 32, 32, a.D).load(kat);
                 const uint4 v = RowView(vbase + key0 * a.v.ss, (int)a.v.ss, 32, 32, a.D).load(vat);
                 W::put(lds[0][0], group_row, group, k);
-                W::put(lds[0][1], group_row, group, v, power == 0.0f ? 1.0f : power);
+                W::put(lds[0][1], group_row, group, v, DT == DT_BF16 ? ve.power.at(t - base) : 1.0f);
             }
         } else {
             const int at = key0 - whole;
@@ -361,10 +300,7 @@ __device__ __forceinline__ void attention8_rows(const AttnArgs& a, const Cache8A
         if (key0 >= wr.end || key0 + 32 <= wr.begin) continue;
         const bool part = key0 < wr.all_lo || key0 + 32 > wr.all_hi;
         f32x16 s = scores(lds[0][0], key0, part);
-        softmax_update<ND>(s, tile_factor(c, ks.at(t - base)), st, acc);
-        const float vscale = DT == DT_BF16 ? __builtin_amdgcn_exp2f(ve.exponent.at(t - base)) : vs.at(t - base);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] *= vscale;
+        softmax(s, t);
         Packed<DT> p;
         p.set(s);
         trans_product<DT, ND, true, SAFE>(lds[0][1], 0, opaque(trans_base<DT, ND>()), p, part, key0, mine, acc);
@@ -375,7 +311,7 @@ __device__ __forceinline__ void attention8_rows(const AttnArgs& a, const Cache8A
     const bool marked = !SAFE && a.hides && !sums_finite<ND>(acc);
     if (!live) return;
     const float sum = half_sum(st.l);
-    const float inv = sum == 0.0f ? 0.0f : (DT == DT_BF16 ? ve.unit : 1.0f) / sum;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     float lse2 = sum == 0.0f ? -INFINITY : st.m + __builtin_amdgcn_logf(sum);
     if (marked) lse2 = NAN;
     const int64_t at = ((int64_t)b * a.H + head) * a.Sq + pos;
