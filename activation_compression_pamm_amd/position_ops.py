@@ -227,14 +227,14 @@ def qk_norm_rotary(q, k, q_weight, k_weight, inv_freq, *, positions=None, offset
 
 def qk_norm_rotary_backward_workspace_size(q, k) -> int:
     """Bytes of workspace ``qk_norm_rotary_backward`` needs for tensors of these
-    shapes (the most over all numbers of rotated pairs)."""
+    shapes (the most over both layouts and all numbers of rotated pairs)."""
     where = "qk_norm_rotary_backward_workspace_size"
     _heads_tensor(where, "q", q)
     kh = _heads_tensor(where, "k", k)
     B, S, H, D = q.shape
-    pack = lambda rot: _pack_rotary(_code(where, q), 0, 0, 0, B, S, H, k.shape[2], D, rot, 1.0, 0.0, 0, 0, 0, 0, 0, 0, 0,
-                                    *kh, *kh, *kh, *kh)
-    return max(int(_lib().pamm_rotary_backward_workspace_size(pack(r))) for r in range(0, D + 1, 2))
+    pack = lambda inter, rot: _pack_rotary(_code(where, q), inter, 0, 0, B, S, H, k.shape[2], D, rot, 1.0, 0.0, 0, 0, 0, 0,
+                                           0, 0, 0, *kh, *kh, *kh, *kh)
+    return max(int(_lib().pamm_rotary_backward_workspace_size(pack(i, r))) for i in (0, 1) for r in range(0, D + 1, 2))
 
 
 def qk_norm_rotary_backward(dq, dk, q, k, q_weight, k_weight, inv_freq, *, positions=None, offset=None,
