@@ -199,15 +199,35 @@ class AddRMSNorm(torch.nn.Module):
         return f"{self.weight.shape[0]}, eps={self.eps}"
 
 
-class KVCache:
-    """Keys and values [B x room x Hkv x D] of the tokens so far, lengths [B]
-    int32 on the GPU."""
+class _Lengths:
+    """Of a cache: lengths [B] int32 on the GPU, and used, the longest of them,
+    on the host.  Replays of a captured call move lengths alone.  So a call
+    attends over the whole room while it is captured, and from then on one
+    that is not captured asks the GPU for used, and waits for it."""
+
+    def _begin(self, batch, device):
+        self.lengths = torch.zeros(batch, device=device, dtype=torch.int32)
+        self.used = 0
+        self._replayed = False
+
+    def _captured(self):
+        """Whether this call is being captured; if not, used is up to date."""
+        if self.lengths.is_cuda and torch.cuda.is_current_stream_capturing():
+            self._replayed = True
+            return True
+        if self._replayed:
+            self.used = max(self.lengths.tolist(), default=0)
+        return False
+
+
+class KVCache(_Lengths):
+    """Keys and values [B x room x Hkv x D] of the tokens so far.  A captured
+    call must not be replayed past the room."""
 
     def __init__(self, batch, room, heads_kv, head_dim, *, device="cuda", dtype=torch.bfloat16):
         self.k = torch.empty(batch, room, heads_kv, head_dim, device=device, dtype=dtype)
         self.v = torch.empty_like(self.k)
-        self.lengths = torch.zeros(batch, device=device, dtype=torch.int32)
-        self.used = 0  # the longest sequence, known on the host
+        self._begin(batch, device)
 
     def append(self, k, v):
         """k, v [B x n x Hkv x D] behind each sequence's tokens."""
@@ -217,7 +237,7 @@ class KVCache:
                              f"{tuple(k.shape)} and {tuple(v.shape)}")
         if k.dtype != self.k.dtype or v.dtype != self.v.dtype:
             raise TypeError(f"KVCache: k and v must be {self.k.dtype}, got {k.dtype} and {v.dtype}")
-        n = k.shape[1]
+        n, captured = k.shape[1], self._captured()
         if self.used + n > room:
             raise ValueError(f"KVCache: {self.used} + {n} tokens do not fit {room}")
         at = self.lengths[:, None].long() + torch.arange(n, device=k.device)
@@ -225,37 +245,39 @@ class KVCache:
         self.k[rows, at] = k
         self.v[rows, at] = v
         self.lengths += n
-        self.used += n
+        if not captured:
+            self.used += n
 
     def attend(self, q, window=0):
         """Causal attention of the newest tokens' queries [B x n x H x D]."""
-        return attention(q, self.k[:, :self.used], self.v[:, :self.used], causal=True, window=window,
-                         kv_len=self.lengths)[0]
+        rows = self.k.shape[1] if self._captured() else self.used
+        return attention(q, self.k[:, :rows], self.v[:, :rows], causal=True, window=window, kv_len=self.lengths)[0]
 
 
-class KVCache8:
+class KVCache8(_Lengths):
     """KVCache in 8 bits, with a scale for each block of tokens and head: half
     of bf16's memory, and of what a new token's attention has to read.  Tokens
-    of the last, partial block stay in dtype until it is whole."""
+    of the last, partial block stay in dtype until it is whole.  Tokens that
+    replays of a captured call bring past the room are dropped."""
 
     def __init__(self, batch, room, heads_kv, head_dim, *, block=64, device="cuda", dtype=torch.bfloat16):
         self.tensors = CacheFP8.empty(batch, room, heads_kv, head_dim, block=block, device=device, dtype=dtype)
-        self.lengths = torch.zeros(batch, device=device, dtype=torch.int32)
-        self.used = 0  # the longest sequence, known on the host
+        self._begin(batch, device)
 
     def append(self, k, v):
         """k, v [B x n x Hkv x D] behind each sequence's tokens."""
-        room = self.tensors.k.shape[1]
+        room, captured = self.tensors.k.shape[1], self._captured()
         if k.dim() == 4 and self.used + k.shape[1] > room:
             raise ValueError(f"KVCache8: {self.used} + {k.shape[1]} tokens do not fit {room}")
         cache_append_fp8(self.tensors, k, v, self.lengths)
-        self.used += k.shape[1]
+        if not captured:
+            self.used += k.shape[1]
 
     def attend(self, q, window=0):
         """Causal attention of the newest tokens' queries [B x n x H x D]."""
         c = self.tensors
-        return attention_fp8(q, c._replace(k=c.k[:, :self.used], v=c.v[:, :self.used]), self.lengths, causal=True,
-                             window=window)[0]
+        rows = c.k.shape[1] if self._captured() else self.used
+        return attention_fp8(q, c._replace(k=c.k[:, :rows], v=c.v[:, :rows]), self.lengths, causal=True, window=window)[0]
 
 
 class PammAttentionBlock(torch.nn.Module):
