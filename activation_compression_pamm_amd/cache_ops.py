@@ -50,7 +50,8 @@ class CacheFP8(NamedTuple):
     scales [B x room // block x Hkv] in fp32, and the tails [B x block x Hkv x D]
     in the type of the queries, where the tokens of each sequence's last,
     partial block wait; block (32, 64 or 128) is the tails' length.  Token j
-    stands for k[b, j, h] * k_scale[b, j // block, h]."""
+    stands for k[b, j, h] * k_scale[b, j // block, h]; k is the nearest to
+    448 x / max|x|, k_scale is max|x| / 448, over a block of one head."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: torch.Tensor
@@ -139,8 +140,8 @@ def cache_append_fp8(cache: CacheFP8, k, v, lengths, *, new_len=None, advance: b
     outer dimensions) behind the lengths[b] tokens of each sequence ([B] int32):
     all n of them, or the first new_len[b] ([B] int32).
 
-    Blocks that become whole are put into 8 bits, with a scale of the largest
-    |x| / 448 in the block; the tokens behind them wait in the tail as they
+    Blocks that become whole are put into 8 bits, 448 x / max|x| over the block,
+    with a scale of max|x| / 448; the tokens behind them wait in the tail as they
     are.  What the cache holds is thus the same whatever chunks its tokens came in.
     What is not finite becomes NaN in 8 bits and does not count for the scale.
     lengths becomes the new lengths (with advance; else it is left).  Tokens
@@ -208,7 +209,9 @@ def attention_fp8(q, cache: CacheFP8, kv_len, *, causal: bool = False, window: i
     and splitting over the device are those of ``attention``.
 
     Products of the 8-bit values are exact, their scales are applied in 32
-    bits; in bf16 each probability times the values' scale is rounded once.
+    bits; in bf16 each probability times the values' scale is rounded once, to
+    bf16, or to two bf16 parts where up to 32 query rows (Sq x H / Hkv) share a
+    key/value head.
     cache.k and cache.v may be sliced to the rows in use.  For serving: there
     is no backward pass.  o and lse, where given, must not share memory with
     the inputs."""

@@ -533,9 +533,9 @@ __global__ __launch_bounds__(256, 1) void attention8_few_again_kernel(AttnArgs a
 // 32 x 32 ones.
 //
 // Bound by reading the cache.  64 sequences of 64 to 8192 keys, 8 heads of 128, 0.56
-// GB: 98 us with the join (5.7 TB/s); all of 8192, 1.07 GB: 162 us whole (6.6 TB/s).  Both
-// with three waves a SIMD; four spill, and a reload in the loop waits for all loads (124 and
-// 205 us).  Without the hint that lines are read once the loads alone take 16% more
+// GB: 101 us a call, the join included (5.5 TB/s); all of 8192, 1.07 GB: 160 us in one part (6.7
+// TB/s), in fp32 (ragged) 209.  bf16 with three waves a SIMD; four spill, and a reload in the loop waits for
+// all loads (124 and 205 us).  Without the hint that lines are read once the loads alone take 16% more
 // (193 us for 167).  With the 32 x 32 products and two waves a SIMD 125 us.
 //
 // A lane holds row (A) or column (B) l % 16 of a product and the 16-byte vector
@@ -911,13 +911,13 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 3 : 2) void attention8_one_ker
     attention8_one<DT, ND>(a, c, blockIdx.x, shared);
 }
 
-// Few rows: two workgroups a unit, and parts of at least 1024 keys.  A second launch and the
-// parts' memory cost a call 7 us (1 x 1024 keys, 12 heads of 64: 16.9 us whole, 22 to 24 in
-// parts; 8192, 8 heads of 128: 63 whole, 27 in 4, 25 in 8).  Where lengths are given, which
-// then differ as a rule, eight a unit even them out, as long as parts have 2048 keys (64
-// sequences of up to 8192, 8 heads of 128: 104 us whole, 100 and 98 in 2 and 4, 105 in 8; of
-// up to 2048: 30 whole, 37 in 2; where all have 8192 after all: 162 whole, 178 and 172 in 2 and 4).
-// Many rows are cut as over a cache that is not in 8 bits.
+// Few rows: two workgroups a unit, in at most a part for each 1024 keys begun (of the room,
+// whatever a window shows of it).  A second launch and the parts' memory cost a call 7 us
+// (1 x 1024 keys, 12 heads of 64: 16.9 us whole, 22 to 24 in parts; 8192, 8 heads of 128: 63
+// whole, 27 in 4, 25 in 8).  Where lengths are given, which then differ as a rule, eight a unit
+// even them out, as long as parts have 2048 keys (64 sequences of up to 8192, 8 heads of 128: 104
+// us whole, 100 and 98 in 2 and 4, 105 in 8; of up to 2048: 30 whole, 37 in 2; where all have 8192
+// after all: 160 whole, 170 in 4).  Many rows are cut as over a cache that is not in 8 bits.
 int attention8_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, bool lengths, int num_cus) {
     if (Sq * G > kFewRows) return attention_splits(B, Sq, Sk, Hkv, G, lengths, num_cus);
     const int64_t blocks = B * Hkv, units = num_cus;

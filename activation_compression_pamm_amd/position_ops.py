@@ -175,10 +175,13 @@ def rotary(x, inv_freq, *, positions=None, offset=None, interleaved: bool = Fals
     Pair j is the elements j and j + len(inv_freq), with interleaved 2 j and
     2 j + 1.  The position of token s of sequence b is positions[b, s] (int64 or
     int32, [B x S] or [S]; s by default) + offset[b] ([B] int32, for instance a
-    cache's lengths).  Angles are formed in 64 bits and are right at any
-    position.  Cosines and sines are multiplied by magnitude.
+    cache's lengths).  Angles are formed in 64 bits: cosines and sines are within
+    4 * 2^-24 + |position * inv_freq| * 2^-51, which at 2^31 radians is another
+    2^-20 (from 2^53 on positions themselves are rounded).  They are
+    multiplied by magnitude.
 
-    inverse turns back: rotary(dy, ..., inverse=True) is the gradient of x.
+    inverse turns by the negative angles: rotary(dy, ..., inverse=True) is the
+    gradient of x and, with a magnitude of 1, takes x's rotation back.
     Queries and keys that lie side by side in a projection's packed output are
     one call.  out may be x itself, and must not share memory with it in any
     other way.  bf16 or fp32, D as for ``attention``; any strides of the outer

@@ -25,8 +25,12 @@ typedef struct {
  * largest 448), whole blocks at a time: token j of head h as
  *
  *   value = k[b, j, h] * k_scale[b, j / block, h],
- *   scale = max |x| / 448 over the block's finite elements, at least 2^-126,
- *   k     = x / scale rounded to nearest even; NaN where x is not finite.
+ *   most  = max |x| over the block's finite elements, at least 448 * 2^-126,
+ *   scale = most / 448 rounded to 32 bits,
+ *   k     = 448 x / most rounded to nearest even; NaN where x is not finite.
+ *
+ * k is a rounding of that quotient, not of x over the rounded scale, which may lie on the other side of a tie.  For
+ * bf16 it is the nearest, ties to even; for fp32, where the quotient is within 4 * 2^-24 of it of a tie, either neighbour.
  *
  * The others, fewer than a block, wait in their own type in row j % block of
  * the tail.  So what a cache holds depends on its tokens alone, not on the calls
@@ -67,7 +71,8 @@ size_t pamm_cache8_attention_workspace_size(const pamm_attention_t *a_host, cons
  * (NULL: seq_k).  The lengths have to be those of the cache: the tail holds the tokens behind its last whole
  * block, so a length may be lowered (to take the last tokens back) as far as the end of that block, but a
  * prefix that ends before it cannot be looked at.  Scores are formed of exact 8-bit values and scaled in 32 bits; bf16:
- * probabilities are multiplied by the values' scale before their one rounding.
+ * each probability times the values' scale is rounded once, to bf16 (where up to 32 query rows share a key/value
+ * head, to two bf16 parts).
  * Scales have to be positive, normal numbers.  What a mask hides does not come through, not even a NaN.
  * Errors as pamm_attention; _SHAPE, _DTYPE where the two do not fit each other.
  */
