@@ -221,8 +221,8 @@ class _Lengths:
 
 
 class KVCache(_Lengths):
-    """Keys and values [B x room x Hkv x D] of the tokens so far.  A captured
-    call must not be replayed past the room."""
+    """Keys and values [B x room x Hkv x D] of the tokens so far.  Tokens that
+    replays of a captured call bring past the room are dropped."""
 
     def __init__(self, batch, room, heads_kv, head_dim, *, device="cuda", dtype=torch.bfloat16):
         self.k = torch.empty(batch, room, heads_kv, head_dim, device=device, dtype=dtype)
@@ -240,12 +240,21 @@ class KVCache(_Lengths):
         n, captured = k.shape[1], self._captured()
         if self.used + n > room:
             raise ValueError(f"KVCache: {self.used} + {n} tokens do not fit {room}")
-        at = self.lengths[:, None].long() + torch.arange(n, device=k.device)
-        rows = torch.arange(batch, device=k.device)[:, None]
+        if n == 0:
+            return
+        new, rows = torch.arange(n, device=k.device), torch.arange(batch, device=k.device)[:, None]
+        at = self.lengths[:, None].long() + new
+        if captured:  # replays know of no limit: what does not fit repeats the last write that does, or changes nothing
+            last = (room - 1 - self.lengths[:, None].long()).clamp(min=0)
+            at, new = at.clamp(max=room - 1), torch.minimum(new, last)
+            full = (self.lengths >= room)[:, None, None, None]
+            k, v = (torch.where(full, old[rows, at], x[rows, new]) for old, x in ((self.k, k), (self.v, v)))
         self.k[rows, at] = k
         self.v[rows, at] = v
-        self.lengths += n
-        if not captured:
+        if captured:
+            self.lengths.add_(n).clamp_(max=room)
+        else:
+            self.lengths += n
             self.used += n
 
     def attend(self, q, window=0):
