@@ -106,9 +106,9 @@ __device__ __forceinline__ int whole_blocks(const Cache8Args& c, int Lk) { retur
 // thread and tile.
 //
 // In bf16 each probability is rounded once, as in attention.  2 x 512 queries over
-// 8192 keys, 32/8 heads of 128: 170 us a call.  Two bf16 parts a probability, as few
-// rows have them: 227 us.  Probabilities in fp16: 178 us, and no bound to what they lose
-// once they are below fp16's range.
+// 8192 keys, 32/8 heads of 128: 165 to 170 us a call, box to box.  Beside 170: two bf16
+// parts a probability, as few rows have them, 227; probabilities in fp16 178, and no bound
+// to what they lose once they are below fp16's range.
 //
 // The softmax of a tile and its probabilities times the values' scale, in the
 // exponent, from which the sum is turned back; otherwise as softmax_update.
@@ -915,8 +915,8 @@ __global__ __launch_bounds__(256, DT == DT_BF16 ? 3 : 2) void attention8_one_ker
 // whatever a window shows of it).  A second launch and the parts' memory cost a call 7 us
 // (1 x 1024 keys, 12 heads of 64: 16.9 us whole, 22 to 24 in parts; 8192, 8 heads of 128: 63
 // whole, 27 in 4, 25 in 8).  Where lengths are given, which then differ as a rule, eight a unit
-// even them out, as long as parts have 2048 keys (64 sequences of up to 8192, 8 heads of 128: 104
-// us whole, 100 and 98 in 2 and 4, 105 in 8; of up to 2048: 30 whole, 37 in 2; where all have 8192
+// even them out, as long as parts have 2048 keys (64 sequences of up to 8192, 8 heads of 128, side by
+// side: 104 us whole, 100 and 98 in 2 and 4, 105 in 8; of up to 2048: 30 whole, 37 in 2; where all have 8192
 // after all: 160 whole, 170 in 4).  Many rows are cut as over a cache that is not in 8 bits.
 int attention8_splits(int64_t B, int64_t Sq, int64_t Sk, int64_t Hkv, int64_t G, bool lengths, int num_cus) {
     if (Sq * G > kFewRows) return attention_splits(B, Sq, Sk, Hkv, G, lengths, num_cus);
